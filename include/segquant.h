@@ -508,6 +508,233 @@ SQ_API sq_status sq_dualscale_seglinear_host_noalloc(const void *x_host, int64_t
                                                      const sq_segments *seg,
                                                      sq_stream_t stream);
 
+/* ======================================================================== *
+ * Around the quantized linear: low-rank adapters beside the shared, frozen
+ * projection; rotary positions on its q|k output columns; the channels-last
+ * group norm that makes its input; and its input gradient, through which
+ * adapters below it are trained.  (The pages describe the quantized linear
+ * only; these operators are defined by their formulas below.)  The conventions
+ * of this header hold: caller-owned buffers, host-side validation before
+ * anything is launched, asynchronous on `stream`; no call keeps state.
+ * A workspace belongs to the calls of one stream at a time.
+ * ======================================================================== */
+
+/*
+ * sq_lora_plan -- the row order of a batch by adapter, for the calls below.
+ * `adapter` names each row's adapter, 0 .. n_adapters - 1; any other value
+ * (-1 by convention) means none.  Rows may come in any order and an adapter
+ * may return in several places.  The plan depends on `adapter` only: one plan
+ * serves every adapted layer that the batch goes through, forward and backward.
+ *   adapter     int32 [M] device, 4-byte aligned; 0 <= M <= 2^24
+ *   n_adapters  L, 1..1024
+ *   plan        int32 device output of sq_lora_plan_bytes(M, L) bytes, 16-byte
+ *               aligned
+ * M == 0 gives a valid plan of no rows.  A plan passed with another M or L than
+ * it was made for is reported as SQ_ERR_INVALID_ARG in the device error word
+ * (sq_get_device_status), and that call writes nothing.
+ * sq_lora_plan_bytes: 0 for sizes out of range.
+ */
+SQ_API size_t sq_lora_plan_bytes(int64_t M, int32_t n_adapters);
+SQ_API sq_status sq_lora_plan(const int32_t *adapter, int64_t M, int32_t n_adapters,
+                              int32_t *plan, sq_stream_t stream);
+
+/*
+ * sq_lora_forward -- adapters of rank R beside a projection, for every row m
+ * with adapter a:   t[m] = A[a] x[m],   y[m] = base[m] + scale[a] B[a] t[m].
+ * Rows without an adapter: y[m] = base[m] (left alone when y is base) and t[m]
+ * is not written.  t is fp32; where y is bf16, t enters the second product
+ * rounded to bf16; where y is fp32, with 24 bits.  Sums are fp32.
+ *   x      bf16 [M][ldx];  A bf16 [L][R][K], B bf16 [L][N][R], scale fp32 [L]
+ *   plan   of sq_lora_plan for this M and L
+ *   base   [M][ldbase] of y's type, or NULL for zeros; y [M][ldy] output.  base
+ *          may be y (with ldbase == ldy: in place); otherwise the buffers must
+ *          not overlap.  y must not overlap x.
+ *   t      fp32 [M][R] output (the backward pass reads it)
+ *   R 8..128, K and N >= 8, all multiples of 8; K, N <= 2^20; leading dimensions
+ *   at least the row's length and multiples of 8; x, A, B, base, y, t, plan
+ *   16-byte aligned, scale 4-byte; M <= 2^24, M * ld <= 2^44.
+ * M == 0 is a valid no-op.  Two kernels.
+ */
+SQ_API sq_status sq_lora_forward(const void *x, int64_t ldx, const void *A, const void *B,
+                                 const float *scale, const int32_t *plan, const void *base,
+                                 int64_t ldbase, void *y, int64_t ldy, sq_out_dtype out_dtype,
+                                 float *t, int64_t M, int64_t N, int64_t K, int32_t R,
+                                 int32_t n_adapters, sq_stream_t stream);
+
+/*
+ * sq_lora_backward -- the gradients of sq_lora_forward from dy = dL/dy:
+ *   dt[m] = scale[a] B[a]^T dy[m]                   (workspace, fp32)
+ *   dB[a] = scale[a] sum_{m of a} dy[m] t[m]^T      dA[a] = sum_{m of a} dt[m] x[m]^T
+ *   dx[m] = dx_base[m] + A[a]^T dt[m]
+ * dA and dB are written whole (zeros for an adapter without rows); rows without
+ * an adapter get dx[m] = dx_base[m].  (dL/dbase is dy itself.)  t and dt enter
+ * the second products rounded to bf16 where the result is bf16, with 24 bits
+ * where it is fp32.  Every sum has a fixed order: the same call gives the same
+ * bits.
+ *   dy       bf16 [M][lddy];  x, A, B, scale, plan as in the forward call
+ *   t        fp32 [M][R] of the forward call
+ *   dx_base  bf16 [M][ldbase] or NULL for zeros; dx bf16 [M][lddx] output, or
+ *            NULL (with dx_base NULL) to skip it; dx_base may be dx
+ *   dA, dB   [L][R][K] and [L][N][R] outputs of grad_dtype, or both NULL
+ *   dt       fp32 [M][R] workspace
+ * Alignment and limits as in the forward call; dA, dB, dt 16-byte aligned.
+ * M == 0 writes zeros to dA and dB.  Up to three kernels.
+ */
+SQ_API sq_status sq_lora_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                  const float *t, const void *A, const void *B,
+                                  const float *scale, const int32_t *plan, const void *dx_base,
+                                  int64_t ldbase, void *dx, int64_t lddx, void *dA, void *dB,
+                                  sq_out_dtype grad_dtype, float *dt, int64_t M, int64_t N,
+                                  int64_t K, int32_t R, int32_t n_adapters, sq_stream_t stream);
+
+/* Which two columns of a head are pair i of `rot` rotated columns. */
+typedef enum {
+  SQ_ROPE_INTERLEAVED = 0, /* 2 i and 2 i + 1     */
+  SQ_ROPE_HALF = 1         /* i and i + rot / 2   */
+} sq_rope_layout;
+
+#define SQ_ROPE_MAX_AXES 4
+
+/*
+ * sq_rope_forward / sq_rope_backward -- rotary positions on the first `rot` of
+ * the D columns of each of H neighbouring heads.  Pair i of row m turns by
+ *   phi = positions[m][axis of i] * inv_freq[i]  (radians; forward +, backward -)
+ *   (u, v) -> factor * (u cos phi - v sin phi, u sin phi + v cos phi)
+ * The backward call maps dL/dout to dL/dx.  Columns rot .. D - 1 of a head are
+ * copied (left alone in place).  One call covers the q and the k columns of a
+ * QKV row, which are neighbours.  The angle is formed and reduced in fp64, so
+ * far positions keep their phase.
+ *   x, out      bf16 or fp32 (dtype) rows [M][ldx], [M][ldo]; out may be x with
+ *               ldo == ldx (in place), otherwise they must not overlap
+ *   positions   int32 [M][n_axes] device, any values
+ *   inv_freq    fp32 [rot / 2] device
+ *   axis_pairs  HOST int32 [n_axes]: pairs that turn with each axis, in order,
+ *               each >= 0, rot / 2 in all; NULL with n_axes == 1
+ *   n_axes 1..SQ_ROPE_MAX_AXES; H >= 1; D a multiple of 8, 8..1024; rot even,
+ *   2..D; ldx, ldo >= H * D, multiples of 8; x, out 16-byte aligned, positions and
+ *   inv_freq 4-byte; factor finite; M <= 2^31 - 1, M * ld <= 2^44, H * D <= 2^20.
+ * M == 0 is a valid no-op.  One kernel.
+ */
+SQ_API sq_status sq_rope_forward(const void *x, int64_t ldx, void *out, int64_t ldo,
+                                 sq_out_dtype dtype, const int32_t *positions,
+                                 const float *inv_freq, const int32_t *axis_pairs,
+                                 int32_t n_axes, float factor, int64_t M, int32_t H, int32_t D,
+                                 int32_t rot, sq_rope_layout layout, sq_stream_t stream);
+SQ_API sq_status sq_rope_backward(const void *dout, int64_t lddo, void *dx, int64_t lddx,
+                                  sq_out_dtype dtype, const int32_t *positions,
+                                  const float *inv_freq, const int32_t *axis_pairs,
+                                  int32_t n_axes, float factor, int64_t M, int32_t H, int32_t D,
+                                  int32_t rot, sq_rope_layout layout, sq_stream_t stream);
+
+/* How frequencies are scaled for contexts longer than the trained one. */
+typedef enum {
+  SQ_ROPE_SCALE_NONE = 0,
+  SQ_ROPE_SCALE_LINEAR = 1, /* positions divided by `scale`                  */
+  SQ_ROPE_SCALE_NTK = 2,    /* base raised so that the slowest pair slows by `scale` */
+  SQ_ROPE_SCALE_YARN = 3    /* linear for slow pairs, none for fast ones, a ramp between */
+} sq_rope_scaling;
+
+/*
+ * sq_rope_frequencies -- inverse frequencies on the HOST, f_i = base^(-2 i / rot)
+ * for i < rot / 2, evaluated in fp64, scaled for long contexts, rounded to fp32:
+ *   LINEAR  f_i / scale  (position interpolation)
+ *   NTK     base' = base * scale^(rot / (rot - 2))  ("NTK-aware"; rot > 2)
+ *   YARN    f_i ((1 - r_i) / scale + r_i), r_i = 1 - clamp((i - lo) / (hi - lo), 0, 1),
+ *           lo = floor(c(beta_fast)), hi = ceil(c(beta_slow)) clamped to
+ *           [0, rot - 1], c(b) = rot ln(orig / (2 pi b)) / (2 ln base), hi - lo taken
+ *           as 0.001 where they are equal; *factor = 0.1 ln(scale) + 1 for scale > 1
+ *           (Peng et al., "YaRN: Efficient Context Window Extension of Large
+ *           Language Models", 2023, section 3)
+ * *factor is 1 for the other kinds; pass it as `factor` of the rotary calls.
+ *   base > 1, scale >= 1, both finite; YARN: original_context >= 1 and
+ *   beta_fast > beta_slow > 0 (32 and 1 by convention); ignored otherwise
+ *   inv_freq HOST fp32 [rot / 2], factor HOST fp32 [1], outputs
+ * Touches no device and launches nothing.
+ */
+SQ_API sq_status sq_rope_frequencies(int32_t rot, double base, sq_rope_scaling kind, double scale,
+                                     double original_context, double beta_fast,
+                                     double beta_slow, float *inv_freq, float *factor);
+
+typedef enum {
+  SQ_ACT_NONE = 0,
+  SQ_ACT_SILU = 1, /* v / (1 + e^-v)                                          */
+  SQ_ACT_GELU = 2  /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))            */
+} sq_activation;
+
+/*
+ * sq_group_norm_forward -- group norm with an activation on channels-last rows,
+ * B samples of S rows (pixels or tokens) of C channels in G groups of C / G
+ * neighbouring channels:
+ *   mean, var (biased) over the S * C/G values of each sample's group,
+ *   rstd = 1 / sqrt(var + eps),
+ *   y = act((x - mean) * rstd * gamma + beta)
+ * Its output rows [B * S][C] are the input rows of a quantized linear.
+ *   x, y         bf16 [B * S][ldx], [B * S][ldy]; y may be x (ldy == ldx)
+ *   gamma, beta  bf16 [C] or NULL (1 and 0)
+ *   mean, rstd   fp32 [B][G] outputs
+ *   workspace    device memory of sq_group_norm_workspace_bytes(B, S, C, G)
+ *                bytes, 16-byte aligned; needs no initial value
+ *   C a multiple of 8, 8..8192; G 1..1024, dividing C; S 1..2^24; B 0..65535;
+ *   ld >= C, multiples of 8; x, y 16-byte aligned, gamma and beta 2-byte, mean
+ *   and rstd 4-byte; B * S * ld <= 2^44; eps >= 0, finite.
+ * B == 0 is a valid no-op.  Two kernels.
+ * sq_group_norm_workspace_bytes: 0 for sizes out of range.
+ */
+SQ_API size_t sq_group_norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G);
+SQ_API sq_status sq_group_norm_forward(const void *x, int64_t ldx, int64_t B, int64_t S,
+                                       int64_t C, int64_t G, const void *gamma,
+                                       const void *beta, float eps, sq_activation act, void *y,
+                                       int64_t ldy, float *mean, float *rstd, void *workspace,
+                                       size_t workspace_bytes, sq_stream_t stream);
+
+/*
+ * sq_group_norm_backward -- its gradients: with dv = dy act'(v), xh = (x - mean)
+ * rstd, h = dv gamma and n = S * C/G,
+ *   dx = rstd (h - (sum h + xh sum h xh) / n)   sums over the sample's group,
+ *   dgamma = sum dv xh,  dbeta = sum dv         sums over samples and rows.
+ *   dy        bf16 [B * S][lddy];  x, gamma, beta, act as in the forward call
+ *   mean, rstd of the forward call
+ *   dx        bf16 [B * S][lddx] output or NULL; dx may be dy (lddx == lddy)
+ *   dgamma, dbeta [C] outputs of grad_dtype, each may be NULL
+ *   workspace as in the forward call
+ * Limits as in the forward call.  B == 0 writes zeros to dgamma and dbeta.
+ * Every sum has a fixed order.  Two kernels.
+ */
+SQ_API sq_status sq_group_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                        int64_t B, int64_t S, int64_t C, int64_t G,
+                                        const void *gamma, const void *beta, const float *mean,
+                                        const float *rstd, sq_activation act, void *dx,
+                                        int64_t lddx, void *dgamma, void *dbeta,
+                                        sq_out_dtype grad_dtype, void *workspace,
+                                        size_t workspace_bytes, sq_stream_t stream);
+
+/*
+ * sq_dualscale_seglinear_input_grad -- the gradient of a frozen quantized layer
+ * with respect to its input, straight through the activation quantizer:
+ *   dx[m][k] = sum_n dy[m][n] W~[n][k],  W~[n][k] = s_w[i(k)][n] W^[n][k] / d[g(n)][k]
+ * with the layer's codes and steps: i(k) the K-segment of channel k, g(n) the
+ * activation group of output n.  W~ is rounded to bf16; products are exact and
+ * sums fp32.
+ *   dy    bf16 [M][lddy];  wq int8 [N][K], s_w fp32 [S][N], d fp32 [G][K] or
+ *         NULL, seg: as in the layer's forward calls (SQ_FLAG_W4: wq of
+ *         sq_unpack_weight_w4; SQ_FLAG_FP8: E4M3 codes; SQ_FLAG_SINGLE_SCALE has no
+ *         effect)
+ *   dx    bf16 [M][lddx] output, must not overlap dy
+ *   workspace  device memory of sq_input_grad_workspace_bytes(N, K) bytes, 256-byte
+ *         aligned (W~, written by every call: layers may share one)
+ *   K % 16 == 0, K >= 16; N >= 1; N, K <= 2^20; lddy >= N and lddx >= K, multiples of 8;
+ *   dy, wq, dx 16-byte aligned, s_w and d 4-byte; M <= 2^24, M * ld <= 2^44.
+ * M == 0 is a valid no-op.  Two kernels.
+ * sq_input_grad_workspace_bytes: 0 for sizes out of range.
+ */
+SQ_API size_t sq_input_grad_workspace_bytes(int64_t N, int64_t K);
+SQ_API sq_status sq_dualscale_seglinear_input_grad(const void *dy, int64_t lddy, const int8_t *wq,
+                                                   const float *s_w, const float *d,
+                                                   const sq_segments *seg, void *dx,
+                                                   int64_t lddx, int64_t M, int64_t N, int64_t K,
+                                                   void *workspace, size_t workspace_bytes,
+                                                   sq_stream_t stream);
+
 /*
  * sq_debug_timeout_probe -- test only: launches one small kernel that waits on
  * a barrier nothing ever signals, with the library's bounded wait and a limit

@@ -1,0 +1,227 @@
+"""Low-rank adapters beside a shared projection (sq_lora_plan, _forward,
+_backward) against the 64-bit formulas, within bounds that count roundings."""
+import pytest
+import torch
+
+from w8a8_gemm_b200 import binding as B
+
+import ops_ref as ref
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _problem(M, K, N, R, L, seed, spread="runs", out=BF):
+    g = _gen(seed)
+
+    def randn(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+
+    x = (randn(M, K) * torch.exp(randn(K))).to(BF)
+    A = (randn(L, R, K) * K ** -0.5).to(BF)
+    Bm = (randn(L, N, R) * 0.2).to(BF)
+    scale = torch.rand(L, generator=g, device="cuda") * 2 - 0.5
+    if spread == "runs":       # ragged neighbouring requests, some without an adapter
+        cuts = torch.sort(torch.randint(0, M + 1, (max(1, min(M, 6)),), generator=g,
+                                        device="cuda")).values
+        req = torch.searchsorted(cuts, torch.arange(M, device="cuda"), right=True)
+        ids = torch.randint(-1, L, (len(cuts) + 1,), generator=g, device="cuda")[req]
+    elif spread == "scattered":  # any row any adapter
+        ids = torch.randint(-1, L, (M,), generator=g, device="cuda")
+    elif spread == "one":
+        ids = torch.full((M,), L - 1, device="cuda")
+    else:                      # no row has one; numbers out of range mean none, too
+        ids = torch.full((M,), -1, device="cuda")
+        ids[::3] = L + 5
+        ids[1::3] = -2 ** 31
+    base = randn(M, N).to(out)
+    dy = randn(M, N).to(BF)
+    return dict(x=x, A=A, B=Bm, scale=scale, ids=ids.to(torch.int32), base=base, dy=dy,
+                dx_base=randn(M, K).to(BF))
+
+
+SIZES = [  # M, K, N, R, L, spread
+    (1, 64, 64, 8, 1, "one"), (1, 1536, 1536, 16, 4, "scattered"), (16, 256, 328, 16, 8, "scattered"),
+    (63, 72, 200, 24, 3, "runs"), (64, 8, 8, 8, 2, "scattered"), (65, 128, 136, 32, 2, "one"),
+    (333, 1000, 520, 48, 5, "runs"), (130, 2056, 264, 64, 3, "scattered"), (257, 512, 384, 128, 2, "runs"),
+    (129, 200, 1160, 96, 7, "scattered"), (1500, 448, 640, 40, 3, "runs"), (77, 64, 128, 16, 40, "scattered"),
+    (100, 64, 72, 8, 3, "none"), (300, 96, 64, 16, 1024, "scattered"), (4100, 256, 256, 64, 1, "one"),
+]
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("M,K,N,R,L,spread", SIZES)
+def test_forward(M, K, N, R, L, spread, out):
+    p = _problem(M, K, N, R, L, seed=M + R, spread=spread, out=out)
+    plan = B.sq_lora_plan(p["ids"], L)
+    t = torch.full((M, R), -7.5, device="cuda")
+    y, t = B.sq_lora_forward(p["x"], p["A"], p["B"], p["scale"], plan, p["base"], t=t)
+    assert y.dtype == out
+    yr, ye, tr, te = ref.lora_forward(p["x"], p["A"], p["B"], p["scale"], p["ids"], p["base"], out)
+    ref.check(y, yr, ye, "y")
+    has = (p["ids"] >= 0) & (p["ids"] < L)
+    ref.check(t[has], tr[has], te[has], "t")
+    assert (t[~has] == -7.5).all()          # rows without an adapter: t left as it was
+    assert torch.equal(y[~has], p["base"][~has])
+    assert B.sq_get_device_status() == B.SQ_OK
+
+
+@pytest.mark.parametrize("grads", [BF, F32])
+@pytest.mark.parametrize("M,K,N,R,L,spread", SIZES)
+def test_backward(M, K, N, R, L, spread, grads):
+    p = _problem(M, K, N, R, L, seed=2 * M + R, spread=spread)
+    plan = B.sq_lora_plan(p["ids"], L)
+    _, _, t, _ = ref.lora_forward(p["x"], p["A"], p["B"], p["scale"], p["ids"], p["base"], BF)
+    t = t.float()
+    has = (p["ids"] >= 0) & (p["ids"] < L)
+    t[~has] = float("nan")                  # never read
+    dA, dB, dx = B.sq_lora_backward(p["dy"], p["x"], t, p["A"], p["B"], p["scale"], plan,
+                                    p["dx_base"], grad_dtype=grads)
+    want = ref.lora_backward(p["dy"], p["x"], t, p["A"], p["B"], p["scale"], p["ids"],
+                             p["dx_base"], grads)
+    assert dA.dtype == dB.dtype == grads
+    for name, got in (("dA", dA), ("dB", dB), ("dx", dx)):
+        ref.check(got, *want[name], name)
+    for a in range(L):                      # an adapter without rows: exact zeros
+        if not (p["ids"] == a).any():
+            assert (dA[a] == 0).all() and (dB[a] == 0).all()
+    assert torch.equal(dx[~has], p["dx_base"][~has])
+
+
+def test_plan_orders_rows_by_adapter_and_keeps_their_order():
+    for M, L, seed in ((0, 3, 1), (1, 1, 2), (1000, 7, 3), (70000, 1024, 4), (33, 1024, 5)):
+        ids = torch.randint(-3, L + 3, (M,), generator=_gen(seed), device="cuda").to(torch.int32)
+        plan = B.sq_lora_plan(ids, L).cpu().tolist()
+        key = torch.where((ids >= 0) & (ids < L), ids, L).cpu()
+        order = torch.sort(key, stable=True).indices.tolist()
+        start = [0]
+        for b in range(L + 1):
+            start.append(start[-1] + int((key == b).sum()))
+        assert plan[1:3] == [M, L]
+        assert plan[4:4 + L + 2] == start
+        assert plan[4 + L + 2:4 + L + 2 + M] == order
+        tiles = [(b, s) for b in range(L + 1) for s in range(start[b], start[b + 1], 64)]
+        at = 4 + L + 2 + M
+        assert plan[3] == len(tiles)
+        assert list(zip(plan[at:at + 2 * len(tiles):2], plan[at + 1:at + 2 * len(tiles):2])) == tiles
+
+
+def test_in_place_strides_and_columns_beyond_are_untouched():
+    """x, base and y as column slices of wider buffers; in place; a NaN in a row
+    without an adapter and in the columns beyond stays where it is."""
+    M, K, N, R, L = 150, 128, 264, 16, 3
+    p = _problem(M, K, N, R, L, seed=9)
+    wide = torch.full((M, K + 24), float("nan"), dtype=BF, device="cuda")
+    wide[:, 8:8 + K] = p["x"]
+    out = torch.full((M, 3 * N), 3.0, dtype=BF, device="cuda")
+    out[:, N:2 * N] = p["base"]
+    none = (p["ids"] < 0).nonzero()[:, 0]
+    assert len(none) > 0
+    wide[none] = float("nan")
+    plan = B.sq_lora_plan(p["ids"], L)
+    view = out[:, N:2 * N]
+    y, t = B.sq_lora_forward(wide[:, 8:8 + K], p["A"], p["B"], p["scale"], plan, view, y=view)
+    yr, ye, _, _ = ref.lora_forward(p["x"], p["A"], p["B"], p["scale"], p["ids"], p["base"], BF)
+    ref.check(out[:, N:2 * N].contiguous(), yr, ye, "y")
+    assert (out[:, :N] == 3.0).all() and (out[:, 2 * N:] == 3.0).all()
+    dy = torch.full((M, N + 8), float("nan"), dtype=BF, device="cuda")
+    dy[:, :N] = p["dy"]
+    dy[none] = float("nan")
+    dxw = torch.full((M, K + 16), 5.0, dtype=BF, device="cuda")
+    dxw[:, :K] = p["dx_base"]
+    tt = torch.nan_to_num(t)
+    want = ref.lora_backward(p["dy"], p["x"], tt, p["A"], p["B"], p["scale"], p["ids"],
+                             p["dx_base"], BF)
+    dA, dB, dx = B.sq_lora_backward(dy[:, :N], wide[:, 8:8 + K], t, p["A"], p["B"], p["scale"],
+                                    plan, dxw[:, :K], dx=dxw[:, :K])
+    ref.check(dA, *want["dA"], "dA")
+    ref.check(dB, *want["dB"], "dB")
+    ref.check(dxw[:, :K].contiguous(), *want["dx"], "dx")
+    assert (dxw[:, K:] == 5.0).all()
+
+
+def test_parts_on_their_own():
+    """No base: zeros; gradients of the weights only, or of the input only."""
+    M, K, N, R, L = 90, 64, 80, 8, 2
+    p = _problem(M, K, N, R, L, seed=3, spread="scattered")
+    plan = B.sq_lora_plan(p["ids"], L)
+    y, t = B.sq_lora_forward(p["x"], p["A"], p["B"], p["scale"], plan, None)
+    yr, ye, _, _ = ref.lora_forward(p["x"], p["A"], p["B"], p["scale"], p["ids"], None, BF)
+    ref.check(y, yr, ye, "y")
+    a = (p["dy"], p["x"], t, p["A"], p["B"], p["scale"], plan)
+    dA, dB, dx = B.sq_lora_backward(*a, None)
+    dA1, dB1, none = B.sq_lora_backward(*a, None, need_dx=False)
+    none2, none3, dx1 = B.sq_lora_backward(*a, None, need_weights=False)
+    assert none is none2 is none3 is None
+    assert torch.equal(dA, dA1) and torch.equal(dB, dB1) and torch.equal(dx, dx1)
+
+
+def test_no_rows():
+    A = torch.zeros(2, 8, 64, dtype=BF, device="cuda")
+    Bm = torch.zeros(2, 72, 8, dtype=BF, device="cuda")
+    s = torch.ones(2, device="cuda")
+    x, dy = torch.empty(0, 64, dtype=BF, device="cuda"), torch.empty(0, 72, dtype=BF, device="cuda")
+    plan = B.sq_lora_plan(torch.empty(0, dtype=torch.int32, device="cuda"), 2)
+    y, t = B.sq_lora_forward(x, A, Bm, s, plan, None)
+    assert y.shape == (0, 72)
+    dA = torch.ones(2, 8, 64, dtype=BF, device="cuda")
+    dA, dB, dx = B.sq_lora_backward(dy, x, t, A, Bm, s, plan, None, dA=dA)
+    assert (dA == 0).all() and (dB == 0).all() and dx.shape == (0, 64)
+
+
+def test_same_bits_every_time_and_from_a_graph():
+    """Fixed orders of all sums: repeated calls, another stream and a replayed
+    graph give the same bits; new inputs in the captured buffers give theirs."""
+    M, K, N, R, L = 700, 640, 896, 32, 2
+    p = _problem(M, K, N, R, L, seed=21)
+    plan = B.sq_lora_plan(p["ids"], L)
+
+    def call():
+        y, t = B.sq_lora_forward(p["x"], p["A"], p["B"], p["scale"], plan, p["base"])
+        return (y, *B.sq_lora_backward(p["dy"], p["x"], t, p["A"], p["B"], p["scale"], plan,
+                                       p["dx_base"]))
+
+    first = call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        second = call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        third = call()
+    graph.replay()
+    torch.cuda.synchronize()
+    for u, v, w in zip(first, second, third):
+        assert torch.equal(u, v) and torch.equal(u, w)
+    p["x"].copy_(p["x"].flip(0))
+    graph.replay()
+    fresh = call()
+    torch.cuda.synchronize()
+    for u, w in zip(fresh, third):
+        assert torch.equal(u, w)
+
+
+def test_plan_of_another_batch_is_reported_and_nothing_written():
+    M, K, N, R, L = 40, 64, 64, 8, 2
+    p = _problem(M, K, N, R, L, seed=4)
+    other = B.sq_lora_plan(torch.zeros(M + 1, dtype=torch.int32, device="cuda"), L)
+    y = torch.full((M, N), 9.0, dtype=BF, device="cuda")
+    # the binding refuses it by its size ...
+    with pytest.raises(ValueError, match="plan"):
+        B.sq_lora_forward(p["x"], p["A"], p["B"], p["scale"], other, p["base"], y=y)
+    # ... and the kernels by what the plan says of itself
+    t = torch.full((M, R), 9.0, device="cuda")
+    rc = B.lib().sq_lora_forward(B._ptr(p["x"]), K, B._ptr(p["A"]), B._ptr(p["B"]),
+                                 B._ptr(p["scale"]), B._ptr(other), B._ptr(p["base"]), N,
+                                 B._ptr(y), N, 0, B._ptr(t), M, N, K, R, L, B._stream())
+    assert rc == B.SQ_OK
+    assert B.sq_get_device_status() == B.SQ_ERR_INVALID_ARG
+    assert (y == 9.0).all() and (t == 9.0).all()
+    assert B.sq_get_device_status() == B.SQ_OK

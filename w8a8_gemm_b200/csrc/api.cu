@@ -19,88 +19,6 @@ constexpr int kMaxDevices = 64;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Current device must be sm_100 (the kernels are built for sm_100a only).
-sq_status check_device() {
-  static int checked[kMaxDevices] = {};  // 0 unknown, 1 ok, -1 unsupported
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-    cudaGetLastError();
-    return SQ_ERR_NO_DEVICE;
-  }
-  if (checked[dev] == 0) {
-    int major = 0, minor = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
-      cudaGetLastError();
-      return SQ_ERR_NO_DEVICE;
-    }
-    checked[dev] = (major == 10 && minor == 0) ? 1 : -1;
-  }
-  return checked[dev] == 1 ? SQ_OK : SQ_ERR_NO_DEVICE;
-}
-
-// Validates a segment table.  extent_n < 0 means N is not known to the call
-// (activation-side calls), in which case the output offsets end is not checked.
-sq_status parse_segments(const sq_segments *seg, int64_t K, int64_t extent_n, SegParams *out) {
-  SegParams p{};
-  if (seg == nullptr) {
-    p.mode = SQ_SEG_NONE;
-    p.n_seg = 1;
-    p.G = 1;
-    p.S = 1;
-    p.P = 2;
-    p.off[0] = 0;
-    p.off[1] = static_cast<int32_t>(K);
-    *out = p;
-    return SQ_OK;
-  }
-  if (seg->mode < SQ_SEG_NONE || seg->mode > SQ_SEG_INPUT) return SQ_ERR_INVALID_ARG;
-  if (seg->n_seg < 1 || seg->n_seg > SQ_MAX_SEGMENTS || seg->n_groups < 1)
-    return SQ_ERR_INVALID_ARG;
-  if ((seg->flags & ~(SQ_FLAG_SINGLE_SCALE | SQ_FLAG_W4 | SQ_FLAG_FP8)) != 0)
-    return SQ_ERR_INVALID_ARG;
-  if ((seg->flags & SQ_FLAG_W4) && (seg->flags & SQ_FLAG_FP8)) return SQ_ERR_INVALID_ARG;
-  p.P = (seg->flags & SQ_FLAG_SINGLE_SCALE) ? 1 : 2;
-  p.w4 = (seg->flags & SQ_FLAG_W4) ? 1 : 0;
-  p.fp8 = (seg->flags & SQ_FLAG_FP8) ? 1 : 0;
-  p.mode = seg->mode;
-  p.n_seg = seg->n_seg;
-  p.G = seg->n_groups;
-  if (seg->mode == SQ_SEG_NONE) {
-    if (seg->n_seg != 1 || seg->n_groups != 1) return SQ_ERR_INVALID_ARG;
-    p.S = 1;
-    p.off[0] = 0;
-    p.off[1] = static_cast<int32_t>(K);
-    *out = p;
-    return SQ_OK;
-  }
-  if (seg->offsets == nullptr || seg->offsets[0] != 0) return SQ_ERR_INVALID_ARG;
-  for (int i = 0; i < seg->n_seg; ++i) {
-    if (seg->offsets[i + 1] <= seg->offsets[i]) return SQ_ERR_INVALID_ARG;
-    p.off[i] = seg->offsets[i];
-  }
-  p.off[seg->n_seg] = seg->offsets[seg->n_seg];
-  if (seg->mode == SQ_SEG_INPUT) {
-    if (seg->n_groups != 1) return SQ_ERR_INVALID_ARG;
-    if (p.off[p.n_seg] != K) return SQ_ERR_INVALID_ARG;
-    for (int i = 0; i < p.n_seg; ++i) {
-      const int64_t w = p.off[i + 1] - p.off[i];
-      if (w % 32 != 0) return SQ_ERR_UNSUPPORTED;
-      if (w > kMaxSegWidth) return SQ_ERR_OVERFLOW;
-    }
-    p.S = p.n_seg;
-  } else {
-    if (seg->n_groups != 1 && seg->n_groups != seg->n_seg) return SQ_ERR_INVALID_ARG;
-    if (extent_n >= 0 && p.off[p.n_seg] != extent_n) return SQ_ERR_INVALID_ARG;
-    if (seg->n_groups > 1)
-      for (int i = 0; i < p.n_seg; ++i)
-        if ((p.off[i + 1] - p.off[i]) % 128 != 0) return SQ_ERR_UNSUPPORTED;
-    p.S = 1;
-  }
-  *out = p;
-  return SQ_OK;
-}
-
 sq_status check_k(int64_t K) {
   if (K < 16 || K % 16 != 0 || K > INT32_MAX) return SQ_ERR_INVALID_ARG;
   return SQ_OK;
@@ -207,6 +125,86 @@ sq_status quantize_common(const void *x, int64_t M, int64_t K, int64_t ldx, cons
 }
 
 }  // namespace
+
+// Current device must be sm_100 (the kernels are built for sm_100a only).
+sq_status check_device() {
+  static int checked[kMaxDevices] = {};  // 0 unknown, 1 ok, -1 unsupported
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return SQ_ERR_NO_DEVICE;
+  }
+  if (checked[dev] == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return SQ_ERR_NO_DEVICE;
+    }
+    checked[dev] = (major == 10 && minor == 0) ? 1 : -1;
+  }
+  return checked[dev] == 1 ? SQ_OK : SQ_ERR_NO_DEVICE;
+}
+
+sq_status parse_segments(const sq_segments *seg, int64_t K, int64_t extent_n, SegParams *out) {
+  SegParams p{};
+  if (seg == nullptr) {
+    p.mode = SQ_SEG_NONE;
+    p.n_seg = 1;
+    p.G = 1;
+    p.S = 1;
+    p.P = 2;
+    p.off[0] = 0;
+    p.off[1] = static_cast<int32_t>(K);
+    *out = p;
+    return SQ_OK;
+  }
+  if (seg->mode < SQ_SEG_NONE || seg->mode > SQ_SEG_INPUT) return SQ_ERR_INVALID_ARG;
+  if (seg->n_seg < 1 || seg->n_seg > SQ_MAX_SEGMENTS || seg->n_groups < 1)
+    return SQ_ERR_INVALID_ARG;
+  if ((seg->flags & ~(SQ_FLAG_SINGLE_SCALE | SQ_FLAG_W4 | SQ_FLAG_FP8)) != 0)
+    return SQ_ERR_INVALID_ARG;
+  if ((seg->flags & SQ_FLAG_W4) && (seg->flags & SQ_FLAG_FP8)) return SQ_ERR_INVALID_ARG;
+  p.P = (seg->flags & SQ_FLAG_SINGLE_SCALE) ? 1 : 2;
+  p.w4 = (seg->flags & SQ_FLAG_W4) ? 1 : 0;
+  p.fp8 = (seg->flags & SQ_FLAG_FP8) ? 1 : 0;
+  p.mode = seg->mode;
+  p.n_seg = seg->n_seg;
+  p.G = seg->n_groups;
+  if (seg->mode == SQ_SEG_NONE) {
+    if (seg->n_seg != 1 || seg->n_groups != 1) return SQ_ERR_INVALID_ARG;
+    p.S = 1;
+    p.off[0] = 0;
+    p.off[1] = static_cast<int32_t>(K);
+    *out = p;
+    return SQ_OK;
+  }
+  if (seg->offsets == nullptr || seg->offsets[0] != 0) return SQ_ERR_INVALID_ARG;
+  for (int i = 0; i < seg->n_seg; ++i) {
+    if (seg->offsets[i + 1] <= seg->offsets[i]) return SQ_ERR_INVALID_ARG;
+    p.off[i] = seg->offsets[i];
+  }
+  p.off[seg->n_seg] = seg->offsets[seg->n_seg];
+  if (seg->mode == SQ_SEG_INPUT) {
+    if (seg->n_groups != 1) return SQ_ERR_INVALID_ARG;
+    if (p.off[p.n_seg] != K) return SQ_ERR_INVALID_ARG;
+    for (int i = 0; i < p.n_seg; ++i) {
+      const int64_t w = p.off[i + 1] - p.off[i];
+      if (w % 32 != 0) return SQ_ERR_UNSUPPORTED;
+      if (w > kMaxSegWidth) return SQ_ERR_OVERFLOW;
+    }
+    p.S = p.n_seg;
+  } else {
+    if (seg->n_groups != 1 && seg->n_groups != seg->n_seg) return SQ_ERR_INVALID_ARG;
+    if (extent_n >= 0 && p.off[p.n_seg] != extent_n) return SQ_ERR_INVALID_ARG;
+    if (seg->n_groups > 1)
+      for (int i = 0; i < p.n_seg; ++i)
+        if ((p.off[i + 1] - p.off[i]) % 128 != 0) return SQ_ERR_UNSUPPORTED;
+    p.S = 1;
+  }
+  *out = p;
+  return SQ_OK;
+}
 
 sq_status validate_quantize_act(const void *x, int64_t M, int64_t K, int64_t ldx, const float *d,
                                 const float *s_act, const sq_segments *seg, int8_t *planes) {

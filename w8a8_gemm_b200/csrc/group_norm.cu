@@ -1,0 +1,550 @@
+// group_norm.cu -- group norm with an activation on channels-last rows, the
+// producer of a quantized linear's input: x [B][S][C] (row stride ld), G groups
+// of C / G neighbouring channels.
+//   mean, var over the S x C/G values of a sample's group; rstd = 1/sqrt(var + eps)
+//   v = (x - mean) rstd gamma + beta,  y = act(v)
+// backward, with dv = dy act'(v), h = dv gamma, xh = (x - mean) rstd, n = S C/G:
+//   dbeta = sum dv, dgamma = sum dv xh over samples and rows,
+//   dx = rstd (h - (sum_group h + xh sum_group h xh) / n).
+//
+// Both directions are bound by memory traffic and take two kernels: one reads
+// the rows and leaves partial results of its chunk of rows, the other joins the
+// partials (a few KB) and reads the rows again, from L2 where they fit.  The
+// statistics are Welford-style (count, mean, sum of squares about the mean):
+// eight rows at a time about their own mean, then joined, in fp32 and in fp64
+// for the last join, so that a mean far above the deviation costs no digits.
+// Every join runs in a fixed order.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mma.cuh"
+#include "sq_internal.h"
+
+namespace sq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 8;  // rows whose values a thread holds at once
+
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = bf16_lo(w[j]);
+    f[2 * j + 1] = bf16_hi(w[j]);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]),
+                    bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ uint4 load8(const uint16_t *p) {
+  return *reinterpret_cast<const uint4 *>(p);
+}
+
+// How a block's threads share C: `oct` octets of 8 channels a pass, `lanes`
+// threads (rows) per octet.
+struct Split {
+  int oct, lanes;
+};
+__host__ __device__ inline Split split_of(int C) {
+  const int o = C / 8;
+  return o >= kThreads ? Split{kThreads, 1} : Split{o, kThreads / o};
+}
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
+}
+
+__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + __expf(-v)); }
+constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
+
+template <int ACT>
+__device__ __forceinline__ float act(float v) {
+  if constexpr (ACT == SQ_ACT_SILU) return v * sigmoid(v);
+  // tanh GELU: v/2 (1 + tanh u) = v sigmoid(2u)
+  if constexpr (ACT == SQ_ACT_GELU)
+    return v * sigmoid(2.0f * kGeluC * (v + 0.044715f * v * v * v));
+  return v;
+}
+template <int ACT>
+__device__ __forceinline__ float act_grad(float v) {
+  if constexpr (ACT == SQ_ACT_SILU) {
+    const float g = sigmoid(v);
+    return g * (1.0f + v * (1.0f - g));
+  }
+  if constexpr (ACT == SQ_ACT_GELU) {
+    const float g = sigmoid(2.0f * kGeluC * (v + 0.044715f * v * v * v));
+    return g + v * g * (1.0f - g) * 2.0f * kGeluC * (1.0f + 3.0f * 0.044715f * v * v);
+  }
+  return 1.0f;
+}
+
+// ------------------------------------------------------------------- forward
+// Chunk statistics: part[b][chunk][g] = {mean, sum of squares about it}.
+__global__ void __launch_bounds__(kThreads) gn_stats_kernel(const GroupNormArgs p) {
+  extern __shared__ float2 sh[];
+  float2 *lane_buf = sh;                   // [lanes][oct * 8] {mean, M2}
+  float2 *chan = sh + kThreads * 8;        // [C]
+  const int b = blockIdx.y;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_chunk;
+  const int rows = p.S - r0 < p.rows_per_chunk ? static_cast<int>(p.S - r0) : p.rows_per_chunk;
+  const Split sp = split_of(p.C);
+  const int lane = threadIdx.x / sp.oct, oct = threadIdx.x % sp.oct;
+  const uint16_t *x = p.x + (static_cast<int64_t>(b) * p.S + r0) * p.ldx;
+
+  for (int o0 = 0; o0 < p.C / 8; o0 += sp.oct) {
+    const int here = p.C / 8 - o0 < sp.oct ? p.C / 8 - o0 : sp.oct;
+    if (lane < sp.lanes && oct < here) {
+      float mean[8], m2[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mean[j] = m2[j] = 0.0f;
+      float n = 0.0f;
+      const uint16_t *src = x + (o0 + oct) * 8;
+      for (int r = lane; r < rows; r += sp.lanes * kBatch) {
+        uint4 v[kBatch];
+        int k = 0;
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          const int rr = r + q * sp.lanes;
+          const bool in = rr < rows;
+          v[q] = in ? load8(src + rr * p.ldx) : make_uint4(0, 0, 0, 0);
+          k += in;
+        }
+        const float fk = static_cast<float>(k), inv = 1.0f / fk;
+        const float total = n + fk, w = fk / total;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float s = 0.0f;
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q) {
+            const uint32_t word = j < 2 ? v[q].x : j < 4 ? v[q].y : j < 6 ? v[q].z : v[q].w;
+            s += (j & 1) ? bf16_hi(word) : bf16_lo(word);
+          }
+          const float bm = s * inv;
+          float bs = 0.0f;
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q) {
+            const uint32_t word = j < 2 ? v[q].x : j < 4 ? v[q].y : j < 6 ? v[q].z : v[q].w;
+            const float d = ((j & 1) ? bf16_hi(word) : bf16_lo(word)) - bm;
+            bs = q < k ? fmaf(d, d, bs) : bs;
+          }
+          const float delta = bm - mean[j];
+          mean[j] = fmaf(delta, w, mean[j]);
+          m2[j] += bs + delta * delta * n * w;
+        }
+        n = total;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        lane_buf[(lane * sp.oct + oct) * 8 + j] = make_float2(mean[j], m2[j]);
+    }
+    __syncthreads();
+    // join the lanes of each channel
+    for (int c = threadIdx.x; c < here * 8; c += kThreads) {
+      float mean = 0.0f, m2 = 0.0f, n = 0.0f;
+      for (int l = 0; l < sp.lanes && l < rows; ++l) {
+        const float k = static_cast<float>((rows - l + sp.lanes - 1) / sp.lanes);
+        const float2 v = lane_buf[l * sp.oct * 8 + c];
+        const float total = n + k, w = k / total, delta = v.x - mean;
+        mean = fmaf(delta, w, mean);
+        m2 += v.y + delta * delta * n * w;
+        n = total;
+      }
+      chan[o0 * 8 + c] = make_float2(mean, m2);
+    }
+    __syncthreads();
+  }
+  // join the channels of each group (equal counts)
+  const int cg = p.C / p.G;
+  const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
+  const int64_t slot = (static_cast<int64_t>(b) * p.chunks + blockIdx.x) * p.G;
+  for (int g = warp; g < p.G; g += kWarps) {
+    float s = 0.0f;
+    for (int c = ln; c < cg; c += 32) s += chan[g * cg + c].x;
+    const float mean = warp_sum(s) / static_cast<float>(cg);
+    float m2 = 0.0f;
+    for (int c = ln; c < cg; c += 32) {
+      const float2 v = chan[g * cg + c];
+      const float d = v.x - mean;
+      m2 += v.y + d * d * static_cast<float>(rows);
+    }
+    m2 = warp_sum(m2);
+    if (ln == 0 && store_ok(p.status, slot + g < static_cast<int64_t>(p.B) * p.chunks * p.G))
+      p.part[slot + g] = make_float2(mean, m2);
+  }
+}
+
+// Joins a sample's chunk statistics into {mean, rstd} of each group.
+__device__ __forceinline__ void join_stats(const GroupNormArgs &p, int b, float2 *stat) {
+  const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
+  const int cg = p.C / p.G;
+  for (int g = warp; g < p.G; g += kWarps) {
+    const float2 *src = p.part + static_cast<int64_t>(b) * p.chunks * p.G + g;
+    double s = 0.0;
+    for (int k = ln; k < p.chunks; k += 32) {
+      const int64_t left = p.S - static_cast<int64_t>(k) * p.rows_per_chunk;
+      const double n = left < p.rows_per_chunk ? left : p.rows_per_chunk;
+      s += n * src[static_cast<int64_t>(k) * p.G].x;
+    }
+    const double mean = warp_sum(s) / static_cast<double>(p.S);
+    double m2 = 0.0;
+    for (int k = ln; k < p.chunks; k += 32) {
+      const int64_t left = p.S - static_cast<int64_t>(k) * p.rows_per_chunk;
+      const double n = left < p.rows_per_chunk ? left : p.rows_per_chunk;
+      const float2 v = src[static_cast<int64_t>(k) * p.G];
+      const double d = v.x - mean;
+      m2 += v.y + n * cg * d * d;
+    }
+    const double var = warp_sum(m2) / (static_cast<double>(p.S) * cg);
+    if (ln == 0)
+      stat[g] = make_float2(static_cast<float>(mean),
+                            static_cast<float>(1.0 / sqrt(var + static_cast<double>(p.eps))));
+  }
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(kThreads) gn_apply_kernel(const GroupNormArgs p) {
+  extern __shared__ float2 sh[];  // [G] {mean, rstd}
+  const int b = blockIdx.y;
+  join_stats(p, b, sh);
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int g = threadIdx.x; g < p.G; g += kThreads)
+      if (store_ok(p.status, b < p.B)) {
+        p.mean[b * p.G + g] = sh[g].x;
+        p.rstd[b * p.G + g] = sh[g].y;
+      }
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_chunk;
+  const int rows = p.S - r0 < p.rows_per_chunk ? static_cast<int>(p.S - r0) : p.rows_per_chunk;
+  const Split sp = split_of(p.C);
+  const int lane = threadIdx.x / sp.oct, oct = threadIdx.x % sp.oct;
+  if (lane >= sp.lanes) return;
+  const int cg = p.C / p.G;
+  const int64_t row0 = static_cast<int64_t>(b) * p.S + r0;
+  for (int o = oct; o < p.C / 8; o += sp.oct) {
+    const int c0 = o * 8;
+    float mean[8], a[8], beta[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 s = sh[(c0 + j) / cg];
+      mean[j] = s.x;
+      a[j] = s.y * (p.gamma ? bf16_lo(p.gamma[c0 + j]) : 1.0f);
+      beta[j] = p.beta ? bf16_lo(p.beta[c0 + j]) : 0.0f;
+    }
+    for (int r = lane; r < rows; r += sp.lanes * 4) {
+      uint4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (r + q * sp.lanes < rows) v[q] = load8(p.x + (row0 + r + q * sp.lanes) * p.ldx + c0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (r + q * sp.lanes >= rows) break;
+        float f[8];
+        unpack8(v[q], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = act<ACT>(fmaf(f[j] - mean[j], a[j], beta[j]));
+        const int64_t row = row0 + r + q * sp.lanes;
+        if (store_ok(p.status, row < static_cast<int64_t>(p.B) * p.S && c0 + 8 <= p.ldy))
+          *reinterpret_cast<uint4 *>(p.y + row * p.ldy + c0) = pack8(f);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ backward
+// One channel's fixed values.
+struct Chan {
+  float mean, rstd, gamma, beta;
+};
+__device__ __forceinline__ Chan chan_of(const GroupNormArgs &p, int b, int c, int cg) {
+  const int g = c / cg;
+  return {p.mean[b * p.G + g], p.rstd[b * p.G + g], p.gamma ? bf16_lo(p.gamma[c]) : 1.0f,
+          p.beta ? bf16_lo(p.beta[c]) : 0.0f};
+}
+
+// Chunk sums: chan_part[b][chunk][c] = {sum dv, sum dv xh} and
+// part[b][chunk][g] = {sum h, sum h xh}.
+template <int ACT>
+__global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const GroupNormArgs p) {
+  extern __shared__ float2 sh[];
+  float2 *lane_buf = sh;             // [lanes][oct * 8]
+  float2 *chan = sh + kThreads * 8;  // [C]
+  const int b = blockIdx.y;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_chunk;
+  const int rows = p.S - r0 < p.rows_per_chunk ? static_cast<int>(p.S - r0) : p.rows_per_chunk;
+  const Split sp = split_of(p.C);
+  const int lane = threadIdx.x / sp.oct, oct = threadIdx.x % sp.oct;
+  const int cg = p.C / p.G;
+  const int64_t row0 = static_cast<int64_t>(b) * p.S + r0;
+  const int64_t slot = static_cast<int64_t>(b) * p.chunks + blockIdx.x;
+
+  for (int o0 = 0; o0 < p.C / 8; o0 += sp.oct) {
+    const int here = p.C / 8 - o0 < sp.oct ? p.C / 8 - o0 : sp.oct;
+    if (lane < sp.lanes && oct < here) {
+      const int c0 = (o0 + oct) * 8;
+      Chan ch[8];
+      float sd[8], sx[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        ch[j] = chan_of(p, b, c0 + j, cg);
+        sd[j] = sx[j] = 0.0f;
+      }
+      for (int r = lane; r < rows; r += sp.lanes * 4) {
+        uint4 vx[4], vd[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t row = row0 + r + q * sp.lanes;
+          const bool in = r + q * sp.lanes < rows;
+          vx[q] = in ? load8(p.x + row * p.ldx + c0) : make_uint4(0, 0, 0, 0);
+          vd[q] = in ? load8(p.dy + row * p.lddy + c0) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (r + q * sp.lanes >= rows) break;
+          float x[8], d[8];
+          unpack8(vx[q], x);
+          unpack8(vd[q], d);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float xh = (x[j] - ch[j].mean) * ch[j].rstd;
+            const float dv = d[j] * act_grad<ACT>(fmaf(xh, ch[j].gamma, ch[j].beta));
+            sd[j] += dv;
+            sx[j] = fmaf(dv, xh, sx[j]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        lane_buf[(lane * sp.oct + oct) * 8 + j] = make_float2(sd[j], sx[j]);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < here * 8; c += kThreads) {
+      float2 s = make_float2(0.0f, 0.0f);
+      for (int l = 0; l < sp.lanes; ++l) {
+        const float2 v = lane_buf[l * sp.oct * 8 + c];
+        s.x += v.x;
+        s.y += v.y;
+      }
+      chan[o0 * 8 + c] = s;
+      if (store_ok(p.status, slot < static_cast<int64_t>(p.B) * p.chunks && o0 * 8 + c < p.C))
+        p.chan_part[slot * p.C + o0 * 8 + c] = s;
+    }
+    __syncthreads();
+  }
+  const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
+  for (int g = warp; g < p.G; g += kWarps) {
+    float s1 = 0.0f, s2 = 0.0f;
+    for (int c = g * cg + ln; c < (g + 1) * cg; c += 32) {
+      const float gm = p.gamma ? bf16_lo(p.gamma[c]) : 1.0f;
+      s1 = fmaf(gm, chan[c].x, s1);
+      s2 = fmaf(gm, chan[c].y, s2);
+    }
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if (ln == 0 && store_ok(p.status, slot < static_cast<int64_t>(p.B) * p.chunks))
+      p.part[slot * p.G + g] = make_float2(s1, s2);
+  }
+}
+
+// The first `grad_blocks` blocks add up 32 channels each of dgamma and dbeta;
+// the others write dx.
+template <int ACT, bool GF32>
+__global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs p) {
+  extern __shared__ float2 sh[];
+  const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
+  if (static_cast<int>(blockIdx.x) < p.grad_blocks) {
+    const int c = blockIdx.x * 32 + ln;
+    double s = 0.0, sx = 0.0;
+    if (c < p.C)
+      for (int64_t k = warp; k < static_cast<int64_t>(p.B) * p.chunks; k += kWarps) {
+        const float2 v = p.chan_part[k * p.C + c];
+        s += v.x;
+        sx += v.y;
+      }
+    double2 *buf = reinterpret_cast<double2 *>(sh);
+    buf[warp * 32 + ln] = make_double2(s, sx);
+    __syncthreads();
+    if (warp != 0 || c >= p.C) return;
+    for (int w = 1; w < kWarps; ++w) {
+      s += buf[w * 32 + ln].x;
+      sx += buf[w * 32 + ln].y;
+    }
+    if (!store_ok(p.status, c < p.C)) return;
+    if constexpr (GF32) {
+      if (p.dgamma) static_cast<float *>(p.dgamma)[c] = static_cast<float>(sx);
+      if (p.dbeta) static_cast<float *>(p.dbeta)[c] = static_cast<float>(s);
+    } else {
+      if (p.dgamma)
+        static_cast<__nv_bfloat16 *>(p.dgamma)[c] = __float2bfloat16_rn(static_cast<float>(sx));
+      if (p.dbeta)
+        static_cast<__nv_bfloat16 *>(p.dbeta)[c] = __float2bfloat16_rn(static_cast<float>(s));
+    }
+    return;
+  }
+  const int blk = blockIdx.x - p.grad_blocks;
+  const int b = blk / p.chunks, chunk = blk % p.chunks;
+  const int cg = p.C / p.G;
+  const double n = static_cast<double>(p.S) * cg;
+  // group sums over n
+  for (int g = warp; g < p.G; g += kWarps) {
+    const float2 *src = p.part + static_cast<int64_t>(b) * p.chunks * p.G + g;
+    double s1 = 0.0, s2 = 0.0;
+    for (int k = ln; k < p.chunks; k += 32) {
+      const float2 v = src[static_cast<int64_t>(k) * p.G];
+      s1 += v.x;
+      s2 += v.y;
+    }
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if (ln == 0) sh[g] = make_float2(static_cast<float>(s1 / n), static_cast<float>(s2 / n));
+  }
+  __syncthreads();
+  const int64_t r0 = static_cast<int64_t>(chunk) * p.rows_per_chunk;
+  const int rows = p.S - r0 < p.rows_per_chunk ? static_cast<int>(p.S - r0) : p.rows_per_chunk;
+  const Split sp = split_of(p.C);
+  const int lane = threadIdx.x / sp.oct, oct = threadIdx.x % sp.oct;
+  if (lane >= sp.lanes) return;
+  const int64_t row0 = static_cast<int64_t>(b) * p.S + r0;
+  for (int o = oct; o < p.C / 8; o += sp.oct) {
+    const int c0 = o * 8;
+    Chan ch[8];
+    float m1[8], m2[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      ch[j] = chan_of(p, b, c0 + j, cg);
+      const float2 s = sh[(c0 + j) / cg];
+      m1[j] = s.x;
+      m2[j] = s.y;
+    }
+    for (int r = lane; r < rows; r += sp.lanes * 4) {
+      uint4 vx[4], vd[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (r + q * sp.lanes < rows) {
+          const int64_t row = row0 + r + q * sp.lanes;
+          vx[q] = load8(p.x + row * p.ldx + c0);
+          vd[q] = load8(p.dy + row * p.lddy + c0);
+        }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (r + q * sp.lanes >= rows) break;
+        float x[8], d[8];
+        unpack8(vx[q], x);
+        unpack8(vd[q], d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float xh = (x[j] - ch[j].mean) * ch[j].rstd;
+          const float h =
+              d[j] * act_grad<ACT>(fmaf(xh, ch[j].gamma, ch[j].beta)) * ch[j].gamma;
+          x[j] = ch[j].rstd * (h - m1[j] - xh * m2[j]);
+        }
+        const int64_t row = row0 + r + q * sp.lanes;
+        if (store_ok(p.status, row < static_cast<int64_t>(p.B) * p.S && c0 + 8 <= p.lddx))
+          *reinterpret_cast<uint4 *>(p.dx + row * p.lddx + c0) = pack8(x);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host side
+// Rows of a chunk: about four blocks per SM of a 148-SM device over all
+// samples, but at least eight rows (one batch) per thread where S allows.  A
+// fixed rule, so that the workspace size and the order of every sum depend on
+// the sizes only.
+int64_t chunk_rows(int64_t B, int64_t S, int64_t C) {
+  const int64_t want = (4 * 148 + B - 1) / B;
+  const int64_t least = static_cast<int64_t>(split_of(static_cast<int>(C)).lanes) * kBatch;
+  int64_t rows = (S + want - 1) / want;
+  if (rows < least) rows = least;
+  return rows;
+}
+
+int stats_smem(int C) { return (kThreads * 8 + C) * static_cast<int>(sizeof(float2)); }
+
+template <auto Kernel>
+cudaError_t allow(int smem) {
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) done[dev] = true;
+  return e;
+}
+
+void fill_chunks(GroupNormArgs &p) {
+  p.rows_per_chunk = static_cast<int32_t>(chunk_rows(p.B, p.S, p.C));
+  p.chunks = static_cast<int32_t>((p.S + p.rows_per_chunk - 1) / p.rows_per_chunk);
+}
+
+template <int ACT>
+cudaError_t run_forward(const GroupNormArgs &p, cudaStream_t stream) {
+  cudaError_t e = allow<gn_stats_kernel>(stats_smem(kGroupNormMaxC));
+  if (e != cudaSuccess) return e;
+  const dim3 grid(p.chunks, p.B);
+  gn_stats_kernel<<<grid, kThreads, stats_smem(p.C), stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  gn_apply_kernel<ACT><<<grid, kThreads, p.G * sizeof(float2), stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int ACT>
+cudaError_t run_backward(GroupNormArgs p, bool gf32, cudaStream_t stream) {
+  cudaError_t e = allow<gn_bwd_sums_kernel<ACT>>(stats_smem(kGroupNormMaxC));
+  if (e != cudaSuccess) return e;
+  gn_bwd_sums_kernel<ACT><<<dim3(p.chunks, p.B), kThreads, stats_smem(p.C), stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  p.grad_blocks = (p.dgamma || p.dbeta) ? (p.C + 31) / 32 : 0;
+  const int dx_blocks = p.dx ? p.chunks * p.B : 0;
+  const int grid = p.grad_blocks + dx_blocks;
+  if (grid == 0) return cudaSuccess;
+  size_t smem = kThreads * sizeof(double2);
+  if (smem < p.G * sizeof(float2)) smem = p.G * sizeof(float2);
+  if (gf32)
+    gn_bwd_dx_kernel<ACT, true><<<grid, kThreads, smem, stream>>>(p);
+  else
+    gn_bwd_dx_kernel<ACT, false><<<grid, kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// float2 words: group partials, then (backward) channel partials.
+size_t group_norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G) {
+  const int64_t rows = chunk_rows(B, S, C);
+  const int64_t chunks = (S + rows - 1) / rows;
+  return static_cast<size_t>(B * chunks * (G + C)) * sizeof(float2);
+}
+
+cudaError_t launch_group_norm_forward(GroupNormArgs p, void *workspace, int act,
+                                      cudaStream_t stream) {
+  fill_chunks(p);
+  p.part = static_cast<float2 *>(workspace);
+  if (act == SQ_ACT_SILU) return run_forward<SQ_ACT_SILU>(p, stream);
+  if (act == SQ_ACT_GELU) return run_forward<SQ_ACT_GELU>(p, stream);
+  return run_forward<SQ_ACT_NONE>(p, stream);
+}
+
+cudaError_t launch_group_norm_backward(GroupNormArgs p, void *workspace, int act, bool gf32,
+                                       cudaStream_t stream) {
+  fill_chunks(p);
+  p.part = static_cast<float2 *>(workspace);
+  p.chan_part = p.part + static_cast<int64_t>(p.B) * p.chunks * p.G;
+  if (act == SQ_ACT_SILU) return run_backward<SQ_ACT_SILU>(p, gf32, stream);
+  if (act == SQ_ACT_GELU) return run_backward<SQ_ACT_GELU>(p, gf32, stream);
+  return run_backward<SQ_ACT_NONE>(p, gf32, stream);
+}
+
+}  // namespace sq

@@ -1,0 +1,342 @@
+// input_grad.cu -- the gradient of a frozen quantized linear with respect to
+// its input, straight through the activation quantizer:
+//   dx[m][k] = sum_n dy[m][n] W~[n][k],  W~[n][k] = s_w[i(k)][n] W^[n][k] / d[g(n)][k].
+//
+// Two kernels.  The first writes W~ transposed, rounded to bf16, into the
+// caller's workspace (3 N K bytes of traffic, a few percent of the product):
+// steps and divisors vary along both dimensions, so they belong to the weight,
+// and with both operands contiguous along the contracted dimension the product
+// needs no transposition.  The rounding to bf16 is one more rounding of the
+// size of dy's own and averages over the N terms.
+//
+// The second is a bf16 product on the tensor cores: persistent blocks of 128 x
+// BN output tiles, TMA into a ring of shared-memory stages (64 columns of the
+// contraction, 128-byte swizzle), tcgen05.mma kind::f16 issued by one thread,
+// fp32 sums in tensor memory, two accumulator buffers so that a tile's
+// epilogue runs under the next tile's products.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mma.cuh"
+#include "sq_internal.h"
+
+namespace sq {
+namespace {
+
+// -------------------------------------------------------------- W~ transposed
+// 64 x 64 tiles through shared memory.  wt [K][ldw], ldw >= N.
+constexpr int kTr = 64;
+__global__ void __launch_bounds__(256) dequant_transpose_kernel(
+    const int8_t *__restrict__ wq, const float *__restrict__ s_w, const float *__restrict__ d,
+    int64_t N, int64_t K, const __grid_constant__ SegParams seg, uint16_t *__restrict__ wt,
+    int64_t ldw, int *status) {
+  __shared__ uint16_t tile[kTr][kTr + 2];  // [k][n]
+  const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kTr;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kTr;
+  // thread: 16 codes of one weight row
+  const int nr = threadIdx.x >> 2, kc = (threadIdx.x & 3) * 16;
+  const int64_t n = n0 + nr, k = k0 + kc;
+  if (n < N && k < K) {  // K % 16 == 0
+    const uint4 v = *reinterpret_cast<const uint4 *>(wq + n * K + k);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const int g = seg.G > 1 ? seg_index(seg.off, seg.n_seg, n) : 0;
+    // input segments are at least 32 wide and aligned to 32: one for 16 codes
+    const int i = seg.S > 1 ? seg_index(seg.off, seg.n_seg, k) : 0;
+    const float s = s_w[i * N + n] * (seg.w4 ? 0.0625f : 1.0f);  // W4 operands hold 16 q
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t byte = (w[j >> 2] >> ((j & 3) * 8)) & 0xFFu;
+      float q;
+      if (seg.fp8) {
+        const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte),
+                                                     __NV_E4M3);
+        q = __half2float(__half(h));
+      } else {
+        q = static_cast<float>(static_cast<int8_t>(byte));
+      }
+      q *= s;
+      if (d != nullptr) q = __fdiv_rn(q, d[g * K + k + j]);
+      const __nv_bfloat16 b = __float2bfloat16_rn(q);
+      tile[kc + j][nr] = *reinterpret_cast<const uint16_t *>(&b);
+    }
+  }
+  __syncthreads();
+  const int c = threadIdx.x & 63;
+  for (int r = threadIdx.x >> 6; r < kTr; r += 4)
+    if (k0 + r < K && n0 + c < N && store_ok(status, n0 + c < ldw))
+      wt[(k0 + r) * ldw + n0 + c] = tile[r][c];
+}
+
+// -------------------------------------------------------------------- product
+constexpr int BM = 128, BK = 64;
+constexpr int kEpiWarps = 8;
+constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s: far above any tile's latency
+
+template <int BN>
+struct GemmSmem {
+  static constexpr int A = BM * BK * 2, B = BN * BK * 2;
+  static constexpr int STAGE = A + B;
+  static constexpr int STAGES = BN == 256 ? 4 : 6;
+  static constexpr int BARS = STAGES * STAGE;
+  static constexpr int BYTES = BARS + (2 * STAGES + 5) * 8 + 16 + 1024;
+};
+
+struct GradArgs {
+  int32_t M, K;         // output rows and columns
+  int32_t num_n_tiles, num_tiles, num_kb;
+  uint16_t *dx;
+  int64_t lddx;
+  int *status;
+};
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                         int *status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      atomicExch(status, static_cast<int>(SQ_ERR_DEVICE_TIMEOUT));
+      return false;
+    }
+  }
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    input_grad_kernel(const __grid_constant__ CUtensorMap tmA,
+                      const __grid_constant__ CUtensorMap tmB, const GradArgs p) {
+  using L = GemmSmem<BN>;
+  constexpr int STAGES = L::STAGES;
+  constexpr int COLS = 2 * BN;  // two accumulator buffers
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::BARS);
+  uint64_t *empty = full + STAGES;
+  uint64_t *acc_full = empty + STAGES;
+  uint64_t *acc_empty = acc_full + 2;
+  uint64_t *mma_done = acc_empty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], kEpiWarps);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_dependency_wait();  // the prologue above touches no global memory
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, armed_parity = 0;
+      for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x) {
+        const int mt = tile / p.num_n_tiles, nt = tile % p.num_n_tiles;
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!wait_bar(&empty[stage], phase ^ 1, abort_flag, p.status)) goto producer_done;
+          uint8_t *sa = smem + stage * L::STAGE;
+          mbar_arrive_expect_tx(&full[stage], L::STAGE);
+          tma_load_2d(sa, &tmA, &full[stage], kb * BK, mt * BM);
+          tma_load_2d(sa + L::A, &tmB, &full[stage], kb * BK, nt * BN);
+          armed |= 1u << stage;
+          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    producer_done:
+      // never leave with a copy in flight into this block's shared memory
+      for (int s = 0; s < STAGES; ++s)
+        if (armed & (1u << s)) mbar_wait(&full[s], (armed_parity >> s) & 1u, kWaitLimitNs);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16(BM, BN);
+      int stage = 0;
+      uint32_t phase = 0, iter = 0;
+      for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x, ++iter) {
+        const uint32_t buf = iter & 1;
+        if (!wait_bar(&acc_empty[buf], ((iter >> 1) & 1) ^ 1, abort_flag, p.status))
+          goto mma_exit;
+        tc_fence_after();
+        const uint32_t acc = tmem_base + buf * BN;
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!wait_bar(&full[stage], phase, abort_flag, p.status)) goto mma_exit;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + stage * L::STAGE), sb = sa + L::A;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            mma_bf16_tc(acc, sdesc_kmajor_sw128(sa + kk * 32), sdesc_kmajor_sw128(sb + kk * 32),
+                        idesc, (kb | kk) != 0);
+          mma_commit(&empty[stage]);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        mma_commit(&acc_full[buf]);
+      }
+    mma_exit:
+      mma_commit(mma_done);
+      mbar_wait(mma_done, 0, kWaitLimitNs);
+    }
+  } else {
+    const int quarter = warp & 3;         // TMEM lanes this warp may read
+    const int half = (warp - 2) >> 2;     // which half of the columns
+    uint32_t iter = 0;
+    for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x, ++iter) {
+      const uint32_t buf = iter & 1;
+      if (!wait_bar(&acc_full[buf], (iter >> 1) & 1, abort_flag, p.status)) break;
+      tc_fence_after();
+      const int mt = tile / p.num_n_tiles, nt = tile % p.num_n_tiles;
+      const int row = mt * BM + quarter * 32 + lane;
+      const uint32_t src = tmem_base + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll 1
+      for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(src + c, r);
+        tmem_ld_wait();
+        const int col = nt * BN + c;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {  // K % 16 == 0: 8 columns are all in or all out
+          const int c8 = col + q * 8;
+          if (row < p.M && c8 < p.K && store_ok(p.status, c8 + 8 <= p.lddx)) {
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              o[j] = bf16x2(__uint_as_float(r[q * 8 + 2 * j]),
+                            __uint_as_float(r[q * 8 + 2 * j + 1]));
+            *reinterpret_cast<uint4 *>(p.dx + static_cast<int64_t>(row) * p.lddx + c8) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, COLS);
+  }
+}
+
+sq_status tensor_map_2d(CUtensorMap *map, const void *ptr, int64_t inner, int64_t outer,
+                        int64_t ld, int box_rows) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (enc == nullptr) return SQ_ERR_CUDA;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {BK, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? SQ_OK
+             : SQ_ERR_CUDA;
+}
+
+template <int BN>
+sq_status run_gemm(const InputGradRequest &r, const uint16_t *wt, int64_t ldw, int sms,
+                   cudaStream_t stream) {
+  using L = GemmSmem<BN>;
+  static_assert(L::BYTES <= 232448, "dynamic shared memory above the per-block limit");
+  CUtensorMap tmA, tmB;
+  sq_status st = tensor_map_2d(&tmA, r.dy, r.N, r.M, r.lddy, BM);
+  if (st == SQ_OK) st = tensor_map_2d(&tmB, wt, r.N, r.K, ldw, BN);
+  if (st != SQ_OK) return st;
+  GradArgs p;
+  p.M = static_cast<int32_t>(r.M);
+  p.K = static_cast<int32_t>(r.K);
+  p.num_n_tiles = static_cast<int32_t>((r.K + BN - 1) / BN);
+  p.num_tiles = static_cast<int32_t>((r.M + BM - 1) / BM) * p.num_n_tiles;
+  p.num_kb = static_cast<int32_t>((r.N + BK - 1) / BK);
+  p.dx = r.dx;
+  p.lddx = r.lddx;
+  p.status = r.status;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SQ_ERR_CUDA;
+  if (!attr_set[dev]) {
+    if (cudaFuncSetAttribute(input_grad_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             L::BYTES) != cudaSuccess)
+      return SQ_ERR_CUDA;
+    attr_set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.num_tiles < sms ? p.num_tiles : sms);
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = L::BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, input_grad_kernel<BN>, tmA, tmB, p) != cudaSuccess)
+    return SQ_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? SQ_OK : SQ_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t input_grad_workspace_bytes(int64_t N, int64_t K) {
+  return static_cast<size_t>((N + 7) / 8 * 8) * static_cast<size_t>(K) * 2;
+}
+
+sq_status launch_input_grad(const InputGradRequest &r, cudaStream_t stream) {
+  const int64_t ldw = (r.N + 7) / 8 * 8;
+  uint16_t *wt = static_cast<uint16_t *>(r.workspace);
+  dequant_transpose_kernel<<<dim3(static_cast<unsigned>((r.K + kTr - 1) / kTr),
+                                  static_cast<unsigned>((r.N + kTr - 1) / kTr)),
+                             256, 0, stream>>>(r.wq, r.s_w, r.d, r.N, r.K, r.seg, wt, ldw,
+                                               r.status);
+  if (cudaGetLastError() != cudaSuccess) return SQ_ERR_CUDA;
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (sms <= 0) sms = 148;
+  // The widest tile that still gives every SM one: a wide tile reads fewer
+  // operand bytes per product, a narrow one spreads a small layer.
+  const int64_t mt = (r.M + BM - 1) / BM;
+  if (mt * ((r.K + 255) / 256) >= sms) return run_gemm<256>(r, wt, ldw, sms, stream);
+  if (mt * ((r.K + 127) / 128) >= sms) return run_gemm<128>(r, wt, ldw, sms, stream);
+  return run_gemm<64>(r, wt, ldw, sms, stream);
+}
+
+}  // namespace sq

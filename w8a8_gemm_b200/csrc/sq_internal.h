@@ -97,6 +97,87 @@ sq_status launch_gemm(const GemmRequest &req, cudaStream_t stream);
 // current device.
 size_t gemm_workspace_bytes();
 
+// ---- low-rank adapters (lora.cu) ---------------------------------------------
+// Rows of one tile of the plan.
+#define SQ_LORA_TILE_ROWS 64
+
+struct LoraRequest {
+  const uint16_t *x, *dy, *A, *B;
+  const float *scale;
+  const int32_t *plan;
+  const void *base;      // forward: y's, backward: dx's; nullptr: zeros
+  void *y;               // forward
+  uint16_t *dx;          // backward, may be nullptr
+  void *dA, *dB;         // backward, both or neither
+  float *t, *dt;         // [M][R]
+  int64_t ldx, lddy, ld_base, ldy, lddx;
+  int64_t M, N, K;
+  int32_t R, L;
+  bool f32;              // forward: base and y are fp32; backward: dA and dB are
+  int *status;
+};
+size_t lora_plan_words(int64_t M, int32_t L);
+cudaError_t launch_lora_plan(const int32_t *adapter, int64_t M, int32_t L, int32_t *plan,
+                             int *status, cudaStream_t stream);
+cudaError_t launch_lora_forward(const LoraRequest &q, cudaStream_t stream);
+cudaError_t launch_lora_backward(const LoraRequest &q, cudaStream_t stream);
+
+// ---- rotary positions (rope.cu) ----------------------------------------------
+struct RopeArgs {
+  const void *x;
+  int64_t ldx;
+  void *out;
+  int64_t ldo;
+  const int32_t *positions;  // [M][axes]
+  const float *inv_freq;     // [rot / 2]
+  int64_t M;
+  int32_t H, D, rot, axes;
+  int32_t axis_end[SQ_ROPE_MAX_AXES];  // pairs before the end of each axis
+  float factor, sign;
+  int32_t rows_per_block;    // set by the launcher
+  int *status;
+};
+cudaError_t launch_rope(const RopeArgs &p, bool half, bool f32, cudaStream_t stream);
+
+// ---- group norm (group_norm.cu) ----------------------------------------------
+constexpr int kGroupNormMaxC = 8192, kGroupNormMaxG = 1024;
+struct GroupNormArgs {
+  const uint16_t *x, *dy;
+  uint16_t *y, *dx;
+  int64_t ldx, lddy, ldy, lddx;
+  const uint16_t *gamma, *beta;  // nullptr: 1 and 0
+  float *mean, *rstd;            // [B][G]; forward writes, backward reads
+  void *dgamma, *dbeta;          // [C], may be nullptr
+  int64_t S;
+  int32_t B, C, G;
+  float eps;
+  // set by the launcher
+  int32_t rows_per_chunk, chunks, grad_blocks;
+  float2 *part, *chan_part;
+  int *status;
+};
+size_t group_norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G);
+cudaError_t launch_group_norm_forward(GroupNormArgs p, void *workspace, int act,
+                                      cudaStream_t stream);
+cudaError_t launch_group_norm_backward(GroupNormArgs p, void *workspace, int act, bool gf32,
+                                       cudaStream_t stream);
+
+// ---- input gradient of a quantized linear (input_grad.cu) ----------------------
+struct InputGradRequest {
+  const uint16_t *dy;
+  int64_t lddy;
+  const int8_t *wq;
+  const float *s_w, *d;
+  SegParams seg;
+  uint16_t *dx;
+  int64_t lddx;
+  void *workspace;
+  int64_t M, N, K;
+  int *status;
+};
+size_t input_grad_workspace_bytes(int64_t N, int64_t K);
+sq_status launch_input_grad(const InputGradRequest &r, cudaStream_t stream);
+
 // ---- test-only probes (probe.cu) -------------------------------------------
 cudaError_t launch_timeout_probe(uint32_t limit_us, int *status, cudaStream_t stream);
 // Debug build only: one checked store to element n of a buffer said to hold n.
@@ -112,6 +193,13 @@ sq_status validate_gemm(const int8_t *planes, const int8_t *wq, const float *s_w
 
 // Device address of the library's error word on the current device.
 int *device_status_word();
+
+// SQ_OK if the current device is an sm_100.
+sq_status check_device();
+
+// Validates a segment table.  extent_n < 0 means N is not known to the call
+// (activation-side calls), in which case the output offsets end is not checked.
+sq_status parse_segments(const sq_segments *seg, int64_t K, int64_t extent_n, SegParams *out);
 
 // cuTensorMapEncodeTiled, resolved through the runtime (no link-time libcuda).
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
