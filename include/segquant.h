@@ -563,7 +563,7 @@ SQ_API sq_status sq_lora_forward(const void *x, int64_t ldx, const void *A, cons
 
 /*
  * sq_lora_backward -- the gradients of sq_lora_forward from dy = dL/dy:
- *   dt[m] = scale[a] B[a]^T dy[m]                   (workspace, fp32)
+ *   dt[m] = scale[a] B[a]^T dy[m]
  *   dB[a] = scale[a] sum_{m of a} dy[m] t[m]^T      dA[a] = sum_{m of a} dt[m] x[m]^T
  *   dx[m] = dx_base[m] + A[a]^T dt[m]
  * dA and dB are written whole (zeros for an adapter without rows); rows without
@@ -576,16 +576,21 @@ SQ_API sq_status sq_lora_forward(const void *x, int64_t ldx, const void *A, cons
  *   dx_base  bf16 [M][ldbase] or NULL for zeros; dx bf16 [M][lddx] output, or
  *            NULL (with dx_base NULL) to skip it; dx_base may be dx
  *   dA, dB   [L][R][K] and [L][N][R] outputs of grad_dtype, or both NULL
- *   dt       fp32 [M][R] workspace
- * Alignment and limits as in the forward call; dA, dB, dt 16-byte aligned.
+ *   workspace  device memory of sq_lora_workspace_bytes(M, R, L, grad_dtype)
+ *            bytes, 16-byte aligned; needs no initial value (NULL when M == 0)
+ * Alignment and limits as in the forward call; dA and dB 16-byte aligned.
  * M == 0 writes zeros to dA and dB.  Up to three kernels.
+ * sq_lora_workspace_bytes: 0 for sizes out of range.
  */
+SQ_API size_t sq_lora_workspace_bytes(int64_t M, int32_t R, int32_t n_adapters,
+                                      sq_out_dtype grad_dtype);
 SQ_API sq_status sq_lora_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
                                   const float *t, const void *A, const void *B,
                                   const float *scale, const int32_t *plan, const void *dx_base,
                                   int64_t ldbase, void *dx, int64_t lddx, void *dA, void *dB,
-                                  sq_out_dtype grad_dtype, float *dt, int64_t M, int64_t N,
-                                  int64_t K, int32_t R, int32_t n_adapters, sq_stream_t stream);
+                                  sq_out_dtype grad_dtype, void *workspace,
+                                  size_t workspace_bytes, int64_t M, int64_t N, int64_t K,
+                                  int32_t R, int32_t n_adapters, sq_stream_t stream);
 
 /* Which two columns of a head are pair i of `rot` rotated columns. */
 typedef enum {

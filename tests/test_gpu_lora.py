@@ -104,12 +104,15 @@ def test_plan_orders_rows_by_adapter_and_keeps_their_order():
         for b in range(L + 1):
             start.append(start[-1] + int((key == b).sum()))
         assert plan[1:3] == [M, L]
-        assert plan[4:4 + L + 2] == start
-        assert plan[4 + L + 2:4 + L + 2 + M] == order
-        tiles = [(b, s) for b in range(L + 1) for s in range(start[b], start[b + 1], 64)]
-        at = 4 + L + 2 + M
+        tiles = [(b, s) for b in range(L + 1) for s in range(start[b], start[b + 1], 128)]
         assert plan[3] == len(tiles)
-        assert list(zip(plan[at:at + 2 * len(tiles):2], plan[at + 1:at + 2 * len(tiles):2])) == tiles
+        assert plan[4:4 + L + 2] == [sum(t[0] < b for t in tiles) for b in range(L + 2)]
+        at = (4 + L + 2 + 3) // 4 * 4
+        for b, s in tiles:     # {bin, rows, place, 0, row numbers}
+            n = min(128, start[b + 1] - s)
+            assert plan[at:at + 3] == [b, n, s]
+            assert plan[at + 4:at + 132] == order[s:s + n] + [order[s]] * (128 - n)
+            at += 132
 
 
 def test_in_place_strides_and_columns_beyond_are_untouched():
@@ -213,15 +216,18 @@ def test_plan_of_another_batch_is_reported_and_nothing_written():
     p = _problem(M, K, N, R, L, seed=4)
     other = B.sq_lora_plan(torch.zeros(M + 1, dtype=torch.int32, device="cuda"), L)
     y = torch.full((M, N), 9.0, dtype=BF, device="cuda")
-    # the binding refuses it by its size ...
+    # the binding refuses a plan of another size ...
     with pytest.raises(ValueError, match="plan"):
-        B.sq_lora_forward(p["x"], p["A"], p["B"], p["scale"], other, p["base"], y=y)
-    # ... and the kernels by what the plan says of itself
+        B.sq_lora_forward(p["x"], p["A"], p["B"], p["scale"], B.sq_lora_plan(
+            torch.zeros(400, dtype=torch.int32, device="cuda"), L), p["base"], y=y)
+    # ... and the kernels one that says that it is not theirs
     t = torch.full((M, R), 9.0, device="cuda")
-    rc = B.lib().sq_lora_forward(B._ptr(p["x"]), K, B._ptr(p["A"]), B._ptr(p["B"]),
-                                 B._ptr(p["scale"]), B._ptr(other), B._ptr(p["base"]), N,
-                                 B._ptr(y), N, 0, B._ptr(t), M, N, K, R, L, B._stream())
-    assert rc == B.SQ_OK
+    B.sq_lora_forward(p["x"], p["A"], p["B"], p["scale"], other, p["base"], y=y, t=t)
     assert B.sq_get_device_status() == B.SQ_ERR_INVALID_ARG
+    dA, dB, dx = (torch.full(s, 9.0, dtype=BF, device="cuda") for s in ((L, R, K), (L, N, R), (M, K)))
+    B.sq_lora_backward(p["dy"], p["x"], t, p["A"], p["B"], p["scale"], other, p["dx_base"], dx=dx,
+                       dA=dA, dB=dB)
+    assert B.sq_get_device_status() == B.SQ_ERR_INVALID_ARG
+    assert all((g == 9.0).all() for g in (dA, dB, dx))
     assert (y == 9.0).all() and (t == 9.0).all()
     assert B.sq_get_device_status() == B.SQ_OK

@@ -32,6 +32,10 @@ def test_lora_refusals(L):
     assert L.sq_lora_plan_bytes(-1, 2) == 0 and L.sq_lora_plan_bytes(8, 0) == 0
     assert L.sq_lora_plan_bytes(8, 1025) == 0 and L.sq_lora_plan_bytes(2 ** 24 + 1, 1) == 0
     assert L.sq_lora_plan_bytes(0, 1) > 0
+    need = L.sq_lora_workspace_bytes(4, 8, 2, 0)
+    assert need > 0 and L.sq_lora_workspace_bytes(4, 8, 2, 1) == 3 * need
+    for bad in ((4, 12, 2, 0), (4, 8, 0, 0), (4, 8, 2, 2), (-1, 8, 2, 0), (4, 136, 2, 0)):
+        assert L.sq_lora_workspace_bytes(*bad) == 0
     plan = dict(adapter=FAKE, M=4, L=2, plan=FAKE)
     for bad in (dict(adapter=None), dict(plan=None), dict(M=-1), dict(L=0), dict(L=1025)):
         assert _call(L.sq_lora_plan, plan, **bad) == INVALID, bad
@@ -54,13 +58,13 @@ def test_lora_refusals(L):
     assert _call(L.sq_lora_forward, fwd, M=0, x=None, y=None, base=None, t=None) == 0
 
     bwd = dict(dy=FAKE, lddy=72, x=FAKE, ldx=64, t=FAKE, A=FAKE, B=FAKE, scale=FAKE, plan=FAKE,
-               dx_base=FAKE, ldbase=64, dx=2 * FAKE, lddx=64, dA=FAKE, dB=FAKE, grads=0, dt=FAKE,
-               M=4, N=72, K=64, R=8, L=2)
-    for bad in (dict(dy=None), dict(x=None), dict(t=None), dict(dt=None), dict(dA=None),
+               dx_base=FAKE, ldbase=64, dx=2 * FAKE, lddx=64, dA=FAKE, dB=FAKE, grads=0,
+               workspace=FAKE, bytes=need, M=4, N=72, K=64, R=8, L=2)
+    for bad in (dict(dy=None), dict(x=None), dict(t=None), dict(workspace=None), dict(bytes=need - 1), dict(dA=None),
                 dict(dB=None), dict(dx=None), dict(grads=5), dict(lddy=64), dict(ldx=56),
                 dict(lddx=56), dict(ldbase=56), dict(dx_base=2 * FAKE, ldbase=72)):
         assert _call(L.sq_lora_backward, bwd, **bad) == INVALID, bad
-    for bad in (dict(dA=FAKE + 2), dict(dt=FAKE + 4), dict(dx=FAKE + 8), dict(lddy=76)):
+    for bad in (dict(dA=FAKE + 2), dict(workspace=FAKE + 4), dict(dx=FAKE + 8), dict(lddy=76)):
         assert _call(L.sq_lora_backward, bwd, **bad) == ALIGNMENT, bad
     # nothing asked for: nothing done, no device needed
     assert _call(L.sq_lora_backward, bwd, dx=None, dx_base=None, dA=None, dB=None) == 0

@@ -42,7 +42,8 @@ EXPORTED = ("sq_calibrate_act", "sq_quantize_act", "sq_quantize_weight_seg",
             "sq_dualscale_seglinear_gemm_ws", "sq_gemm_workspace_bytes", "sq_debug_gemm_s32_ws",
             "sq_debug_bounds_checks", "sq_debug_bounds_probe",
             "sq_quantize_act_plan", "sq_quantize_act_planned",
-            "sq_lora_plan_bytes", "sq_lora_plan", "sq_lora_forward", "sq_lora_backward",
+            "sq_lora_plan_bytes", "sq_lora_plan", "sq_lora_forward", "sq_lora_workspace_bytes",
+            "sq_lora_backward",
             "sq_rope_forward", "sq_rope_backward", "sq_rope_frequencies",
             "sq_group_norm_workspace_bytes", "sq_group_norm_forward", "sq_group_norm_backward",
             "sq_input_grad_workspace_bytes", "sq_dualscale_seglinear_input_grad")
@@ -156,8 +157,10 @@ def lib() -> ctypes.CDLL:
         L.sq_lora_plan.argtypes = [p, i64, i32, p, p]
         L.sq_lora_forward.argtypes = [p, i64, p, p, p, p, p, i64, p, i64, c_int, p, i64, i64, i64,
                                       i32, i32, p]
+        L.sq_lora_workspace_bytes.argtypes = [i64, i32, i32, c_int]
+        L.sq_lora_workspace_bytes.restype = size
         L.sq_lora_backward.argtypes = [p, i64, p, i64, p, p, p, p, p, p, i64, p, i64, p, p, c_int,
-                                       p, i64, i64, i64, i32, i32, p]
+                                       p, size, i64, i64, i64, i32, i32, p]
         for f in (L.sq_rope_forward, L.sq_rope_backward):
             f.argtypes = [p, i64, p, i64, c_int, p, p, p, i32, f32, i64, i32, i32, i32, c_int, p]
         L.sq_rope_frequencies.argtypes = [i32, dbl, c_int, dbl, dbl, dbl, dbl, p, p]
@@ -629,11 +632,16 @@ def sq_lora_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: to
     return y, t
 
 
+def sq_lora_workspace_bytes(M: int, R: int, n_adapters: int, grad_dtype=torch.bfloat16) -> int:
+    """Workspace bytes of sq_lora_backward (0: sizes out of range)."""
+    return lib().sq_lora_workspace_bytes(M, R, n_adapters, _out_dtype(grad_dtype, "grad_dtype"))
+
+
 def sq_lora_backward(dy: torch.Tensor, x: torch.Tensor, t: torch.Tensor, A: torch.Tensor,
                      B: torch.Tensor, scale: torch.Tensor, plan: torch.Tensor,
                      dx_base: Optional[torch.Tensor], dx: Optional[torch.Tensor] = None,
                      dA: Optional[torch.Tensor] = None, dB: Optional[torch.Tensor] = None,
-                     grad_dtype=torch.bfloat16, dt: Optional[torch.Tensor] = None,
+                     grad_dtype=torch.bfloat16, workspace: Optional[torch.Tensor] = None,
                      need_dx: bool = True, need_weights: bool = True):
     """Gradients of sq_lora_forward -> (dA, dB, dx): dA [L, R, K] and dB [L, N, R]
     of grad_dtype (bf16 or fp32; None without need_weights), dx = dx_base + the
@@ -657,22 +665,24 @@ def sq_lora_backward(dy: torch.Tensor, x: torch.Tensor, t: torch.Tensor, A: torc
             dB = torch.empty(L, N, R, dtype=grad_dtype, device=dev)
     elif dA is not None or dB is not None:
         raise ValueError("dA and dB are of no use without need_weights")
-    if dt is None:
-        dt = torch.empty(M, R, dtype=torch.float32, device=dev)
     out = _out_dtype(grad_dtype, "grad_dtype")
+    if workspace is None:
+        workspace = torch.empty(sq_lora_workspace_bytes(M, R, L, grad_dtype), dtype=torch.uint8,
+                                device=dev)
+    _need(workspace, torch.uint8, "workspace")
     _shape(x, torch.bfloat16, (M, K), "x", contiguous=False)
     _shape(t, torch.float32, (M, R), "t")
-    _shape(dt, torch.float32, (M, R), "dt")
     _shape(dx_base, torch.bfloat16, (M, K), "dx_base", contiguous=False)
     _shape(dx, torch.bfloat16, (M, K), "dx", contiguous=False)
     _shape(dA, grad_dtype, (L, R, K), "dA")
     _shape(dB, grad_dtype, (L, N, R), "dB")
-    _here(dev, x=x, t=t, A=A, dx_base=dx_base, dx=dx, dA=dA, dB=dB, dt=dt)
+    _here(dev, x=x, t=t, A=A, dx_base=dx_base, dx=dx, dA=dA, dB=dB,
+          workspace=workspace)
     _check(lib().sq_lora_backward(
         _ptr(dy), _ld(dy), _ptr(x), _ld(x), _ptr(t), _ptr(A), _ptr(B), _ptr(scale), _ptr(plan),
         _ptr(dx_base), 0 if dx_base is None else _ld(dx_base), _ptr(dx),
-        0 if dx is None else _ld(dx), _ptr(dA), _ptr(dB), out, _ptr(dt), M, N, K, R, L,
-        _stream()), "sq_lora_backward")
+        0 if dx is None else _ld(dx), _ptr(dA), _ptr(dB), out, _ptr(workspace),
+        workspace.numel(), M, N, K, R, L, _stream()), "sq_lora_backward")
     return dA, dB, dx
 
 

@@ -126,6 +126,19 @@ sq_status quantize_common(const void *x, int64_t M, int64_t K, int64_t ldx, cons
 
 }  // namespace
 
+int sm_count() {
+  static int count[kMaxDevices] = {};  // 0 unknown
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
+  if (count[dev] == 0) {
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+      sms = 148;
+    count[dev] = sms;
+  }
+  return count[dev];
+}
+
 // Current device must be sm_100 (the kernels are built for sm_100a only).
 sq_status check_device() {
   static int checked[kMaxDevices] = {};  // 0 unknown, 1 ok, -1 unsupported

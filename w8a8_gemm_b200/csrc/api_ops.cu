@@ -154,6 +154,13 @@ size_t sq_lora_plan_bytes(int64_t M, int32_t n_adapters) {
   return lora_sizes_ok(M, n_adapters) ? lora_plan_words(M, n_adapters) * sizeof(int32_t) : 0;
 }
 
+size_t sq_lora_workspace_bytes(int64_t M, int32_t R, int32_t n_adapters,
+                               sq_out_dtype grad_dtype) {
+  if (!lora_sizes_ok(M, n_adapters) || R < 8 || R > kMaxRank || R % 8 != 0) return 0;
+  if (grad_dtype != SQ_OUT_BF16 && grad_dtype != SQ_OUT_F32) return 0;
+  return lora_workspace_bytes(M, R, n_adapters, grad_dtype == SQ_OUT_F32);
+}
+
 sq_status sq_lora_plan(const int32_t *adapter, int64_t M, int32_t n_adapters, int32_t *plan,
                        sq_stream_t stream) {
   if (!lora_sizes_ok(M, n_adapters)) return SQ_ERR_INVALID_ARG;
@@ -202,9 +209,9 @@ sq_status sq_lora_forward(const void *x, int64_t ldx, const void *A, const void 
 sq_status sq_lora_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
                            const float *t, const void *A, const void *B, const float *scale,
                            const int32_t *plan, const void *dx_base, int64_t ldbase, void *dx,
-                           int64_t lddx, void *dA, void *dB, sq_out_dtype grad_dtype, float *dt,
-                           int64_t M, int64_t N, int64_t K, int32_t R, int32_t n_adapters,
-                           sq_stream_t stream) {
+                           int64_t lddx, void *dA, void *dB, sq_out_dtype grad_dtype,
+                           void *workspace, size_t workspace_bytes, int64_t M, int64_t N,
+                           int64_t K, int32_t R, int32_t n_adapters, sq_stream_t stream) {
   if (grad_dtype != SQ_OUT_BF16 && grad_dtype != SQ_OUT_F32) return SQ_ERR_INVALID_ARG;
   SQ_TRY(check_lora(M, N, K, R, n_adapters, A, B, scale, plan));
   SQ_TRY(check_rows(dy, M, N, lddy));
@@ -213,9 +220,12 @@ sq_status sq_lora_backward(const void *dy, int64_t lddy, const void *x, int64_t 
   if (dx == nullptr && dx_base != nullptr) return SQ_ERR_INVALID_ARG;
   if (dx != nullptr) SQ_TRY(check_rows(dx, M, K, lddx));
   if (dx_base != nullptr) SQ_TRY(check_rows(dx_base, M, K, ldbase));
-  if (M > 0 && (t == nullptr || dt == nullptr)) return SQ_ERR_INVALID_ARG;
+  const bool f32 = grad_dtype == SQ_OUT_F32;
+  if (M > 0 && (t == nullptr || workspace == nullptr ||
+                workspace_bytes < lora_workspace_bytes(M, R, n_adapters, f32)))
+    return SQ_ERR_INVALID_ARG;
   if (dx != nullptr && dx_base == dx && ldbase != lddx) return SQ_ERR_INVALID_ARG;
-  if (!aligned(t, 16) || !aligned(dt, 16) || !aligned(dA, 16) || !aligned(dB, 16))
+  if (!aligned(t, 16) || !aligned(workspace, 16) || !aligned(dA, 16) || !aligned(dB, 16))
     return SQ_ERR_ALIGNMENT;
   if (dA == nullptr && (dx == nullptr || M == 0)) return SQ_OK;
   LoraRequest q = {};
@@ -235,13 +245,13 @@ sq_status sq_lora_backward(const void *dy, int64_t lddy, const void *x, int64_t 
   q.dA = dA;
   q.dB = dB;
   q.t = const_cast<float *>(t);
-  q.dt = dt;
+  q.workspace = workspace;
   q.M = M;
   q.N = N;
   q.K = K;
   q.R = R;
   q.L = n_adapters;
-  q.f32 = grad_dtype == SQ_OUT_F32;
+  q.f32 = f32;
   return from_cuda(launch_lora_backward(q, cs(stream)));
 }
 

@@ -74,7 +74,6 @@ __global__ void __launch_bounds__(256) dequant_transpose_kernel(
 constexpr int BM = 128, BK = 64;
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s: far above any tile's latency
 
 template <int BN>
 struct GemmSmem {
@@ -95,17 +94,7 @@ struct GradArgs {
 
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
                                          int *status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    if (mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
-    if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
-      *abort_flag = 1;
-      atomicExch(status, static_cast<int>(SQ_ERR_DEVICE_TIMEOUT));
-      return false;
-    }
-  }
+  return bounded_wait(bar, parity, abort_flag, status, SQ_ERR_DEVICE_TIMEOUT);
 }
 
 template <int BN>
@@ -175,7 +164,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     producer_done:
       // never leave with a copy in flight into this block's shared memory
       for (int s = 0; s < STAGES; ++s)
-        if (armed & (1u << s)) mbar_wait(&full[s], (armed_parity >> s) & 1u, kWaitLimitNs);
+        if (armed & (1u << s)) mbar_wait(&full[s], (armed_parity >> s) & 1u, kBoundedWaitNs);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -206,7 +195,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
     mma_exit:
       mma_commit(mma_done);
-      mbar_wait(mma_done, 0, kWaitLimitNs);
+      mbar_wait(mma_done, 0, kBoundedWaitNs);
     }
   } else {
     const int quarter = warp & 3;         // TMEM lanes this warp may read
@@ -327,10 +316,7 @@ sq_status launch_input_grad(const InputGradRequest &r, cudaStream_t stream) {
                              256, 0, stream>>>(r.wq, r.s_w, r.d, r.N, r.K, r.seg, wt, ldw,
                                                r.status);
   if (cudaGetLastError() != cudaSuccess) return SQ_ERR_CUDA;
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (sms <= 0) sms = 148;
+  const int sms = sm_count();
   // The widest tile that still gives every SM one: a wide tile reads fewer
   // operand bytes per product, a narrow one spreads a small layer.
   const int64_t mt = (r.M + BM - 1) / BM;

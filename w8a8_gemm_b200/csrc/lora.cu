@@ -5,7 +5,7 @@
 //   dB[a] = c[a] sum_{m of a} dy[m] t[m]^T           dA[a] = sum_{m of a} dt[m] x[m]^T
 //
 // with a = adapter[m].  A plan, made once per batch, lists the rows adapter by
-// adapter and cuts them into tiles of at most 64 rows of one adapter, so that
+// adapter and cuts them into tiles of at most 128 rows of one adapter, so that
 // every tile is an ordinary pair of thin matrix products whatever the order of
 // the rows: scattered rows are gathered, single tokens of one adapter share a
 // tile, and the plan serves every layer that the batch goes through.
@@ -15,12 +15,12 @@
 //   expand    [rows] x R -> [rows] x [C] added to base: y and dx;
 //   outer     [rows] x [C], [rows] x R -> [C] x R: dB and dA.
 // All are bound by the rows' traffic (at rank 64 a row element that is read
-// and written, four bytes, meets 128 flop); the products run on the warp-level
-// matrix path, whose rate suffices up to rank 128.  Sums are fp32; the small
-// operand t (dt) is kept in fp32 and enters the second product as bf16 where
-// the result is rounded to bf16 anyway, or split into three bf16 terms (24
-// significant bits) where the result stays fp32.
+// and written, four bytes, meets 128 flop).  Sums are fp32; the small operand t
+// (dt) enters the second product as bf16 where the result is rounded to bf16
+// anyway, or split into three bf16 terms (24 significant bits) where the result
+// stays fp32.
 #include <cooperative_groups.h>
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -35,30 +35,24 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kTileRows = SQ_LORA_TILE_ROWS;
-constexpr int32_t kPlanMagic = 0x53514C31;
-constexpr int kThreads = 256;
+constexpr int32_t kPlanMagic = 0x53514C32;
 
 // ------------------------------------------------------------------- the plan
-// int32 words: [0] magic, [1] M, [2] L, [3] tiles, then bin_start[L + 2] (bin L
-// holds the rows without an adapter), perm[M] (rows, adapter by adapter, in
-// ascending order within one), tiles[max_tiles] of {bin, first place in perm}.
-struct PlanView {
-  const int32_t *head, *bin_start, *perm, *tiles;
-};
-__host__ __device__ inline int64_t plan_perm_at(int32_t L) { return 4 + (L + 2); }
-__host__ __device__ inline int64_t plan_tiles_at(int64_t M, int32_t L) {
-  return plan_perm_at(L) + M;
-}
+// int32 words: [0] magic, [1] M, [2] L, [3] tiles, tile_at[L + 2] (the first tile
+// of each bin; bin L holds the rows without an adapter), padding to a multiple
+// of four, then a record per tile: {bin, rows, first place in the order by
+// adapter, 0, row numbers[128]}.  A kernel finds everything about its tile at
+// one address; row numbers past the tile's rows repeat its first.
+constexpr int kRecWords = 4 + kTileRows;
+__host__ __device__ inline int64_t plan_recs_at(int32_t L) { return (4 + (L + 2) + 3) / 4 * 4; }
 __host__ __device__ inline int64_t plan_max_tiles(int64_t M, int32_t L) {
   return M / kTileRows + (M < L + 1 ? M : L + 1);
 }
-__device__ __forceinline__ PlanView plan_view(const int32_t *plan, int64_t M, int32_t L) {
-  return {plan, plan + 4, plan + plan_perm_at(L), plan + plan_tiles_at(M, L)};
-}
 // A plan of another batch size or adapter count: reported, nothing computed.
-__device__ __forceinline__ bool plan_fits(const PlanView &v, int64_t M, int32_t L, int *status) {
-  const bool ok = v.head[0] == kPlanMagic && v.head[1] == static_cast<int32_t>(M) &&
-                  v.head[2] == L;
+__device__ __forceinline__ bool plan_fits(const int32_t *plan, int64_t M, int32_t L,
+                                          int *status) {
+  const int4 h = *reinterpret_cast<const int4 *>(plan);
+  const bool ok = h.x == kPlanMagic && h.y == static_cast<int32_t>(M) && h.z == L;
   if (!ok && threadIdx.x == 0) atomicCAS(status, 0, static_cast<int>(SQ_ERR_INVALID_ARG));
   return ok;
 }
@@ -128,21 +122,23 @@ __global__ void __launch_bounds__(kPlanWarps * 32) lora_plan_kernel(
   __syncthreads();
   if (threadIdx.x < 4) {
     const int32_t v[4] = {kPlanMagic, M, L, tile_at[bins]};
-    if (store_ok(status, threadIdx.x < plan_perm_at(L))) plan[threadIdx.x] = v[threadIdx.x];
+    if (store_ok(status, threadIdx.x < plan_recs_at(L))) plan[threadIdx.x] = v[threadIdx.x];
   }
   for (int b = threadIdx.x; b <= bins; b += blockDim.x)
-    if (store_ok(status, 4 + b < plan_perm_at(L))) plan[4 + b] = start[b];
-  int32_t *tiles = plan + plan_tiles_at(M, L);
+    if (store_ok(status, 4 + b < plan_recs_at(L))) plan[4 + b] = tile_at[b];
+  int32_t *recs = plan + plan_recs_at(L);
   const int64_t max_tiles = plan_max_tiles(M, L);
   for (int b = warp; b < bins; b += kPlanWarps)
     for (int i = lane; i < tile_at[b + 1] - tile_at[b]; i += 32) {
       const int64_t at = tile_at[b] + i;
       if (!store_ok(status, at < max_tiles)) continue;
-      tiles[2 * at] = b;
-      tiles[2 * at + 1] = start[b] + i * kTileRows;
+      const int first = start[b] + i * kTileRows, left = start[b + 1] - first;
+      recs[at * kRecWords] = b;
+      recs[at * kRecWords + 1] = left < kTileRows ? left : kTileRows;
+      recs[at * kRecWords + 2] = first;
+      recs[at * kRecWords + 3] = 0;
     }
   // places: 32 rows a step in order; equal bins of a step rank by lane
-  int32_t *perm = plan + plan_perm_at(L);
   for (int64_t r0 = lo; r0 < hi; r0 += 32) {
     const int64_t r = r0 + lane;
     const bool in = r < hi;
@@ -151,8 +147,17 @@ __global__ void __launch_bounds__(kPlanWarps * 32) lora_plan_kernel(
     const unsigned same = __match_any_sync(~0u, b);
     const int rank = __popc(same & ((1u << lane) - 1));
     if (in) {
-      const int64_t at = start[b] + mine[b] + rank;
-      if (store_ok(status, at >= 0 && at < M)) perm[at] = static_cast<int32_t>(r);
+      const int place = mine[b] + rank;  // within the bin
+      const int64_t at = tile_at[b] + place / kTileRows;
+      if (store_ok(status, at < max_tiles)) {
+        int32_t *rows = recs + at * kRecWords + 4;
+        rows[place % kTileRows] = static_cast<int32_t>(r);
+        // the tile's first row also fills the places past its last
+        if (place % kTileRows == 0) {
+          const int left = start[b + 1] - start[b] - place;
+          for (int i = left; i < kTileRows; ++i) rows[i] = static_cast<int32_t>(r);
+        }
+      }
     }
     __syncwarp();
     if (in && rank == 0) mine[b] += __popc(same);
@@ -161,195 +166,256 @@ __global__ void __launch_bounds__(kPlanWarps * 32) lora_plan_kernel(
 }
 
 // ----------------------------------------------------------------- shared parts
-// A tile's rows: bin, first place, count; false past the last tile.
-struct Tile {
-  int bin, start, count;
-};
-__device__ __forceinline__ bool get_tile(const PlanView &v, int i, Tile &t) {
-  if (i >= v.head[3]) return false;
-  t.bin = v.tiles[2 * i];
-  t.start = v.tiles[2 * i + 1];
-  const int left = v.bin_start[t.bin + 1] - t.start;
-  t.count = left < kTileRows ? left : kTileRows;
-  return true;
-}
-
-// Byte offset of 16-byte chunk c of row r in a tile of 128-byte rows, chunks
-// exchanged within groups of eight rows so that ldmatrix meets no bank twice.
-__device__ __forceinline__ uint32_t swz(int r, int c) {
-  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+// v as TERMS bf16 values whose sum has 8 TERMS significant bits, packed in pairs.
+template <int TERMS>
+__device__ __forceinline__ void split_terms(float4 v, uint2 (&out)[TERMS]) {
+#pragma unroll
+  for (int s = 0; s < TERMS; ++s) {
+    const uint32_t lo = bf16x2(v.x, v.y), hi = bf16x2(v.z, v.w);
+    out[s] = make_uint2(lo, hi);
+    v = make_float4(v.x - bf16_lo(lo), v.y - bf16_hi(lo), v.z - bf16_lo(hi), v.w - bf16_hi(hi));
+  }
 }
 
 // ------------------------------------------------------------------- contract
 // out[m][j] = f sum_c in[m][c] W(j, c), f = scale[a] or 1; W(j, c) = w[a][j][c]
-// (TRANS false: A) or w[a][c][j] (TRANS true: B).  One block per row tile and
-// slice of the contracted dimension; the blocks of a cluster hold the slices
-// of one tile and add their partial sums through distributed shared memory in
-// a fixed order.
+// (TRANS false: A) or w[a][c][j] (TRANS true: B, an operand whose rows run
+// along the contraction).  One block per row tile and slice of the contracted
+// dimension: TMA gathers the tile's rows by number, 64 columns a stage, and
+// brings the weight's box beside them; one thread issues tcgen05.mma (M = 128,
+// N = RT, sums in tensor memory), so that reading the rows costs the SM no
+// instructions.  The blocks of a cluster hold the slices of one tile and add
+// their partial sums through distributed shared memory in a fixed order.  The
+// forward pass stores t by row in fp32; the backward pass stores dt, and beside
+// it t, as bf16 terms by tile, 128 rows each with zeros past the tile's last:
+// the operand that the outer products and dx read.
 struct ContractArgs {
-  const uint16_t *in;
-  int64_t ld;
-  const uint16_t *w;
   const float *scale;  // nullptr: 1
   const int32_t *plan;
-  float *out;
-  int64_t M;
+  float *out;             // forward: t [M][R]
+  const float *t;         // backward: t [M][R]
+  uint16_t *vt, *vdt;     // backward: [TERMS][max_tiles][128][R]
+  int64_t M, max_tiles;
   int32_t C, R, L;
   int *status;
 };
 
-template <int RT, bool TRANS>
+constexpr int kContractThreads = 128;
+
+template <int RT>
 struct ContractSmem {
-  static constexpr int kStages = 4;
+  static constexpr int kStages = RT == 64 ? 4 : 3;
   static constexpr int kIn = kTileRows * 128;
-  static constexpr int kWRow = TRANS ? RT * 2 + 16 : 128;
-  static constexpr int kW = TRANS ? 64 * kWRow : RT * 128;
+  static constexpr int kW = RT * 128;  // both orders: 64 columns by RT
   static constexpr int kStage = kIn + kW;
-  static constexpr int kRows = kStages * kStage;  // then the tile's row numbers
-  static constexpr int kBytes = kRows + kTileRows * 4;
-  static_assert(kTileRows * (RT + 1) * 4 <= kRows, "partial sums reuse the stages");
+  static constexpr int kBars = kStages * kStage;
+  static constexpr int kBytes = kBars + (2 * kStages + 1) * 8 + 16 + 1024;
+  static constexpr int kPartRow = RT + 4;  // floats
+  static_assert(kTileRows * kPartRow * 4 <= kBars, "partial sums reuse the stages");
 };
 
-template <int RT, bool TRANS>
-__global__ void __launch_bounds__(kThreads) lora_contract_kernel(const ContractArgs p) {
-  using S = ContractSmem<RT, TRANS>;
-  extern __shared__ __align__(128) uint8_t smem[];
+// TERMS 0: the forward pass.
+template <int RT, bool TRANS, int TERMS>
+__global__ void __launch_bounds__(kContractThreads)
+    lora_contract_kernel(const __grid_constant__ CUtensorMap tm_in,
+                         const __grid_constant__ CUtensorMap tm_w, const ContractArgs p) {
+  using S = ContractSmem<RT>;
+  constexpr int STAGES = S::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kBars);
+  uint64_t *empty = full + STAGES;
+  uint64_t *done = empty + STAGES;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   cg::cluster_group cluster = cg::this_cluster();
   const int slices = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
-  const PlanView plan = plan_view(p.plan, p.M, p.L);
-  if (!plan_fits(plan, p.M, p.L, p.status)) return;
-  Tile t;
-  if (!get_tile(plan, blockIdx.x, t) || t.bin >= p.L) return;  // the whole cluster returns
-
-  int32_t *rows = reinterpret_cast<int32_t *>(smem + S::kRows);
-  for (int i = threadIdx.x; i < kTileRows; i += kThreads)
-    rows[i] = plan.perm[t.start + (i < t.count ? i : 0)];
-  __syncthreads();
-
-  const int C = p.C;
-  const int slice = ((C + slices - 1) / slices + 63) / 64 * 64;
-  const int c_lo = rank * slice;
-  const int c_hi = c_lo + slice < C ? c_lo + slice : C;
-  const int steps = c_hi > c_lo ? (c_hi - c_lo + 63) / 64 : 0;
-  const uint16_t *w = p.w + static_cast<int64_t>(t.bin) * p.R * C;
-  const uint32_t base = smem_u32(smem);
-
-  auto load = [&](int step) {
-    const uint32_t st = base + (step % S::kStages) * S::kStage;
-    const int c0 = c_lo + step * 64;
-    for (int i = threadIdx.x; i < kTileRows * 8; i += kThreads) {
-      const int r = i >> 3, c = i & 7;
-      const int col = c0 + c * 8;
-      const bool ok = r < t.count && col < c_hi;
-      cp_async16(st + swz(r, c), p.in + rows[r] * p.ld + (ok ? col : 0), ok);
-    }
-    const uint32_t sw = st + S::kIn;
-    if constexpr (!TRANS) {
-      for (int i = threadIdx.x; i < RT * 8; i += kThreads) {
-        const int r = i >> 3, c = i & 7;
-        const int col = c0 + c * 8;
-        const bool ok = r < p.R && col < c_hi;
-        cp_async16(sw + swz(r, c), ok ? w + static_cast<int64_t>(r) * C + col : w, ok);
-      }
-    } else {
-      for (int i = threadIdx.x; i < 64 * (RT / 8); i += kThreads) {
-        const int r = i / (RT / 8), c = i % (RT / 8);
-        const int row = c0 + r;
-        const bool ok = row < c_hi && c * 8 < p.R;
-        cp_async16(sw + r * S::kWRow + c * 16,
-                   ok ? w + static_cast<int64_t>(row) * p.R + c * 8 : w, ok);
-      }
-    }
-  };
-
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wm = warp & 3, wn = warp >> 2;
-  constexpr int NT = RT / 16;  // n tiles of 8 columns per warp (half of RT)
-  float acc[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
 
-#pragma unroll
-  for (int s = 0; s < S::kStages - 1; ++s) {
-    if (s < steps) load(s);
-    cp_async_commit();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tm_in);
+    prefetch_tmap(&tm_w);
   }
-  for (int step = 0; step < steps; ++step) {
-    cp_async_wait<S::kStages - 2>();
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, RT);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
+  grid_dependency_launch();
+
+  // A fitting plan has a record for every block of the grid; the blocks of a
+  // cluster share their tile and so their way through this kernel.
+  int4 tile = make_int4(p.L, 0, 0, 0);
+  const int32_t *rec = p.plan + plan_recs_at(p.L) + static_cast<int64_t>(blockIdx.x) * kRecWords;
+  if (plan_fits(p.plan, p.M, p.L, p.status) && static_cast<int>(blockIdx.x) < p.plan[3])
+    tile = *reinterpret_cast<const int4 *>(rec);
+  const int bin = tile.x, count = tile.y;
+  if (bin < p.L) {
+    const int slice = ((p.C + slices - 1) / slices + 63) / 64 * 64;
+    const int c_lo = rank * slice;
+    const int c_hi = c_lo + slice < p.C ? c_lo + slice : p.C;
+    const int steps = c_hi > c_lo ? (c_hi - c_lo + 63) / 64 : 0;
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      // Lane l brings rows 4 l .. 4 l + 3; groups past the tile's last row are
+      // left out (what stands there only meets sums that are not stored).
+      const bool brings = 4 * lane < count;
+      const int4 rows = *reinterpret_cast<const int4 *>(rec + 4 + 4 * lane);
+      const uint32_t bytes = (count + 3) / 4 * 512 + S::kW;
+      uint32_t armed = 0, armed_parity = 0;
+      for (int step = 0; step < steps; ++step) {
+        const int st = step % STAGES;
+        const uint32_t phase = (step / STAGES) & 1;
+        bool ok = true;
+        uint8_t *in = smem + st * S::kStage;
+        const int c0 = c_lo + step * 64;
+        if (lane == 0) {
+          ok = bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
+          if (ok) {
+            mbar_arrive_expect_tx(&full[st], bytes);
+            if constexpr (!TRANS) {
+              tma_load_3d(in + S::kIn, &tm_w, &full[st], c0, 0, bin);
+            } else {
+#pragma unroll
+              for (int h = 0; h < RT / 64; ++h)
+                tma_load_3d(in + S::kIn + h * 8192, &tm_w, &full[st], h * 64, c0, bin);
+            }
+            armed |= 1u << st;
+            armed_parity = (armed_parity & ~(1u << st)) | (phase << st);
+          }
+        }
+        if (!__shfl_sync(~0u, ok, 0)) break;
+        if (brings) tma_gather4(in + lane * 512, &tm_in, &full[st], c0, rows);
+        __syncwarp();
+      }
+      // never leave with a copy in flight into this block's shared memory
+      if (lane == 0)
+        for (int s = 0; s < STAGES; ++s)
+          if (armed & (1u << s)) mbar_wait(&full[s], (armed_parity >> s) & 1u, kBoundedWaitNs);
+      __syncwarp();
+    } else if (warp == 1) {
+      // -------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t idesc = idesc_bf16(kTileRows, RT) | (TRANS ? kIdescTransB : 0u);
+        for (int step = 0; step < steps; ++step) {
+          const int st = step % STAGES;
+          if (!bounded_wait(&full[st], (step / STAGES) & 1, abort_flag, p.status,
+                            SQ_ERR_DEVICE_TIMEOUT))
+            break;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + st * S::kStage), sb = sa + S::kIn;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_tc(tmem, sdesc_kmajor_sw128(sa + kk * 32),
+                        TRANS ? sdesc_mnmajor_sw128(sb + kk * 2048, 8192)
+                              : sdesc_kmajor_sw128(sb + kk * 32),
+                        idesc, (step | kk) != 0);
+          mma_commit(&empty[st]);
+        }
+        mma_commit(done);
+      }
+      __syncwarp();
+    }
+    const bool ok = bounded_wait(done, 0, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
+    tc_fence_after();
+    // nothing reads or fills the stages any more
     __syncthreads();
-    if (step + S::kStages - 1 < steps) load(step + S::kStages - 1);
-    cp_async_commit();
-    if (wm * 16 >= t.count) continue;  // no rows in this warp's part
-    const uint32_t si = base + (step % S::kStages) * S::kStage;
-    const uint32_t sw = si + S::kIn;
+
+    // partial sums -> shared memory -> sum over the slices
+    float *part = reinterpret_cast<float *>(smem);
+    constexpr int PS = S::kPartRow;
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      uint32_t a[4];
-      ldsm_x4(si + swz(wm * 16 + (lane & 15), kk * 2 + (lane >> 4)), a);
-      if constexpr (NT == 1) {
-        uint32_t b0, b1;
-        if constexpr (!TRANS)
-          ldsm_x2(sw + swz(wn * 8 + (lane & 7), kk * 2 + ((lane >> 3) & 1)), b0, b1);
-        else
-          ldsm_x2_t(sw + (kk * 16 + (lane & 15)) * S::kWRow + wn * 16, b0, b1);
-        mma_bf16(acc[0], a, b0, b1);
+    for (int c = 0; c < RT; c += 32) {
+      uint32_t r[32];
+      __syncwarp();
+      tmem_ld_32x32b_x32(tmem + c + (static_cast<uint32_t>(warp * 32) << 16), r);
+      tmem_ld_wait();
+      float *to = part + threadIdx.x * PS + c;
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<uint4 *>(to + j) =
+            steps > 0 ? make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]) : make_uint4(0, 0, 0, 0);
+    }
+    if (slices > 1) cluster.sync(); else __syncthreads();
+    const float f = p.scale ? p.scale[bin] : 1.0f;
+    const int quads = p.R / 4;
+    const int total = ok ? (TERMS > 0 ? kTileRows : count) * quads : 0;
+    for (int e = rank * kContractThreads + threadIdx.x; e < total;
+         e += slices * kContractThreads) {
+      const int r = e / quads, j = (e - r * quads) * 4;
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (TERMS == 0 || r < count) {
+        for (int q = 0; q < slices; ++q) {
+          const float *src = slices > 1 ? cluster.map_shared_rank(part, q) : part;
+          const float4 v = *reinterpret_cast<const float4 *>(src + r * PS + j);
+          s.x += v.x;
+          s.y += v.y;
+          s.z += v.z;
+          s.w += v.w;
+        }
+        s = make_float4(f * s.x, f * s.y, f * s.z, f * s.w);
+      }
+      const int row = rec[4 + r];
+      const int64_t at = static_cast<int64_t>(row) * p.R + j;
+      if constexpr (TERMS == 0) {
+        if (store_ok(p.status, row >= 0 && row < p.M))
+          *reinterpret_cast<float4 *>(p.out + at) = s;
       } else {
+        const int64_t place = static_cast<int64_t>(blockIdx.x) * kTileRows + r;
+        if (!store_ok(p.status, place < p.max_tiles * kTileRows)) continue;
+        float4 tv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r < count) tv = *reinterpret_cast<const float4 *>(p.t + at);
+        uint2 d[TERMS], t[TERMS];
+        split_terms<TERMS>(s, d);
+        split_terms<TERMS>(tv, t);
 #pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-          uint32_t b[4];
-          const int col = wn * (RT / 2) + n * 8;
-          if constexpr (!TRANS)
-            ldsm_x4(sw + swz(col + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)),
-                    b);
-          else
-            ldsm_x4_t(sw + (kk * 16 + (lane & 15)) * S::kWRow + (col + (lane >> 4) * 8) * 2, b);
-          mma_bf16(acc[n], a, b[0], b[1]);
-          mma_bf16(acc[n + 1], a, b[2], b[3]);
+        for (int q = 0; q < TERMS; ++q) {
+          const int64_t to = (q * p.max_tiles * kTileRows + place) * p.R + j;
+          *reinterpret_cast<uint2 *>(p.vdt + to) = d[q];
+          *reinterpret_cast<uint2 *>(p.vt + to) = t[q];
         }
       }
     }
+    if (slices > 1) cluster.sync();  // no block leaves while its sums are read
   }
-  cp_async_wait<0>();
-  __syncthreads();
 
-  // partial sums -> shared memory [64][RT + 1] -> sum over the slices
-  float *part = reinterpret_cast<float *>(smem);
-  constexpr int PS = RT + 1;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int col = wn * (RT / 2) + n * 8 + (lane & 3) * 2;
-    const int row = wm * 16 + (lane >> 2);
-    part[row * PS + col] = acc[n][0];
-    part[row * PS + col + 1] = acc[n][1];
-    part[(row + 8) * PS + col] = acc[n][2];
-    part[(row + 8) * PS + col + 1] = acc[n][3];
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, RT);
   }
-  if (slices > 1) cluster.sync(); else __syncthreads();
-  const float f = p.scale ? p.scale[t.bin] : 1.0f;
-  const int total = t.count * p.R;
-  for (int e = rank * kThreads + threadIdx.x; e < total; e += slices * kThreads) {
-    const int r = e / p.R, j = e - r * p.R;
-    float s = 0.0f;
-    for (int q = 0; q < slices; ++q) {
-      const float *src = slices > 1 ? cluster.map_shared_rank(part, q) : part;
-      s += src[r * PS + j];
-    }
-    const int64_t at = static_cast<int64_t>(rows[r]) * p.R + j;
-    if (store_ok(p.status, rows[r] >= 0 && rows[r] < p.M && j < p.R)) p.out[at] = f * s;
-  }
-  if (slices > 1) cluster.sync();  // no block leaves while its sums are read
 }
 
 // --------------------------------------------------------------------- expand
 // out[m][c] = base[m][c] + f sum_j t[m][j] W(j, c); W(j, c) = w[a][c][j] (TRANS
-// false: B) or w[a][j][c] (TRANS true: A).  One block per row tile and 128
-// output columns.  Rows without an adapter are copied from base (left alone
-// when out is base).
+// false: B, t fp32 by row) or w[a][j][c] (TRANS true: A, t bf16 by tile).
+// Persistent blocks, one per SM, take equal shares of the units (row tile, slab
+// of 128 columns), neighbouring slabs of a tile in a row, so that t is loaded
+// once for many slabs.  Base goes from memory into registers one unit ahead and
+// the result from registers to memory, 16 bytes a thread: the columns of a slab
+// are dealt to the product's columns so that the eight that a thread holds of a
+// row in four accumulator tiles are neighbours.  Column 32 b + 8 c + 2 j + e is
+// column 2 c + e of tile 4 b + j; the weight slab is permuted accordingly on
+// its way into shared memory.  Rows without an adapter are copied from base
+// (left alone when out is base).
 struct ExpandArgs {
-  const float *t;
+  const float *t;      // TRANS false: [M][R]
+  const uint16_t *vt;  // TRANS true: [max_tiles][128][R]
   const uint16_t *w;
   const float *scale;  // nullptr: 1
   const int32_t *plan;
@@ -362,6 +428,7 @@ struct ExpandArgs {
   int *status;
 };
 
+constexpr int kExpandThreads = 512;
 constexpr int kSlab = 128;
 
 template <int RT, bool TRANS, bool F32>
@@ -371,157 +438,248 @@ struct ExpandSmem {
   static constexpr int kT = kTerms * kTileRows * kTRow;
   static constexpr int kWRow = TRANS ? kSlab * 2 + 16 : RT * 2 + 16;
   static constexpr int kW = TRANS ? RT * kWRow : kSlab * kWRow;
-  static constexpr int kElem = F32 ? 4 : 2;
-  static constexpr int kORow = kSlab * kElem + 16;
-  static constexpr int kOut = kTileRows * kORow;
-  static constexpr int kRows = kT + kW + kOut;
-  static constexpr int kBytes = kRows + kTileRows * 4;
+  static constexpr int kStages = 3;
+  static constexpr int kBytes = kT + kStages * kW;
+  static_assert(kBytes <= 232448, "dynamic shared memory above the per-block limit");
 };
 
 template <int RT, bool TRANS, bool F32>
-__global__ void __launch_bounds__(kThreads) lora_expand_kernel(const ExpandArgs p) {
+__global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const ExpandArgs p) {
   using S = ExpandSmem<RT, TRANS, F32>;
+  constexpr int E = F32 ? 4 : 2;
+  constexpr int Q = F32 ? 2 : 1;     // 16-byte pieces of eight columns
+  constexpr int KK = RT / 16;
   extern __shared__ __align__(128) uint8_t smem[];
-  const PlanView plan = plan_view(p.plan, p.M, p.L);
-  if (!plan_fits(plan, p.M, p.L, p.status)) return;
-  const unsigned slabs = (static_cast<unsigned>(p.C) + kSlab - 1) / kSlab;
-  Tile t;
-  if (!get_tile(plan, static_cast<int>(blockIdx.x / slabs), t)) return;
-  const bool none = t.bin >= p.L;
-  if (none && p.base == p.out) return;
+  const uint32_t sm = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int wm = warp & 7, wn = warp >> 3;  // 16 rows, 64 columns
+  const int g = lane >> 2, c8 = (lane & 3) * 8;
 
-  constexpr int E = S::kElem;
-  constexpr int VE = 16 / E;            // elements of a 16-byte chunk
-  constexpr int CH = kSlab / VE;        // chunks of a row
-  uint8_t *st = smem, *sw = smem + S::kT, *so = smem + S::kT + S::kW;
-  int32_t *rows = reinterpret_cast<int32_t *>(smem + S::kRows);
-  for (int i = threadIdx.x; i < kTileRows; i += kThreads)
-    rows[i] = plan.perm[t.start + (i < t.count ? i : 0)];
-  __syncthreads();
-  const int c0 = static_cast<int>(blockIdx.x % slabs) * kSlab;
+  // base, weights and plan were complete before the kernel ahead of this one
+  // began; only its own output, t, has to be waited for
+  const int32_t *recs = p.plan + plan_recs_at(p.L);
+  const int slabs = (p.C + kSlab - 1) / kSlab;
+  const bool fits = plan_fits(p.plan, p.M, p.L, p.status);
+  const int64_t units = fits ? static_cast<int64_t>(p.plan[3]) * slabs : 0;
+  const int64_t u_lo = units * blockIdx.x / gridDim.x;
+  const int mine = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x - u_lo);
+  const bool in_place = p.base == p.out;
 
-  // base tile and weight slab, asynchronously
-  for (int i = threadIdx.x; i < kTileRows * CH; i += kThreads) {
-    const int r = i / CH, c = i % CH;
-    const bool ok = p.base != nullptr && r < t.count && c0 + c * VE < p.C;
-    const uint8_t *src = static_cast<const uint8_t *>(p.base) +
-                         (rows[r] * p.ld_base + (ok ? c0 + c * VE : 0)) * E;
-    cp_async16(smem_u32(so + r * S::kORow + c * 16), ok ? src : static_cast<const void *>(p.t), ok);
-  }
-  if (!none) {
-    const uint16_t *w = p.w + static_cast<int64_t>(t.bin) * p.R * p.C;
-    if constexpr (!TRANS) {
-      for (int i = threadIdx.x; i < kSlab * (RT / 8); i += kThreads) {
-        const int r = i / (RT / 8), c = i % (RT / 8);
-        const bool ok = c0 + r < p.C && c * 8 < p.R;
-        cp_async16(smem_u32(sw + r * S::kWRow + c * 16),
-                   ok ? w + static_cast<int64_t>(c0 + r) * p.R + c * 8 : w, ok);
-      }
-    } else {
-      for (int i = threadIdx.x; i < RT * (kSlab / 8); i += kThreads) {
-        const int r = i / (kSlab / 8), c = i % (kSlab / 8);
-        const bool ok = r < p.R && c0 + c * 8 < p.C;
-        cp_async16(smem_u32(sw + r * S::kWRow + c * 16),
-                   ok ? w + static_cast<int64_t>(r) * p.C + c0 + c * 8 : w, ok);
-      }
-    }
-    // t rows -> bf16 terms
-    for (int i = threadIdx.x; i < kTileRows * (RT / 4); i += kThreads) {
-      const int r = i / (RT / 4), c = i % (RT / 4);
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (r < t.count && c * 4 < p.R)
-        v = *reinterpret_cast<const float4 *>(p.t + static_cast<int64_t>(rows[r]) * p.R + c * 4);
+  // weights of a unit -> its stage
+  int w_tile = static_cast<int>(u_lo / slabs), w_slab = static_cast<int>(u_lo % slabs);
+  const int tile0 = w_tile, slab0 = w_slab;
+  int w_bin = mine > 0 ? recs[static_cast<int64_t>(w_tile) * kRecWords] : 0;
+  auto load_w = [&](int stage) {
+    if (w_bin < p.L) {
+      const uint16_t *w = p.w + static_cast<int64_t>(w_bin) * p.R * p.C;
+      const uint32_t sw = sm + S::kT + stage * S::kW;
+      const int c0 = w_slab * kSlab;
+      if constexpr (!TRANS) {
+        constexpr int PER = RT / 8;
 #pragma unroll
-      for (int s = 0; s < S::kTerms; ++s) {
-        const uint32_t lo = bf16x2(v.x, v.y), hi = bf16x2(v.z, v.w);
-        *reinterpret_cast<uint2 *>(st + s * kTileRows * S::kTRow + r * S::kTRow + c * 8) =
-            make_uint2(lo, hi);
-        v = make_float4(v.x - bf16_lo(lo), v.y - bf16_hi(lo), v.z - bf16_lo(hi),
-                        v.w - bf16_hi(hi));
+        for (int k = tid; k < kSlab * PER; k += kExpandThreads) {
+          const int r = k / PER, cc = k % PER;
+          const int at = (r & ~31) | (((r >> 1) & 3) << 3) | (((r >> 3) & 3) << 1) | (r & 1);
+          const bool ok = c0 + r < p.C && cc * 8 < p.R;
+          cp_async16(sw + at * S::kWRow + cc * 16,
+                     ok ? w + static_cast<int64_t>(c0 + r) * p.R + cc * 8 : w, ok);
+        }
+      } else {
+        constexpr int PER = kSlab / 2;  // pairs of columns
+#pragma unroll 8
+        for (int k = tid; k < RT * PER; k += kExpandThreads) {
+          const int r = k / PER, cc = k % PER;
+          const int at = (cc & ~15) | ((cc & 3) << 2) | ((cc >> 2) & 3);
+          const bool ok = r < p.R && c0 + cc * 2 < p.C;
+          cp_async4(sw + r * S::kWRow + at * 4,
+                    ok ? w + static_cast<int64_t>(r) * p.C + c0 + cc * 2 : w, ok);
+        }
       }
     }
-  }
-  cp_async_commit();
-  cp_async_wait<0>();
-  __syncthreads();
+    if (++w_slab == slabs) {
+      w_slab = 0;
+      ++w_tile;
+      if (w_tile < p.plan[3]) w_bin = recs[static_cast<int64_t>(w_tile) * kRecWords];
+    }
+  };
 
-  if (!none) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int wm = warp & 3, wn = warp >> 2;
-    if (wm * 16 < t.count) {
+  // base of a unit -> registers: this thread's rows wm 16 + g (+ 8), columns
+  // wn 64 + 32 b + c8 .. + 7
+  int b_tile = tile0, b_slab = slab0, b_count = 0;
+  int32_t b_row[2] = {0, 0};
+  auto base_rows = [&]() {
+    const int32_t *rec = recs + static_cast<int64_t>(b_tile) * kRecWords;
+    b_count = rec[1];
+    b_row[0] = rec[4 + wm * 16 + g];
+    b_row[1] = rec[4 + wm * 16 + g + 8];
+  };
+  uint4 next[2][2][Q];
+  auto load_base = [&]() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int col = b_slab * kSlab + wn * 64 + b * 32 + c8;
+        const bool ok = p.base != nullptr && wm * 16 + g + h * 8 < b_count && col < p.C;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            static_cast<const uint8_t *>(p.base) + (b_row[h] * p.ld_base + col) * E);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) next[h][b][q] = ok ? src[q] : make_uint4(0, 0, 0, 0);
+      }
+    if (++b_slab == slabs) {
+      b_slab = 0;
+      ++b_tile;
+      if (b_tile < p.plan[3]) base_rows();
+    }
+  };
+
+  if (mine > 0) base_rows();
+#pragma unroll
+  for (int s = 0; s < S::kStages - 1; ++s) {
+    if (s < mine) load_w(s);
+    cp_async_commit();
+  }
+  if (mine > 0) load_base();
+  grid_dependency_wait();
+
+  int tile = tile0, slab = slab0, bin = 0, count = 0;
+  int32_t row[2] = {0, 0};
+  float f = 1.0f;
+  bool fresh = true;
+  for (int i = 0; i < mine; ++i) {
+    if (fresh) {
+      const int32_t *rec = recs + static_cast<int64_t>(tile) * kRecWords;
+      bin = rec[0];
+      count = rec[1];
+      row[0] = rec[4 + wm * 16 + g];
+      row[1] = rec[4 + wm * 16 + g + 8];
+      if (i > 0) __syncthreads();  // the last tile's t is no longer read
+      if (bin < p.L) {
+        f = p.scale ? p.scale[bin] : 1.0f;
+        if constexpr (TRANS) {
+          for (int k = tid; k < kTileRows * (RT / 8); k += kExpandThreads) {
+            const int r = k / (RT / 8), cc = k % (RT / 8);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (cc * 8 < p.R)
+              v = *reinterpret_cast<const uint4 *>(
+                  p.vt + (static_cast<int64_t>(tile) * kTileRows + r) * p.R + cc * 8);
+            *reinterpret_cast<uint4 *>(smem + r * S::kTRow + cc * 16) = v;
+          }
+        } else {
+          for (int k = tid; k < kTileRows * (RT / 4); k += kExpandThreads) {
+            const int r = k / (RT / 4), cc = k % (RT / 4);
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (r < count && cc * 4 < p.R)
+              v = *reinterpret_cast<const float4 *>(
+                  p.t + static_cast<int64_t>(rec[4 + r]) * p.R + cc * 4);
+            uint2 o[S::kTerms];
+            split_terms<S::kTerms>(v, o);
+#pragma unroll
+            for (int s = 0; s < S::kTerms; ++s)
+              *reinterpret_cast<uint2 *>(smem + (s * kTileRows + r) * S::kTRow + cc * 8) = o[s];
+          }
+        }
+      }
+    }
+    uint4 now[2][2][Q];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int q = 0; q < Q; ++q) now[h][b][q] = next[h][b][q];
+    cp_async_wait<S::kStages - 2>();
+    __syncthreads();
+    if (i + S::kStages - 1 < mine) load_w((i + S::kStages - 1) % S::kStages);
+    cp_async_commit();
+    if (i + 1 < mine) load_base();
+    if (wm * 16 < count && (bin < p.L || !in_place)) {
       float acc[8][4];
 #pragma unroll
       for (int n = 0; n < 8; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+        for (int k = 0; k < 4; ++k) acc[n][k] = 0.0f;
+      if (bin < p.L) {
+        const uint32_t sw = sm + S::kT + (i % S::kStages) * S::kW;
+#pragma unroll 1
+        for (int s = S::kTerms - 1; s >= 0; --s) {  // the smallest terms first
 #pragma unroll
-      for (int s = S::kTerms - 1; s >= 0; --s) {  // the smallest terms first
+          for (int kk = 0; kk < KK; ++kk) {
+            uint32_t a[4];
+            ldsm_x4(sm + (s * kTileRows + wm * 16 + (lane & 15)) * S::kTRow +
+                        (kk * 16 + (lane >> 4) * 8) * 2,
+                    a);
 #pragma unroll
-        for (int kk = 0; kk < RT / 16; ++kk) {
-          uint32_t a[4];
-          ldsm_x4(smem_u32(st + s * kTileRows * S::kTRow + (wm * 16 + (lane & 15)) * S::kTRow +
-                           (kk * 16 + (lane >> 4) * 8) * 2),
-                  a);
-#pragma unroll
-          for (int n = 0; n < 8; n += 2) {
-            uint32_t b[4];
-            const int col = wn * 64 + n * 8;
-            if constexpr (!TRANS)
-              ldsm_x4(smem_u32(sw + (col + (lane & 7) + ((lane >> 4) << 3)) * S::kWRow +
-                               (kk * 16 + ((lane >> 3) & 1) * 8) * 2),
-                      b);
-            else
-              ldsm_x4_t(smem_u32(sw + (kk * 16 + (lane & 15)) * S::kWRow +
-                                 (col + (lane >> 4) * 8) * 2),
+            for (int n = 0; n < 8; n += 2) {
+              uint32_t b[4];
+              const int col = wn * 64 + n * 8;
+              if constexpr (!TRANS)
+                ldsm_x4(sw + (col + (lane & 7) + ((lane >> 4) << 3)) * S::kWRow +
+                            (kk * 16 + ((lane >> 3) & 1) * 8) * 2,
                         b);
-            mma_bf16(acc[n], a, b[0], b[1]);
-            mma_bf16(acc[n + 1], a, b[2], b[3]);
+              else
+                ldsm_x4_t(sw + (kk * 16 + (lane & 15)) * S::kWRow + (col + (lane >> 4) * 8) * 2,
+                          b);
+              mma_bf16(acc[n], a, b[0], b[1]);
+              mma_bf16(acc[n + 1], a, b[2], b[3]);
+            }
           }
         }
       }
-      const float f = p.scale ? p.scale[t.bin] : 1.0f;
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
+      for (int h = 0; h < 2; ++h) {
+        if (wm * 16 + g + h * 8 >= count) continue;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = wm * 16 + (lane >> 2) + h * 8;
-          const int col = wn * 64 + n * 8 + (lane & 3) * 2;
-          uint8_t *at = so + row * S::kORow + col * E;
-          const float u = acc[n][2 * h], v = acc[n][2 * h + 1];
-          if constexpr (F32) {
-            float2 o = *reinterpret_cast<float2 *>(at);
-            o.x = fmaf(f, u, o.x);
-            o.y = fmaf(f, v, o.y);
-            *reinterpret_cast<float2 *>(at) = o;
-          } else {
-            const uint32_t o = *reinterpret_cast<uint32_t *>(at);
-            *reinterpret_cast<uint32_t *>(at) =
-                bf16x2(fmaf(f, u, bf16_lo(o)), fmaf(f, v, bf16_hi(o)));
+        for (int b = 0; b < 2; ++b) {
+          const int col = slab * kSlab + wn * 64 + b * 32 + c8;
+          if (col >= p.C || !store_ok(p.status, row[h] >= 0 && row[h] < p.M && col + 8 <= p.ld_out))
+            continue;
+          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) +
+                                                 (row[h] * p.ld_out + col) * E);
+          uint32_t o[4 * Q];
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            o[4 * q] = now[h][b][q].x;
+            o[4 * q + 1] = now[h][b][q].y;
+            o[4 * q + 2] = now[h][b][q].z;
+            o[4 * q + 3] = now[h][b][q].w;
           }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = acc[b * 4 + j][2 * h], y = acc[b * 4 + j][2 * h + 1];
+            if constexpr (F32) {
+              o[2 * j] = __float_as_uint(fmaf(f, x, __uint_as_float(o[2 * j])));
+              o[2 * j + 1] = __float_as_uint(fmaf(f, y, __uint_as_float(o[2 * j + 1])));
+            } else {
+              o[j] = bf16x2(fmaf(f, x, bf16_lo(o[j])), fmaf(f, y, bf16_hi(o[j])));
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < Q; ++q)
+            dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
+      }
     }
-    __syncthreads();
+    fresh = ++slab == slabs;
+    if (fresh) {
+      slab = 0;
+      ++tile;
+    }
   }
-  for (int i = threadIdx.x; i < t.count * CH; i += kThreads) {
-    const int r = i / CH, c = i % CH;
-    if (c0 + c * VE >= p.C) continue;
-    uint8_t *dst =
-        static_cast<uint8_t *>(p.out) + (rows[r] * p.ld_out + c0 + c * VE) * E;
-    if (store_ok(p.status, rows[r] >= 0 && rows[r] < p.M && c0 + c * VE + VE <= p.ld_out))
-      *reinterpret_cast<uint4 *>(dst) =
-          *reinterpret_cast<const uint4 *>(so + r * S::kORow + c * 16);
-  }
+  cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------------- outer
 // out[a](c, j) = f sum_{m of a} src[m][c] v[m][j]: dB[a][n][j] (src dy, v t, f =
 // scale) and dA[a][j][k] (src x, v dt, f = 1, stored transposed).  One block
-// per adapter, 64 columns c and share of the adapter's row tiles; the blocks
-// of a cluster hold the shares and add them in a fixed order.
+// per adapter, slab of 128 columns c and share of the adapter's rows, 64 rows a
+// stage: TMA gathers the rows of src by number and brings v's box; both are
+// operands whose rows run along the contraction, M = 128 columns of src by N =
+// RT.  v is zero in the rows past a tile's last, where src repeats a row.  The
+// blocks of a cluster hold the shares and add them in a fixed order.  Rows are
+// taken from the last to the first: dy's last rows are what the contraction
+// before left in L2.
 struct OuterSide {
-  const uint16_t *src;
-  int64_t ld;
-  const float *v;
   const float *scale;  // nullptr: 1
   void *out;
   int32_t C;
@@ -531,190 +689,224 @@ struct OuterArgs {
   OuterSide side[2];
   int32_t slabs0;  // slabs of side 0
   const int32_t *plan;
-  int64_t M;
+  int64_t M, max_tiles;
   int32_t R, L;
   int *status;
 };
-
-template <int RT, bool F32>
-struct OuterSmem {
-  static constexpr int kTerms = F32 ? 3 : 1;
-  static constexpr int kStages = 4;
-  static constexpr int kSrc = kTileRows * 128;
-  static constexpr int kVRow = RT * 2 + 16;
-  static constexpr int kV = kTerms * kTileRows * kVRow;  // two buffers
-  static constexpr int kVAt = kStages * kSrc;
-  static constexpr int kPart = 64 * (RT + 1) * 4;
-  static constexpr int kBuf = kVAt + 2 * kV;
-  static constexpr int kBytes = kBuf > kPart ? kBuf : kPart;
+struct OuterMaps {
+  CUtensorMap src[2], v[2];
 };
 
-template <int RT, bool F32>
-__global__ void __launch_bounds__(kThreads) lora_outer_kernel(const OuterArgs p) {
-  using S = OuterSmem<RT, F32>;
-  extern __shared__ __align__(128) uint8_t smem[];
+constexpr int kOuterThreads = 128;
+constexpr int kOuterSlab = 128;
+constexpr int kOuterRows = 64;  // a stage
+
+template <int RT, int TERMS>
+struct OuterSmem {
+  static constexpr int kSrc = kOuterRows * kOuterSlab * 2;  // two boxes of 64 columns
+  static constexpr int kV = TERMS * kOuterRows * RT * 2;
+  static constexpr int kStage = kSrc + kV;
+  static constexpr int kStages = 4 * kStage <= 104 * 1024 ? 4 : 3;
+  static constexpr int kBars = kStages * kStage;
+  static constexpr int kPartRow = RT + 1;  // floats
+  static constexpr int kBytes = kBars + (2 * kStages + 1) * 8 + 16 + 1024;
+  static_assert(kOuterSlab * kPartRow * 4 <= kBars, "partial sums reuse the stages");
+  static_assert(kBytes <= 232448, "dynamic shared memory above the per-block limit");
+};
+
+template <int RT, int TERMS>
+__global__ void __launch_bounds__(kOuterThreads)
+    lora_outer_kernel(const __grid_constant__ OuterMaps maps, const OuterArgs p) {
+  using S = OuterSmem<RT, TERMS>;
+  constexpr int STAGES = S::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kBars);
+  uint64_t *empty = full + STAGES;
+  uint64_t *done = empty + STAGES;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   cg::cluster_group cluster = cg::this_cluster();
   const int shares = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
-  const PlanView plan = plan_view(p.plan, p.M, p.L);
-  if (!plan_fits(plan, p.M, p.L, p.status)) return;
-  const int bin = blockIdx.y;
-  const bool second = static_cast<int>(blockIdx.x) >= p.slabs0;
-  const OuterSide &sd = p.side[second ? 1 : 0];
-  const int c0 = (static_cast<int>(blockIdx.x) - (second ? p.slabs0 : 0)) * 64;
-  const int first = plan.bin_start[bin], end = plan.bin_start[bin + 1];
-  const int tiles = (end - first + kTileRows - 1) / kTileRows;
-  const int steps = tiles > rank ? (tiles - rank + shares - 1) / shares : 0;
-  const uint32_t base = smem_u32(smem);
-
-  auto load = [&](int step) {
-    const int at = first + (rank + step * shares) * kTileRows;
-    const uint32_t st = base + (step % S::kStages) * S::kSrc;
-    for (int i = threadIdx.x; i < kTileRows * 8; i += kThreads) {
-      const int r = i >> 3, c = i & 7;
-      const bool ok = at + r < end && c0 + c * 8 < sd.C;
-      const int64_t row = ok ? plan.perm[at + r] : 0;
-      cp_async16(st + swz(r, c), sd.src + (ok ? row * sd.ld + c0 + c * 8 : 0), ok);
-    }
-  };
-  // this thread's part of a tile of v: RT / 16 groups of four values
-  constexpr int VN = kTileRows * (RT / 4) / kThreads;
-  float4 vr[VN];
-  auto fetch_v = [&](int step) {
-    const int at = first + (rank + step * shares) * kTileRows;
-#pragma unroll
-    for (int q = 0; q < VN; ++q) {
-      const int i = threadIdx.x + q * kThreads;
-      const int r = i / (RT / 4), c = i % (RT / 4);
-      vr[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (at + r < end && c * 4 < p.R)
-        vr[q] = *reinterpret_cast<const float4 *>(
-            sd.v + static_cast<int64_t>(plan.perm[at + r]) * p.R + c * 4);
-    }
-  };
-  auto store_v = [&](int buf) {
-#pragma unroll
-    for (int q = 0; q < VN; ++q) {
-      const int i = threadIdx.x + q * kThreads;
-      const int r = i / (RT / 4), c = i % (RT / 4);
-      float4 v = vr[q];
-#pragma unroll
-      for (int s = 0; s < S::kTerms; ++s) {
-        const uint32_t lo = bf16x2(v.x, v.y), hi = bf16x2(v.z, v.w);
-        *reinterpret_cast<uint2 *>(smem + S::kVAt + buf * S::kV +
-                                   (s * kTileRows + r) * S::kVRow + c * 8) = make_uint2(lo, hi);
-        v = make_float4(v.x - bf16_lo(lo), v.y - bf16_hi(lo), v.z - bf16_lo(hi),
-                        v.w - bf16_hi(hi));
-      }
-    }
-  };
-
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wm = warp & 3, wn = warp >> 2;
-  constexpr int NT = RT / 16;
-  float acc[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+  const bool second = static_cast<int>(blockIdx.x) >= p.slabs0;
+  const OuterSide sd = second ? p.side[1] : p.side[0];
+  const CUtensorMap *tm_src = second ? &maps.src[1] : &maps.src[0];
+  const CUtensorMap *tm_v = second ? &maps.v[1] : &maps.v[0];
+  const int c0 = (static_cast<int>(blockIdx.x) - (second ? p.slabs0 : 0)) * kOuterSlab;
 
-#pragma unroll
-  for (int s = 0; s < S::kStages - 1; ++s) {
-    if (s < steps) load(s);
-    cp_async_commit();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(tm_src);
+    prefetch_tmap(tm_v);
   }
-  if (steps > 0) fetch_v(0);
-  for (int step = 0; step < steps; ++step) {
-    store_v(step & 1);  // the buffer read two steps ago
-    cp_async_wait<S::kStages - 2>();
-    __syncthreads();
-    if (step + S::kStages - 1 < steps) load(step + S::kStages - 1);
-    cp_async_commit();
-    if (step + 1 < steps) fetch_v(step + 1);
-    const uint32_t ss = base + (step % S::kStages) * S::kSrc;
-    const uint32_t sv = base + S::kVAt + (step & 1) * S::kV;
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, RT);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int bin = blockIdx.y;
+  const bool fits = plan_fits(p.plan, p.M, p.L, p.status);
+  int tile0 = 0, steps = 0, all = 0;
+  const int32_t *recs = p.plan + plan_recs_at(p.L);
+  if (fits) {
+    tile0 = p.plan[4 + bin];
+    const int tiles = p.plan[4 + bin + 1] - tile0;
+    // stages of 64 rows: two per full tile, one or two in the last
+    if (tiles > 0)
+      all = 2 * (tiles - 1) +
+            (recs[static_cast<int64_t>(tile0 + tiles - 1) * kRecWords + 1] + kOuterRows - 1) /
+                kOuterRows;
+    steps = all > rank ? (all - rank + shares - 1) / shares : 0;
+  }
+  grid_dependency_wait();
+
+  if (fits) {
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      // lane l: rows 4 (l % 16) .. + 3 of column box l / 16
+      const bool brings = c0 + (lane >> 4) * 64 < sd.C;  // no box past the last column
+      const uint32_t bytes = S::kV + (c0 + 64 < sd.C ? 2 : 1) * 8192;
+      uint32_t armed = 0, armed_parity = 0;
+      auto fetch = [&](int step) {
+        const int s64 = all - 1 - (rank + step * shares);
+        return *reinterpret_cast<const int4 *>(
+            recs + static_cast<int64_t>(tile0 + s64 / 2) * kRecWords + 4 + (s64 & 1) * 64 +
+            (lane & 15) * 4);
+      };
+      int4 rows = make_int4(0, 0, 0, 0);
+      if (steps > 0) rows = fetch(0);
+      for (int step = 0; step < steps; ++step) {
+        const int st = step % STAGES;
+        const uint32_t phase = (step / STAGES) & 1;
+        const int s64 = all - 1 - (rank + step * shares);
+        uint8_t *src = smem + st * S::kStage;
+        bool ok = true;
+        if (lane == 0) {
+          ok = bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
+          if (ok) {
+            mbar_arrive_expect_tx(&full[st], bytes);
+            const int vrow = tile0 * kTileRows + s64 * kOuterRows;
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      // source columns are the product's rows: transposed fragments
-      uint32_t a[4];
-      ldsm_x4_t(ss + swz(kk * 16 + (lane & 7) + ((lane >> 4) << 3), wm * 2 + ((lane >> 3) & 1)),
-                a);
+            for (int q = 0; q < TERMS; ++q)
 #pragma unroll
-      for (int s = S::kTerms - 1; s >= 0; --s) {
-        const uint32_t vrow = sv + (s * kTileRows + kk * 16 + (lane & 15)) * S::kVRow;
-        if constexpr (NT == 1) {
-          uint32_t b0, b1;
-          ldsm_x2_t(vrow + wn * 16, b0, b1);
-          mma_bf16(acc[0], a, b0, b1);
-        } else {
-#pragma unroll
-          for (int n = 0; n < NT; n += 2) {
-            uint32_t b[4];
-            ldsm_x4_t(vrow + (wn * (RT / 2) + n * 8 + (lane >> 4) * 8) * 2, b);
-            mma_bf16(acc[n], a, b[0], b[1]);
-            mma_bf16(acc[n + 1], a, b[2], b[3]);
+              for (int h = 0; h < RT / 64; ++h)
+                tma_load_3d(src + S::kSrc + (q * (RT / 64) + h) * 8192, tm_v, &full[st], h * 64,
+                            vrow, q);
+            armed |= 1u << st;
+            armed_parity = (armed_parity & ~(1u << st)) | (phase << st);
           }
         }
+        if (!__shfl_sync(~0u, ok, 0)) break;
+        if (brings)
+          tma_gather4(src + (lane >> 4) * 8192 + (lane & 15) * 512, tm_src, &full[st],
+                      c0 + (lane >> 4) * 64, rows);
+        if (step + 1 < steps) rows = fetch(step + 1);
+        __syncwarp();
       }
-    }
-  }
-  cp_async_wait<0>();
-  __syncthreads();
-
-  float *part = reinterpret_cast<float *>(smem);
-  constexpr int PS = RT + 1;
+      if (lane == 0)
+        for (int s = 0; s < STAGES; ++s)
+          if (armed & (1u << s)) mbar_wait(&full[s], (armed_parity >> s) & 1u, kBoundedWaitNs);
+      __syncwarp();
+    } else if (warp == 1) {
+      // -------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t idesc = idesc_bf16(kOuterSlab, RT) | kIdescTransA | kIdescTransB;
+        for (int step = 0; step < steps; ++step) {
+          const int st = step % STAGES;
+          if (!bounded_wait(&full[st], (step / STAGES) & 1, abort_flag, p.status,
+                            SQ_ERR_DEVICE_TIMEOUT))
+            break;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + st * S::kStage), sb = sa + S::kSrc;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int col = wn * (RT / 2) + n * 8 + (lane & 3) * 2;
-    const int row = wm * 16 + (lane >> 2);
-    part[row * PS + col] = acc[n][0];
-    part[row * PS + col + 1] = acc[n][1];
-    part[(row + 8) * PS + col] = acc[n][2];
-    part[(row + 8) * PS + col + 1] = acc[n][3];
-  }
-  if (shares > 1) cluster.sync(); else __syncthreads();
-  const float f = sd.scale ? sd.scale[bin] : 1.0f;
-  const int cols = sd.C - c0 < 64 ? sd.C - c0 : 64;
-  const int total = cols * p.R;
-  const int64_t obase = static_cast<int64_t>(bin) * p.R * sd.C;
-  for (int e = rank * kThreads + threadIdx.x; e < total; e += shares * kThreads) {
-    int c, j;
-    if (sd.transposed) {
-      j = e / cols;
-      c = e - j * cols;
-    } else {
-      c = e / p.R;
-      j = e - c * p.R;
+          for (int q = TERMS - 1; q >= 0; --q)
+#pragma unroll
+            for (int kk = 0; kk < kOuterRows / 16; ++kk)
+              mma_bf16_tc(tmem, sdesc_mnmajor_sw128(sa + kk * 2048, 8192),
+                          sdesc_mnmajor_sw128(sb + q * (RT / 64) * 8192 + kk * 2048, 8192), idesc,
+                          step > 0 || kk > 0 || q < TERMS - 1);
+          mma_commit(&empty[st]);
+        }
+        mma_commit(done);
+      }
+      __syncwarp();
     }
-    float s = 0.0f;
-    for (int q = 0; q < shares; ++q) {
-      const float *src = shares > 1 ? cluster.map_shared_rank(part, q) : part;
-      s += src[c * PS + j];
+    const bool ok = bounded_wait(done, 0, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
+    tc_fence_after();
+    __syncthreads();  // nothing reads or fills the stages any more
+
+    float *part = reinterpret_cast<float *>(smem);
+    constexpr int PS = S::kPartRow;
+#pragma unroll
+    for (int c = 0; c < RT; c += 32) {
+      uint32_t r[32];
+      __syncwarp();
+      tmem_ld_32x32b_x32(tmem + c + (static_cast<uint32_t>(warp * 32) << 16), r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        part[threadIdx.x * PS + c + j] = steps > 0 ? __uint_as_float(r[j]) : 0.0f;
     }
-    const int64_t at = obase + (sd.transposed ? static_cast<int64_t>(j) * sd.C + c0 + c
-                                              : static_cast<int64_t>(c0 + c) * p.R + j);
-    if (!store_ok(p.status, j < p.R && c0 + c < sd.C)) continue;
-    if constexpr (F32)
-      static_cast<float *>(sd.out)[at] = f * s;
-    else
-      static_cast<__nv_bfloat16 *>(sd.out)[at] = __float2bfloat16_rn(f * s);
+    if (shares > 1) cluster.sync(); else __syncthreads();
+    const float f = sd.scale ? sd.scale[bin] : 1.0f;
+    const int cols = sd.C - c0 < kOuterSlab ? sd.C - c0 : kOuterSlab;
+    const int n_out = ok ? cols * p.R : 0;
+    const int64_t obase = static_cast<int64_t>(bin) * p.R * sd.C;
+    for (int e = rank * kOuterThreads + threadIdx.x; e < n_out; e += shares * kOuterThreads) {
+      int c, j;
+      if (sd.transposed) {
+        j = e / cols;
+        c = e - j * cols;
+      } else {
+        c = e / p.R;
+        j = e - c * p.R;
+      }
+      float s = 0.0f;
+      for (int q = 0; q < shares; ++q) {
+        const float *src = shares > 1 ? cluster.map_shared_rank(part, q) : part;
+        s += src[c * PS + j];
+      }
+      const int64_t at = obase + (sd.transposed ? static_cast<int64_t>(j) * sd.C + c0 + c
+                                                : static_cast<int64_t>(c0 + c) * p.R + j);
+      if (!store_ok(p.status, j < p.R && c0 + c < sd.C)) continue;
+      if constexpr (TERMS > 1)
+        static_cast<float *>(sd.out)[at] = f * s;
+      else
+        static_cast<__nv_bfloat16 *>(sd.out)[at] = __float2bfloat16_rn(f * s);
+    }
+    if (shares > 1) cluster.sync();
   }
-  if (shares > 1) cluster.sync();
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, RT);
+  }
 }
 
 // ------------------------------------------------------------------ host side
-int sm_count() {
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms > 0 ? sms : 148;
-}
-
 // Launch with dynamic shared memory and clusters of `cluster` blocks along the
-// grid's dimension `dim` (0 x, 1 y, 2 z).
-template <auto Kernel, typename Args>
-cudaError_t launch(dim3 grid, int smem, int cluster, int dim, const Args &args,
-                   cudaStream_t stream) {
+// grid's dimension `dim` (0 x, 1 y, 2 z).  Every kernel here waits for the one
+// ahead of it in the stream (programmatic dependent launch) before it reads
+// what that one may have written.
+template <auto Kernel, typename... Args>
+cudaError_t launch(dim3 grid, int threads, int smem, int cluster, int dim, cudaStream_t stream,
+                   const Args &...args) {
   static bool attr_set[64] = {};  // per kernel and device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -726,67 +918,153 @@ cudaError_t launch(dim3 grid, int smem, int cluster, int dim, const Args &args,
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = dim == 0 ? cluster : 1;
-  attr[0].val.clusterDim.y = dim == 1 ? cluster : 1;
-  attr[0].val.clusterDim.z = dim == 2 ? cluster : 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = dim == 0 ? cluster : 1;
+  attr[1].val.clusterDim.y = dim == 1 ? cluster : 1;
+  attr[1].val.clusterDim.z = dim == 2 ? cluster : 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, Kernel, args);
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, Kernel, args...);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int RT, bool TRANS>
-cudaError_t run_contract(const ContractArgs &a, cudaStream_t stream) {
+// Tensor map of bf16 [d2][d1][d0] with row stride ld (elements), boxes of 64
+// columns by `rows`, 128-byte swizzle; d2 == 0: two dimensions.
+cudaError_t bf16_map(CUtensorMap *map, const void *ptr, int64_t d0, int64_t d1, int64_t d2,
+                     int64_t ld, int rows) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1),
+                              static_cast<cuuint64_t>(d2)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2,
+                                 static_cast<cuuint64_t>(ld) * 2 * static_cast<cuuint64_t>(d1)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 == 0 ? 2 : 3, const_cast<void *>(ptr),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <int RT, bool TRANS, int TERMS>
+cudaError_t run_contract(const uint16_t *in, int64_t ld, const uint16_t *w, const ContractArgs &a,
+                         cudaStream_t stream) {
+  CUtensorMap tm_in, tm_w;
+  cudaError_t e = bf16_map(&tm_in, in, a.C, a.M, 0, ld, 1);
+  if (e == cudaSuccess)
+    e = TRANS ? bf16_map(&tm_w, w, a.R, a.C, a.L, a.R, 64)
+              : bf16_map(&tm_w, w, a.C, a.R, a.L, a.C, RT);
+  if (e != cudaSuccess) return e;
   // Slices of the contracted dimension: enough blocks for two per SM, none
   // shorter than 256 columns.
-  const int64_t tiles = plan_max_tiles(a.M, a.L);
   int slices = 1;
-  while (slices < 8 && tiles * slices < 2 * sm_count() && a.C >= 256 * slices * 2) slices *= 2;
-  return launch<lora_contract_kernel<RT, TRANS>>(dim3(static_cast<unsigned>(tiles), slices),
-                                                 ContractSmem<RT, TRANS>::kBytes, slices, 1, a,
-                                                 stream);
+  while (slices < 8 && a.max_tiles * slices < 2 * sm_count() && a.C >= 256 * slices * 2)
+    slices *= 2;
+  return launch<lora_contract_kernel<RT, TRANS, TERMS>>(
+      dim3(static_cast<unsigned>(a.max_tiles), slices), kContractThreads,
+      ContractSmem<RT>::kBytes, slices, 1, stream, tm_in, tm_w, a);
 }
 
 template <int RT, bool TRANS, bool F32>
 cudaError_t run_expand(const ExpandArgs &a, cudaStream_t stream) {
-  const int64_t tiles = plan_max_tiles(a.M, a.L);
-  const int64_t blocks = tiles * ((a.C + kSlab - 1) / kSlab);
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  return launch<lora_expand_kernel<RT, TRANS, F32>>(dim3(static_cast<unsigned>(blocks)),
-                                                    ExpandSmem<RT, TRANS, F32>::kBytes, 1, 0, a,
-                                                    stream);
+  const int64_t units = plan_max_tiles(a.M, a.L) * ((a.C + kSlab - 1) / kSlab);
+  const int sms = sm_count();
+  return launch<lora_expand_kernel<RT, TRANS, F32>>(
+      dim3(static_cast<unsigned>(units < sms ? units : sms)), kExpandThreads,
+      ExpandSmem<RT, TRANS, F32>::kBytes, 1, 0, stream, a);
 }
 
-template <int RT, bool F32>
-cudaError_t run_outer(const OuterArgs &a, cudaStream_t stream) {
-  const int slabs = a.slabs0 + (a.side[1].C + 63) / 64;
-  // Shares of an adapter's rows: enough blocks for four per SM, none with
-  // fewer than two row tiles on average.
+template <int RT, int TERMS>
+cudaError_t run_outer(const OuterMaps &maps, const OuterArgs &a, cudaStream_t stream) {
+  const int slabs = a.slabs0 + (a.side[1].C + kOuterSlab - 1) / kOuterSlab;
+  // Shares of an adapter's rows: enough blocks for two per SM, none with fewer
+  // than two stages on average.
   int shares = 1;
-  while (shares < 8 && static_cast<int64_t>(slabs) * a.L * shares < 4 * sm_count() &&
-         a.M / a.L >= 2 * kTileRows * shares * 2)
+  while (shares < 8 && static_cast<int64_t>(slabs) * a.L * shares < 2 * sm_count() &&
+         a.M / a.L >= 2 * kOuterRows * shares * 2)
     shares *= 2;
-  return launch<lora_outer_kernel<RT, F32>>(dim3(slabs, a.L, shares), OuterSmem<RT, F32>::kBytes,
-                                            shares, 2, a, stream);
+  return launch<lora_outer_kernel<RT, TERMS>>(dim3(slabs, a.L, shares), kOuterThreads,
+                                              OuterSmem<RT, TERMS>::kBytes, shares, 2, stream,
+                                              maps, a);
 }
 
+// Ranks are padded to 64 (128) columns: the boxes' columns past R read as zero.
 template <typename F>
 cudaError_t by_rank(int R, F &&f) {
-  if (R <= 16) return f(std::integral_constant<int, 16>());
-  if (R <= 32) return f(std::integral_constant<int, 32>());
   if (R <= 64) return f(std::integral_constant<int, 64>());
   return f(std::integral_constant<int, 128>());
+}
+// The expansion's inner dimension, in which padding costs products.
+template <typename F>
+cudaError_t by_rank_fine(int R, F &&f) {
+  if (R <= 16) return f(std::integral_constant<int, 16>());
+  if (R <= 32) return f(std::integral_constant<int, 32>());
+  return by_rank(R, f);
+}
+
+template <int TERMS>
+cudaError_t run_backward(const LoraRequest &q, cudaStream_t stream) {
+  if (q.M == 0) {
+    const size_t elem = TERMS > 1 ? 4 : 2, rank = static_cast<size_t>(q.L) * q.R;
+    const cudaError_t err = cudaMemsetAsync(q.dA, 0, rank * q.K * elem, stream);
+    return err != cudaSuccess ? err : cudaMemsetAsync(q.dB, 0, rank * q.N * elem, stream);
+  }
+  const int32_t N = static_cast<int32_t>(q.N), K = static_cast<int32_t>(q.K);
+  const int64_t max_tiles = plan_max_tiles(q.M, q.L), rows = max_tiles * kTileRows;
+  uint16_t *vdt = static_cast<uint16_t *>(q.workspace);
+  uint16_t *vt = vdt + TERMS * rows * q.R;
+  const ContractArgs c = {q.scale, q.plan, nullptr, q.t, vt,  vdt,
+                          q.M,     max_tiles, N,    q.R, q.L, q.status};
+  cudaError_t e = by_rank(q.R, [&](auto rt) {
+    return run_contract<decltype(rt)::value, true, TERMS>(q.dy, q.lddy, q.B, c, stream);
+  });
+  if (e == cudaSuccess && q.dA != nullptr) {
+    OuterMaps maps;
+    OuterArgs o = {};
+    o.side[0] = {q.scale, q.dB, N, 0};
+    o.side[1] = {nullptr, q.dA, K, 1};
+    o.slabs0 = (N + kOuterSlab - 1) / kOuterSlab;
+    o.plan = q.plan;
+    o.M = q.M;
+    o.max_tiles = max_tiles;
+    o.R = q.R;
+    o.L = q.L;
+    o.status = q.status;
+    e = bf16_map(&maps.src[0], q.dy, N, q.M, 0, q.lddy, 1);
+    if (e == cudaSuccess) e = bf16_map(&maps.src[1], q.x, K, q.M, 0, q.ldx, 1);
+    if (e == cudaSuccess) e = bf16_map(&maps.v[0], vt, q.R, rows, TERMS, q.R, kOuterRows);
+    if (e == cudaSuccess) e = bf16_map(&maps.v[1], vdt, q.R, rows, TERMS, q.R, kOuterRows);
+    if (e == cudaSuccess)
+      e = by_rank(q.R, [&](auto rt) {
+        return run_outer<decltype(rt)::value, TERMS>(maps, o, stream);
+      });
+  }
+  if (e == cudaSuccess && q.dx != nullptr) {
+    const ExpandArgs x = {nullptr, vdt, q.A, nullptr, q.plan, q.base, q.ld_base, q.dx, q.lddx,
+                          q.M, K, q.R, q.L, q.status};
+    e = by_rank_fine(q.R, [&](auto rt) {
+      return run_expand<decltype(rt)::value, true, false>(x, stream);
+    });
+  }
+  return e;
 }
 
 }  // namespace
 
 size_t lora_plan_words(int64_t M, int32_t L) {
-  return static_cast<size_t>(plan_tiles_at(M, L) + 2 * plan_max_tiles(M, L));
+  return static_cast<size_t>(plan_recs_at(L) + kRecWords * plan_max_tiles(M, L));
+}
+
+size_t lora_workspace_bytes(int64_t M, int32_t R, int32_t L, bool f32) {
+  return static_cast<size_t>(plan_max_tiles(M, L)) * kTileRows * R * 2 * 2 * (f32 ? 3 : 1);
 }
 
 cudaError_t launch_lora_plan(const int32_t *adapter, int64_t M, int32_t L, int32_t *plan,
@@ -801,48 +1079,23 @@ cudaError_t launch_lora_plan(const int32_t *adapter, int64_t M, int32_t L, int32
 }
 
 cudaError_t launch_lora_forward(const LoraRequest &q, cudaStream_t stream) {
-  const ContractArgs c = {q.x, q.ldx, q.A, nullptr, q.plan, q.t, q.M,
-                          static_cast<int32_t>(q.K), q.R, q.L, q.status};
-  const ExpandArgs e = {q.t, q.B, q.scale, q.plan, q.base, q.ld_base, q.y, q.ldy, q.M,
+  const ContractArgs c = {nullptr, q.plan, q.t, nullptr, nullptr, nullptr,
+                          q.M, plan_max_tiles(q.M, q.L), static_cast<int32_t>(q.K), q.R, q.L,
+                          q.status};
+  const ExpandArgs e = {q.t, nullptr, q.B, q.scale, q.plan, q.base, q.ld_base, q.y, q.ldy, q.M,
                         static_cast<int32_t>(q.N), q.R, q.L, q.status};
-  return by_rank(q.R, [&](auto rt) {
+  const cudaError_t err = by_rank(q.R, [&](auto rt) {
+    return run_contract<decltype(rt)::value, false, 0>(q.x, q.ldx, q.A, c, stream);
+  });
+  if (err != cudaSuccess) return err;
+  return by_rank_fine(q.R, [&](auto rt) {
     constexpr int RT = decltype(rt)::value;
-    const cudaError_t err = run_contract<RT, false>(c, stream);
-    if (err != cudaSuccess) return err;
     return q.f32 ? run_expand<RT, false, true>(e, stream) : run_expand<RT, false, false>(e, stream);
   });
 }
 
 cudaError_t launch_lora_backward(const LoraRequest &q, cudaStream_t stream) {
-  return by_rank(q.R, [&](auto rt) {
-    constexpr int RT = decltype(rt)::value;
-    if (q.M > 0) {
-      const ContractArgs c = {q.dy, q.lddy, q.B, q.scale, q.plan, q.dt, q.M,
-                              static_cast<int32_t>(q.N), q.R, q.L, q.status};
-      const cudaError_t err = run_contract<RT, true>(c, stream);
-      if (err != cudaSuccess) return err;
-    }
-    if (q.dA != nullptr) {
-      OuterArgs o = {};
-      o.side[0] = {q.dy, q.lddy, q.t, q.scale, q.dB, static_cast<int32_t>(q.N), 0};
-      o.side[1] = {q.x, q.ldx, q.dt, nullptr, q.dA, static_cast<int32_t>(q.K), 1};
-      o.slabs0 = static_cast<int32_t>((q.N + 63) / 64);
-      o.plan = q.plan;
-      o.M = q.M;
-      o.R = q.R;
-      o.L = q.L;
-      o.status = q.status;
-      const cudaError_t err =
-          q.f32 ? run_outer<RT, true>(o, stream) : run_outer<RT, false>(o, stream);
-      if (err != cudaSuccess) return err;
-    }
-    if (q.M > 0 && q.dx != nullptr) {
-      const ExpandArgs e = {q.dt, q.A, nullptr, q.plan, q.base, q.ld_base, q.dx, q.lddx, q.M,
-                            static_cast<int32_t>(q.K), q.R, q.L, q.status};
-      return run_expand<RT, true, false>(e, stream);
-    }
-    return cudaSuccess;
-  });
+  return q.f32 ? run_backward<3>(q, stream) : run_backward<1>(q, stream);
 }
 
 }  // namespace sq

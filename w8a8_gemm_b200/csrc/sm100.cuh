@@ -82,6 +82,26 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
   }
 }
 
+// Limit of a wait inside a kernel: far above any tile's latency.
+constexpr uint64_t kBoundedWaitNs = 2000000000ull;  // 2 s
+
+// mbar_wait that also gives up when another role of the block has given up
+// (*abort_flag), and records `code` in the error word when it does so itself.
+__device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity,
+                                             volatile int *abort_flag, int *status, int code) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > kBoundedWaitNs) {
+      *abort_flag = 1;
+      atomicExch(status, code);
+      return false;
+    }
+  }
+}
+
 // ----------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar,
                                             int32_t c0, int32_t c1) {
@@ -98,6 +118,17 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Four rows of a 2D tensor (its map's box is one row high), given by number,
+// into four neighbouring rows of the tile; columns from c0.
+__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                            int32_t c0, const int4 &rows) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w)
       : "memory");
 }
 
@@ -151,6 +182,12 @@ __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Lets the next kernel of the stream, if it was launched with programmatic
+// stream serialization, begin its prologue now.
+__device__ __forceinline__ void grid_dependency_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -198,6 +235,23 @@ __device__ __forceinline__ uint64_t sdesc_kmajor_sw128(uint32_t saddr) {
   d |= static_cast<uint64_t>(2) << 61;
   return d;
 }
+
+// The same for an operand tile whose rows run along the contracted dimension
+// (MN-major): boxes of 64 16-bit elements (128 bytes) by any multiple of 8 rows,
+// 128-byte swizzled; `box_bytes` apart along M or N (bits 16-29), 1024 bytes
+// between groups of 8 rows of the contraction (bits 32-45).
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr, uint32_t box_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((box_bytes >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// Bits of an instruction descriptor: A or B is MN-major.
+constexpr uint32_t kIdescTransA = 1u << 15, kIdescTransB = 1u << 16;
 
 // Instruction descriptor of tcgen05.mma kind::i8: signed A and B, int32 D,
 // both operands K-major, shape M x N.

@@ -99,7 +99,7 @@ size_t gemm_workspace_bytes();
 
 // ---- low-rank adapters (lora.cu) ---------------------------------------------
 // Rows of one tile of the plan.
-#define SQ_LORA_TILE_ROWS 64
+#define SQ_LORA_TILE_ROWS 128
 
 struct LoraRequest {
   const uint16_t *x, *dy, *A, *B;
@@ -109,7 +109,8 @@ struct LoraRequest {
   void *y;               // forward
   uint16_t *dx;          // backward, may be nullptr
   void *dA, *dB;         // backward, both or neither
-  float *t, *dt;         // [M][R]
+  float *t;              // [M][R]
+  void *workspace;       // backward
   int64_t ldx, lddy, ld_base, ldy, lddx;
   int64_t M, N, K;
   int32_t R, L;
@@ -117,6 +118,7 @@ struct LoraRequest {
   int *status;
 };
 size_t lora_plan_words(int64_t M, int32_t L);
+size_t lora_workspace_bytes(int64_t M, int32_t R, int32_t L, bool f32);
 cudaError_t launch_lora_plan(const int32_t *adapter, int64_t M, int32_t L, int32_t *plan,
                              int *status, cudaStream_t stream);
 cudaError_t launch_lora_forward(const LoraRequest &q, cudaStream_t stream);
@@ -193,6 +195,9 @@ sq_status validate_gemm(const int8_t *planes, const int8_t *wq, const float *s_w
 
 // Device address of the library's error word on the current device.
 int *device_status_word();
+
+// SMs of the current device.
+int sm_count();
 
 // SQ_OK if the current device is an sm_100.
 sq_status check_device();
