@@ -108,9 +108,9 @@ def test_plan_orders_rows_by_adapter_and_keeps_their_order():
         assert plan[3] == len(tiles)
         assert plan[4:4 + L + 2] == [sum(t[0] < b for t in tiles) for b in range(L + 2)]
         at = (4 + L + 2 + 3) // 4 * 4
-        for b, s in tiles:     # {bin, rows, place, 0, row numbers}
+        for b, s in tiles:     # {bin, rows, place, neighbours, row numbers}
             n = min(128, start[b + 1] - s)
-            assert plan[at:at + 3] == [b, n, s]
+            assert plan[at:at + 4] == [b, n, s, int(order[s + n - 1] - order[s] == n - 1)]
             assert plan[at + 4:at + 132] == order[s:s + n] + [order[s]] * (128 - n)
             at += 132
 

@@ -41,8 +41,9 @@ constexpr int32_t kPlanMagic = 0x53514C32;
 // int32 words: [0] magic, [1] M, [2] L, [3] tiles, tile_at[L + 2] (the first tile
 // of each bin; bin L holds the rows without an adapter), padding to a multiple
 // of four, then a record per tile: {bin, rows, first place in the order by
-// adapter, 0, row numbers[128]}.  A kernel finds everything about its tile at
-// one address; row numbers past the tile's rows repeat its first.
+// adapter, 1 if its rows are neighbours, row numbers[128]}.  A kernel finds
+// everything about its tile at one address; row numbers past the tile's rows
+// repeat its first.
 constexpr int kRecWords = 4 + kTileRows;
 __host__ __device__ inline int64_t plan_recs_at(int32_t L) { return (4 + (L + 2) + 3) / 4 * 4; }
 __host__ __device__ inline int64_t plan_max_tiles(int64_t M, int32_t L) {
@@ -136,7 +137,6 @@ __global__ void __launch_bounds__(kPlanWarps * 32) lora_plan_kernel(
       recs[at * kRecWords] = b;
       recs[at * kRecWords + 1] = left < kTileRows ? left : kTileRows;
       recs[at * kRecWords + 2] = first;
-      recs[at * kRecWords + 3] = 0;
     }
   // places: 32 rows a step in order; equal bins of a step rank by lane
   for (int64_t r0 = lo; r0 < hi; r0 += 32) {
@@ -163,6 +163,12 @@ __global__ void __launch_bounds__(kPlanWarps * 32) lora_plan_kernel(
     if (in && rank == 0) mine[b] += __popc(same);
     __syncwarp();
   }
+  __syncthreads();
+  // rows ascend within a tile: neighbours if the last is the first + rows - 1
+  for (int64_t at = threadIdx.x; at < tile_at[bins]; at += blockDim.x) {
+    int32_t *rec = recs + at * kRecWords;
+    if (store_ok(status, at < max_tiles)) rec[3] = rec[4 + rec[1] - 1] - rec[4] == rec[1] - 1;
+  }
 }
 
 // ----------------------------------------------------------------- shared parts
@@ -181,10 +187,11 @@ __device__ __forceinline__ void split_terms(float4 v, uint2 (&out)[TERMS]) {
 // out[m][j] = f sum_c in[m][c] W(j, c), f = scale[a] or 1; W(j, c) = w[a][j][c]
 // (TRANS false: A) or w[a][c][j] (TRANS true: B, an operand whose rows run
 // along the contraction).  One block per row tile and slice of the contracted
-// dimension: TMA gathers the tile's rows by number, 64 columns a stage, and
-// brings the weight's box beside them; one thread issues tcgen05.mma (M = 128,
-// N = RT, sums in tensor memory), so that reading the rows costs the SM no
-// instructions.  The blocks of a cluster hold the slices of one tile and add
+// dimension: TMA brings the tile's rows, 64 columns a stage -- one box where
+// they are neighbours, four rows by number at a time where they are scattered
+// (110 MB of rows: 43 us against 72) -- and the weight's box beside them; one
+// thread issues tcgen05.mma (M = 128, N = RT, sums in tensor memory), so that
+// reading the rows costs the SM no instructions.  The blocks of a cluster hold the slices of one tile and add
 // their partial sums through distributed shared memory in a fixed order.  The
 // forward pass stores t by row in fp32; the backward pass stores dt, and beside
 // it t, as bf16 terms by tile, 128 rows each with zeros past the tile's last:
@@ -218,6 +225,7 @@ struct ContractSmem {
 template <int RT, bool TRANS, int TERMS>
 __global__ void __launch_bounds__(kContractThreads)
     lora_contract_kernel(const __grid_constant__ CUtensorMap tm_in,
+                         const __grid_constant__ CUtensorMap tm_rows,
                          const __grid_constant__ CUtensorMap tm_w, const ContractArgs p) {
   using S = ContractSmem<RT>;
   constexpr int STAGES = S::kStages;
@@ -243,6 +251,7 @@ __global__ void __launch_bounds__(kContractThreads)
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tm_in);
+    prefetch_tmap(&tm_rows);
     prefetch_tmap(&tm_w);
   }
   if (warp == 1) {
@@ -270,11 +279,13 @@ __global__ void __launch_bounds__(kContractThreads)
     const int steps = c_hi > c_lo ? (c_hi - c_lo + 63) / 64 : 0;
     if (warp == 0) {
       // ---------------------------------------------------------- producer
-      // Lane l brings rows 4 l .. 4 l + 3; groups past the tile's last row are
-      // left out (what stands there only meets sums that are not stored).
-      const bool brings = 4 * lane < count;
+      // Scattered: lane l brings rows 4 l .. 4 l + 3; groups past the tile's
+      // last row are left out.  Whatever stands in a row past the last only
+      // meets sums that are not stored.
+      const bool run = tile.w != 0;
+      const bool brings = !run && 4 * lane < count;
       const int4 rows = *reinterpret_cast<const int4 *>(rec + 4 + 4 * lane);
-      const uint32_t bytes = (count + 3) / 4 * 512 + S::kW;
+      const uint32_t bytes = (run ? S::kIn : (count + 3) / 4 * 512) + S::kW;
       uint32_t armed = 0, armed_parity = 0;
       for (int step = 0; step < steps; ++step) {
         const int st = step % STAGES;
@@ -286,6 +297,7 @@ __global__ void __launch_bounds__(kContractThreads)
           ok = bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
           if (ok) {
             mbar_arrive_expect_tx(&full[st], bytes);
+            if (run) tma_load_2d(in, &tm_in, &full[st], c0, rows.x);
             if constexpr (!TRANS) {
               tma_load_3d(in + S::kIn, &tm_w, &full[st], c0, 0, bin);
             } else {
@@ -298,7 +310,7 @@ __global__ void __launch_bounds__(kContractThreads)
           }
         }
         if (!__shfl_sync(~0u, ok, 0)) break;
-        if (brings) tma_gather4(in + lane * 512, &tm_in, &full[st], c0, rows);
+        if (brings) tma_gather4(in + lane * 512, &tm_rows, &full[st], c0, rows);
         __syncwarp();
       }
       // never leave with a copy in flight into this block's shared memory
@@ -406,10 +418,12 @@ __global__ void __launch_bounds__(kContractThreads)
 // false: B, t fp32 by row) or w[a][j][c] (TRANS true: A, t bf16 by tile).
 // Persistent blocks, one per SM, take equal shares of the units (row tile, slab
 // of 128 columns), neighbouring slabs of a tile in a row, so that t is loaded
-// once for many slabs.  Base goes from memory into registers one unit ahead and
-// the result from registers to memory, 16 bytes a thread: the columns of a slab
-// are dealt to the product's columns so that the eight that a thread holds of a
-// row in four accumulator tiles are neighbours.  Column 32 b + 8 c + 2 j + e is
+// once for many slabs.  Every thread copies the pieces of base that it will
+// add to, 16 bytes each, asynchronously into slots of its own some units ahead
+// (nobody else reads them, so they need no barrier), and writes its sums back
+// in 16-byte pieces: the columns of a slab are dealt to the product's columns
+// so that the eight that a thread holds of a row in four accumulator tiles are
+// neighbours.  Column 32 b + 8 c + 2 j + e is
 // column 2 c + e of tile 4 b + j; the weight slab is permuted accordingly on
 // its way into shared memory.  Rows without an adapter are copied from base
 // (left alone when out is base).
@@ -429,17 +443,22 @@ struct ExpandArgs {
 };
 
 constexpr int kExpandThreads = 512;
-constexpr int kSlab = 128;
 
 template <int RT, bool TRANS, bool F32>
 struct ExpandSmem {
   static constexpr int kTerms = F32 ? 3 : 1;  // bf16 terms of t
+  static constexpr int kSlab = F32 || RT > 64 ? 64 : 128;  // columns of a unit
   static constexpr int kTRow = RT * 2 + 16;
   static constexpr int kT = kTerms * kTileRows * kTRow;
   static constexpr int kWRow = TRANS ? kSlab * 2 + 16 : RT * 2 + 16;
   static constexpr int kW = TRANS ? RT * kWRow : kSlab * kWRow;
-  static constexpr int kStages = 3;
-  static constexpr int kBytes = kT + kStages * kW;
+  static constexpr int kPieces = kTileRows * kSlab * (F32 ? 4 : 2) / 16 / kExpandThreads;
+  static constexpr int kBase = kPieces * kExpandThreads * 16;
+  static constexpr int kStage = kW + kBase;
+  static constexpr int kFit = (224 * 1024 - kT) / kStage;
+  static constexpr int kStages = kFit > 4 ? 4 : kFit;
+  static constexpr int kBytes = kT + kStages * kStage;
+  static_assert(kStages >= 2, "one unit ahead at least");
   static_assert(kBytes <= 232448, "dynamic shared memory above the per-block limit");
 };
 
@@ -447,37 +466,62 @@ template <int RT, bool TRANS, bool F32>
 __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const ExpandArgs p) {
   using S = ExpandSmem<RT, TRANS, F32>;
   constexpr int E = F32 ? 4 : 2;
-  constexpr int Q = F32 ? 2 : 1;     // 16-byte pieces of eight columns
+  constexpr int Q = F32 ? 2 : 1;       // 16-byte pieces of eight columns
+  constexpr int SLAB = S::kSlab;
+  constexpr int NB = SLAB / 64;        // blocks of 32 columns of a warp
   constexpr int KK = RT / 16;
+  static_assert(S::kPieces == 2 * NB * Q, "a thread's share of a unit");
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sm = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int wm = warp & 7, wn = warp >> 3;  // 16 rows, 64 columns
+  const int wm = warp & 7, wn = warp >> 3;  // 16 rows, half of the slab
   const int g = lane >> 2, c8 = (lane & 3) * 8;
 
   // base, weights and plan were complete before the kernel ahead of this one
   // began; only its own output, t, has to be waited for
   const int32_t *recs = p.plan + plan_recs_at(p.L);
-  const int slabs = (p.C + kSlab - 1) / kSlab;
+  const int slabs = (p.C + SLAB - 1) / SLAB;
   const bool fits = plan_fits(p.plan, p.M, p.L, p.status);
-  const int64_t units = fits ? static_cast<int64_t>(p.plan[3]) * slabs : 0;
+  const int tiles = fits ? p.plan[3] : 0;
+  const int64_t units = static_cast<int64_t>(tiles) * slabs;
   const int64_t u_lo = units * blockIdx.x / gridDim.x;
   const int mine = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x - u_lo);
   const bool in_place = p.base == p.out;
+  const int tile0 = static_cast<int>(u_lo / slabs), slab0 = static_cast<int>(u_lo % slabs);
 
-  // weights of a unit -> its stage
-  int w_tile = static_cast<int>(u_lo / slabs), w_slab = static_cast<int>(u_lo % slabs);
-  const int tile0 = w_tile, slab0 = w_slab;
-  int w_bin = mine > 0 ? recs[static_cast<int64_t>(w_tile) * kRecWords] : 0;
-  auto load_w = [&](int stage) {
-    if (w_bin < p.L) {
-      const uint16_t *w = p.w + static_cast<int64_t>(w_bin) * p.R * p.C;
-      const uint32_t sw = sm + S::kT + stage * S::kW;
-      const int c0 = w_slab * kSlab;
+  // A unit's weights and base -> its stage.  The thread's rows of base are
+  // wm 16 + g (+ 8), its columns wn SLAB/2 + 32 b + c8 .. + 7.
+  int l_tile = tile0, l_slab = slab0, l_bin = 0, l_count = 0;
+  int32_t l_row[2] = {0, 0};
+  auto next_tile = [&]() {
+    const int32_t *rec = recs + static_cast<int64_t>(l_tile) * kRecWords;
+    l_bin = rec[0];
+    l_count = rec[1];
+    l_row[0] = rec[4 + wm * 16 + g];
+    l_row[1] = rec[4 + wm * 16 + g + 8];
+  };
+  auto load = [&](int stage) {
+    const uint32_t sw = sm + S::kT + stage * S::kStage;
+    const int c0 = l_slab * SLAB;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int col = c0 + wn * (SLAB / 2) + b * 32 + c8;
+        const bool ok = p.base != nullptr && wm * 16 + g + h * 8 < l_count && col < p.C;
+        const uint8_t *src = static_cast<const uint8_t *>(p.base) +
+                             (l_row[h] * p.ld_base + col) * E;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          cp_async16(sw + S::kW + (((h * NB + b) * Q + q) * kExpandThreads + tid) * 16,
+                     ok ? src + q * 16 : reinterpret_cast<const uint8_t *>(p.w), ok);
+      }
+    if (l_bin < p.L) {
+      const uint16_t *w = p.w + static_cast<int64_t>(l_bin) * p.R * p.C;
       if constexpr (!TRANS) {
         constexpr int PER = RT / 8;
 #pragma unroll
-        for (int k = tid; k < kSlab * PER; k += kExpandThreads) {
+        for (int k = tid; k < SLAB * PER; k += kExpandThreads) {
           const int r = k / PER, cc = k % PER;
           const int at = (r & ~31) | (((r >> 1) & 3) << 3) | (((r >> 3) & 3) << 1) | (r & 1);
           const bool ok = c0 + r < p.C && cc * 8 < p.R;
@@ -485,7 +529,7 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const Expan
                      ok ? w + static_cast<int64_t>(c0 + r) * p.R + cc * 8 : w, ok);
         }
       } else {
-        constexpr int PER = kSlab / 2;  // pairs of columns
+        constexpr int PER = SLAB / 2;  // pairs of columns
 #pragma unroll 8
         for (int k = tid; k < RT * PER; k += kExpandThreads) {
           const int r = k / PER, cc = k % PER;
@@ -496,53 +540,21 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const Expan
         }
       }
     }
-    if (++w_slab == slabs) {
-      w_slab = 0;
-      ++w_tile;
-      if (w_tile < p.plan[3]) w_bin = recs[static_cast<int64_t>(w_tile) * kRecWords];
+    if (++l_slab == slabs) {
+      l_slab = 0;
+      if (++l_tile < tiles) next_tile();
     }
   };
 
-  // base of a unit -> registers: this thread's rows wm 16 + g (+ 8), columns
-  // wn 64 + 32 b + c8 .. + 7
-  int b_tile = tile0, b_slab = slab0, b_count = 0;
-  int32_t b_row[2] = {0, 0};
-  auto base_rows = [&]() {
-    const int32_t *rec = recs + static_cast<int64_t>(b_tile) * kRecWords;
-    b_count = rec[1];
-    b_row[0] = rec[4 + wm * 16 + g];
-    b_row[1] = rec[4 + wm * 16 + g + 8];
-  };
-  uint4 next[2][2][Q];
-  auto load_base = [&]() {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int col = b_slab * kSlab + wn * 64 + b * 32 + c8;
-        const bool ok = p.base != nullptr && wm * 16 + g + h * 8 < b_count && col < p.C;
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            static_cast<const uint8_t *>(p.base) + (b_row[h] * p.ld_base + col) * E);
-#pragma unroll
-        for (int q = 0; q < Q; ++q) next[h][b][q] = ok ? src[q] : make_uint4(0, 0, 0, 0);
-      }
-    if (++b_slab == slabs) {
-      b_slab = 0;
-      ++b_tile;
-      if (b_tile < p.plan[3]) base_rows();
-    }
-  };
-
-  if (mine > 0) base_rows();
+  if (mine > 0) next_tile();
 #pragma unroll
   for (int s = 0; s < S::kStages - 1; ++s) {
-    if (s < mine) load_w(s);
+    if (s < mine) load(s);
     cp_async_commit();
   }
-  if (mine > 0) load_base();
   grid_dependency_wait();
 
-  int tile = tile0, slab = slab0, bin = 0, count = 0;
+  int tile = tile0, slab = slab0, bin = 0, count = 0, stage = 0;
   int32_t row[2] = {0, 0};
   float f = 1.0f;
   bool fresh = true;
@@ -581,26 +593,19 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const Expan
         }
       }
     }
-    uint4 now[2][2][Q];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int q = 0; q < Q; ++q) now[h][b][q] = next[h][b][q];
     cp_async_wait<S::kStages - 2>();
     __syncthreads();
-    if (i + S::kStages - 1 < mine) load_w((i + S::kStages - 1) % S::kStages);
+    if (i + S::kStages - 1 < mine) load(stage == 0 ? S::kStages - 1 : stage - 1);
     cp_async_commit();
-    if (i + 1 < mine) load_base();
     if (wm * 16 < count && (bin < p.L || !in_place)) {
-      float acc[8][4];
+      const uint8_t *st = smem + S::kT + stage * S::kStage;
+      float acc[4 * NB][4];
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
+      for (int n = 0; n < 4 * NB; ++n)
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[n][k] = 0.0f;
       if (bin < p.L) {
-        const uint32_t sw = sm + S::kT + (i % S::kStages) * S::kW;
+        const uint32_t sw = smem_u32(st);
 #pragma unroll 1
         for (int s = S::kTerms - 1; s >= 0; --s) {  // the smallest terms first
 #pragma unroll
@@ -610,9 +615,9 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const Expan
                         (kk * 16 + (lane >> 4) * 8) * 2,
                     a);
 #pragma unroll
-            for (int n = 0; n < 8; n += 2) {
+            for (int n = 0; n < 4 * NB; n += 2) {
               uint32_t b[4];
-              const int col = wn * 64 + n * 8;
+              const int col = wn * (SLAB / 2) + n * 8;
               if constexpr (!TRANS)
                 ldsm_x4(sw + (col + (lane & 7) + ((lane >> 4) << 3)) * S::kWRow +
                             (kk * 16 + ((lane >> 3) & 1) * 8) * 2,
@@ -630,8 +635,8 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const Expan
       for (int h = 0; h < 2; ++h) {
         if (wm * 16 + g + h * 8 >= count) continue;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int col = slab * kSlab + wn * 64 + b * 32 + c8;
+        for (int b = 0; b < NB; ++b) {
+          const int col = slab * SLAB + wn * (SLAB / 2) + b * 32 + c8;
           if (col >= p.C || !store_ok(p.status, row[h] >= 0 && row[h] < p.M && col + 8 <= p.ld_out))
             continue;
           uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) +
@@ -639,10 +644,12 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const Expan
           uint32_t o[4 * Q];
 #pragma unroll
           for (int q = 0; q < Q; ++q) {
-            o[4 * q] = now[h][b][q].x;
-            o[4 * q + 1] = now[h][b][q].y;
-            o[4 * q + 2] = now[h][b][q].z;
-            o[4 * q + 3] = now[h][b][q].w;
+            const uint4 v = *reinterpret_cast<const uint4 *>(
+                st + S::kW + (((h * NB + b) * Q + q) * kExpandThreads + tid) * 16);
+            o[4 * q] = v.x;
+            o[4 * q + 1] = v.y;
+            o[4 * q + 2] = v.z;
+            o[4 * q + 3] = v.w;
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -660,6 +667,7 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const Expan
         }
       }
     }
+    if (++stage == S::kStages) stage = 0;
     fresh = ++slab == slabs;
     if (fresh) {
       slab = 0;
@@ -673,9 +681,10 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const Expan
 // out[a](c, j) = f sum_{m of a} src[m][c] v[m][j]: dB[a][n][j] (src dy, v t, f =
 // scale) and dA[a][j][k] (src x, v dt, f = 1, stored transposed).  One block
 // per adapter, slab of 128 columns c and share of the adapter's rows, 64 rows a
-// stage: TMA gathers the rows of src by number and brings v's box; both are
-// operands whose rows run along the contraction, M = 128 columns of src by N =
-// RT.  v is zero in the rows past a tile's last, where src repeats a row.  The
+// stage: TMA brings src's rows -- as a box where 64 neighbours are the
+// adapter's, else by number -- and v's box; both are operands whose rows run
+// along the contraction, M = 128 columns of src by N = RT.  v is zero in the
+// rows past a tile's last, where src repeats a row of the tile.  The
 // blocks of a cluster hold the shares and add them in a fixed order.  Rows are
 // taken from the last to the first: dy's last rows are what the contraction
 // before left in L2.
@@ -694,7 +703,7 @@ struct OuterArgs {
   int *status;
 };
 struct OuterMaps {
-  CUtensorMap src[2], v[2];
+  CUtensorMap src[2], rows[2], v[2];
 };
 
 constexpr int kOuterThreads = 128;
@@ -734,6 +743,7 @@ __global__ void __launch_bounds__(kOuterThreads)
   const bool second = static_cast<int>(blockIdx.x) >= p.slabs0;
   const OuterSide sd = second ? p.side[1] : p.side[0];
   const CUtensorMap *tm_src = second ? &maps.src[1] : &maps.src[0];
+  const CUtensorMap *tm_rows = second ? &maps.rows[1] : &maps.rows[0];
   const CUtensorMap *tm_v = second ? &maps.v[1] : &maps.v[0];
   const int c0 = (static_cast<int>(blockIdx.x) - (second ? p.slabs0 : 0)) * kOuterSlab;
 
@@ -746,6 +756,7 @@ __global__ void __launch_bounds__(kOuterThreads)
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(tm_src);
+    prefetch_tmap(tm_rows);
     prefetch_tmap(tm_v);
   }
   if (warp == 1) {
@@ -780,14 +791,15 @@ __global__ void __launch_bounds__(kOuterThreads)
       const bool brings = c0 + (lane >> 4) * 64 < sd.C;  // no box past the last column
       const uint32_t bytes = S::kV + (c0 + 64 < sd.C ? 2 : 1) * 8192;
       uint32_t armed = 0, armed_parity = 0;
+      int4 rows = make_int4(0, 0, 0, 0);
+      bool run = false;
       auto fetch = [&](int step) {
         const int s64 = all - 1 - (rank + step * shares);
-        return *reinterpret_cast<const int4 *>(
-            recs + static_cast<int64_t>(tile0 + s64 / 2) * kRecWords + 4 + (s64 & 1) * 64 +
-            (lane & 15) * 4);
+        const int32_t *rec = recs + static_cast<int64_t>(tile0 + s64 / 2) * kRecWords;
+        rows = *reinterpret_cast<const int4 *>(rec + 4 + (s64 & 1) * 64 + (lane & 15) * 4);
+        run = rec[3] != 0 && (s64 & 1) * 64 + kOuterRows <= rec[1];
       };
-      int4 rows = make_int4(0, 0, 0, 0);
-      if (steps > 0) rows = fetch(0);
+      if (steps > 0) fetch(0);
       for (int step = 0; step < steps; ++step) {
         const int st = step % STAGES;
         const uint32_t phase = (step / STAGES) & 1;
@@ -798,6 +810,10 @@ __global__ void __launch_bounds__(kOuterThreads)
           ok = bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
           if (ok) {
             mbar_arrive_expect_tx(&full[st], bytes);
+            if (run) {
+              tma_load_2d(src, tm_src, &full[st], c0, rows.x);
+              if (c0 + 64 < sd.C) tma_load_2d(src + 8192, tm_src, &full[st], c0 + 64, rows.x);
+            }
             const int vrow = tile0 * kTileRows + s64 * kOuterRows;
 #pragma unroll
             for (int q = 0; q < TERMS; ++q)
@@ -810,10 +826,10 @@ __global__ void __launch_bounds__(kOuterThreads)
           }
         }
         if (!__shfl_sync(~0u, ok, 0)) break;
-        if (brings)
-          tma_gather4(src + (lane >> 4) * 8192 + (lane & 15) * 512, tm_src, &full[st],
+        if (brings && !run)
+          tma_gather4(src + (lane >> 4) * 8192 + (lane & 15) * 512, tm_rows, &full[st],
                       c0 + (lane >> 4) * 64, rows);
-        if (step + 1 < steps) rows = fetch(step + 1);
+        if (step + 1 < steps) fetch(step + 1);
         __syncwarp();
       }
       if (lane == 0)
@@ -957,38 +973,40 @@ cudaError_t bf16_map(CUtensorMap *map, const void *ptr, int64_t d0, int64_t d1, 
 template <int RT, bool TRANS, int TERMS>
 cudaError_t run_contract(const uint16_t *in, int64_t ld, const uint16_t *w, const ContractArgs &a,
                          cudaStream_t stream) {
-  CUtensorMap tm_in, tm_w;
-  cudaError_t e = bf16_map(&tm_in, in, a.C, a.M, 0, ld, 1);
+  CUtensorMap tm_in, tm_rows, tm_w;
+  cudaError_t e = bf16_map(&tm_in, in, a.C, a.M, 0, ld, kTileRows);
+  if (e == cudaSuccess) e = bf16_map(&tm_rows, in, a.C, a.M, 0, ld, 1);
   if (e == cudaSuccess)
     e = TRANS ? bf16_map(&tm_w, w, a.R, a.C, a.L, a.R, 64)
               : bf16_map(&tm_w, w, a.C, a.R, a.L, a.C, RT);
   if (e != cudaSuccess) return e;
-  // Slices of the contracted dimension: enough blocks for two per SM, none
-  // shorter than 256 columns.
+  // Slices of the contracted dimension: as many blocks as run at once (two per
+  // SM), none shorter than 256 columns.
   int slices = 1;
-  while (slices < 8 && a.max_tiles * slices < 2 * sm_count() && a.C >= 256 * slices * 2)
+  while (slices < 8 && a.max_tiles * slices * 2 <= 2 * sm_count() && a.C >= 256 * slices * 2)
     slices *= 2;
   return launch<lora_contract_kernel<RT, TRANS, TERMS>>(
       dim3(static_cast<unsigned>(a.max_tiles), slices), kContractThreads,
-      ContractSmem<RT>::kBytes, slices, 1, stream, tm_in, tm_w, a);
+      ContractSmem<RT>::kBytes, slices, 1, stream, tm_in, tm_rows, tm_w, a);
 }
 
 template <int RT, bool TRANS, bool F32>
 cudaError_t run_expand(const ExpandArgs &a, cudaStream_t stream) {
-  const int64_t units = plan_max_tiles(a.M, a.L) * ((a.C + kSlab - 1) / kSlab);
+  using S = ExpandSmem<RT, TRANS, F32>;
+  const int64_t units = plan_max_tiles(a.M, a.L) * ((a.C + S::kSlab - 1) / S::kSlab);
   const int sms = sm_count();
   return launch<lora_expand_kernel<RT, TRANS, F32>>(
-      dim3(static_cast<unsigned>(units < sms ? units : sms)), kExpandThreads,
-      ExpandSmem<RT, TRANS, F32>::kBytes, 1, 0, stream, a);
+      dim3(static_cast<unsigned>(units < sms ? units : sms)), kExpandThreads, S::kBytes, 1, 0,
+      stream, a);
 }
 
 template <int RT, int TERMS>
 cudaError_t run_outer(const OuterMaps &maps, const OuterArgs &a, cudaStream_t stream) {
   const int slabs = a.slabs0 + (a.side[1].C + kOuterSlab - 1) / kOuterSlab;
-  // Shares of an adapter's rows: enough blocks for two per SM, none with fewer
-  // than two stages on average.
+  // Shares of an adapter's rows: as many blocks as run at once (two per SM),
+  // none with fewer than two stages on average.
   int shares = 1;
-  while (shares < 8 && static_cast<int64_t>(slabs) * a.L * shares < 2 * sm_count() &&
+  while (shares < 8 && static_cast<int64_t>(slabs) * a.L * shares * 2 <= 2 * sm_count() &&
          a.M / a.L >= 2 * kOuterRows * shares * 2)
     shares *= 2;
   return launch<lora_outer_kernel<RT, TERMS>>(dim3(slabs, a.L, shares), kOuterThreads,
@@ -1038,8 +1056,10 @@ cudaError_t run_backward(const LoraRequest &q, cudaStream_t stream) {
     o.R = q.R;
     o.L = q.L;
     o.status = q.status;
-    e = bf16_map(&maps.src[0], q.dy, N, q.M, 0, q.lddy, 1);
-    if (e == cudaSuccess) e = bf16_map(&maps.src[1], q.x, K, q.M, 0, q.ldx, 1);
+    e = bf16_map(&maps.src[0], q.dy, N, q.M, 0, q.lddy, kOuterRows);
+    if (e == cudaSuccess) e = bf16_map(&maps.src[1], q.x, K, q.M, 0, q.ldx, kOuterRows);
+    if (e == cudaSuccess) e = bf16_map(&maps.rows[0], q.dy, N, q.M, 0, q.lddy, 1);
+    if (e == cudaSuccess) e = bf16_map(&maps.rows[1], q.x, K, q.M, 0, q.ldx, 1);
     if (e == cudaSuccess) e = bf16_map(&maps.v[0], vt, q.R, rows, TERMS, q.R, kOuterRows);
     if (e == cudaSuccess) e = bf16_map(&maps.v[1], vdt, q.R, rows, TERMS, q.R, kOuterRows);
     if (e == cudaSuccess)
