@@ -172,6 +172,62 @@ __global__ void __launch_bounds__(kPlanWarps * 32) lora_plan_kernel(
 }
 
 // ----------------------------------------------------------------- shared parts
+// Byte offset of 16-byte chunk c (0..7) of row r in a tile of 128-byte rows with
+// 128-byte swizzling, as TMA writes it and tcgen05 reads it.
+__device__ __forceinline__ uint32_t swz128(int r, int c) {
+  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+// Scattered rows come by plain asynchronous copies of a whole warp; their
+// arrival is announced two stages late, when the next two stages' copies are
+// already under way.  (TMA can gather four rows by number, but 110 MB of rows
+// took 72 us that way, against 43 us in boxes.)
+struct LateArrival {
+  uint64_t *older = nullptr, *newer = nullptr;  // stages whose copies are under way
+  template <int KEEP>
+  __device__ __forceinline__ void arrive(int lane, uint64_t *bar) {
+    if (bar == nullptr) return;
+    cp_async_wait<KEEP>();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  }
+  // this stage's copies were just committed
+  __device__ __forceinline__ void push(int lane, uint64_t *bar) {
+    arrive<2>(lane, older);
+    older = newer;
+    newer = bar;
+  }
+  __device__ __forceinline__ void catch_up(int lane) {
+    arrive<1>(lane, older);
+    arrive<0>(lane, newer);
+    older = newer = nullptr;
+  }
+};
+
+// Sum over blocks lo .. hi (at most 8) of a cluster of the four floats at
+// `at`(block) in each one's `part`, in block order, all loads in flight at once.
+template <typename At>
+__device__ __forceinline__ float4 cluster_sum(cg::cluster_group &cluster, float *part, int lo,
+                                              int hi, At &&at) {
+  float4 v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (lo + k <= hi)
+      v[k] = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(part, lo + k) + at(lo + k));
+  }
+  float4 s = v[0];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) {
+    s.x += v[k].x;
+    s.y += v[k].y;
+    s.z += v[k].z;
+    s.w += v[k].w;
+  }
+  return s;
+}
+
 // v as TERMS bf16 values whose sum has 8 TERMS significant bits, packed in pairs.
 template <int TERMS>
 __device__ __forceinline__ void split_terms(float4 v, uint2 (&out)[TERMS]) {
@@ -187,16 +243,17 @@ __device__ __forceinline__ void split_terms(float4 v, uint2 (&out)[TERMS]) {
 // out[m][j] = f sum_c in[m][c] W(j, c), f = scale[a] or 1; W(j, c) = w[a][j][c]
 // (TRANS false: A) or w[a][c][j] (TRANS true: B, an operand whose rows run
 // along the contraction).  One block per row tile and slice of the contracted
-// dimension: TMA brings the tile's rows, 64 columns a stage -- one box where
-// they are neighbours, four rows by number at a time where they are scattered
-// (110 MB of rows: 43 us against 72) -- and the weight's box beside them; one
-// thread issues tcgen05.mma (M = 128, N = RT, sums in tensor memory), so that
-// reading the rows costs the SM no instructions.  The blocks of a cluster hold the slices of one tile and add
+// dimension: TMA brings the tile's rows as a box, 64 columns a stage, where they
+// are neighbours (else a warp copies them), and the weight's box beside them;
+// one thread issues tcgen05.mma (M = 128, N = RT, sums in tensor memory), so that
+// reading the rows costs the SM next to no instructions.  The blocks of a cluster hold the slices of one tile and add
 // their partial sums through distributed shared memory in a fixed order.  The
 // forward pass stores t by row in fp32; the backward pass stores dt, and beside
 // it t, as bf16 terms by tile, 128 rows each with zeros past the tile's last:
 // the operand that the outer products and dx read.
 struct ContractArgs {
+  const uint16_t *in;  // as tm_in
+  int64_t ld;
   const float *scale;  // nullptr: 1
   const int32_t *plan;
   float *out;             // forward: t [M][R]
@@ -225,7 +282,6 @@ struct ContractSmem {
 template <int RT, bool TRANS, int TERMS>
 __global__ void __launch_bounds__(kContractThreads)
     lora_contract_kernel(const __grid_constant__ CUtensorMap tm_in,
-                         const __grid_constant__ CUtensorMap tm_rows,
                          const __grid_constant__ CUtensorMap tm_w, const ContractArgs p) {
   using S = ContractSmem<RT>;
   constexpr int STAGES = S::kStages;
@@ -243,25 +299,13 @@ __global__ void __launch_bounds__(kContractThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    mbar_init(done, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
     prefetch_tmap(&tm_in);
-    prefetch_tmap(&tm_rows);
     prefetch_tmap(&tm_w);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, RT);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();
   grid_dependency_launch();
 
@@ -272,6 +316,20 @@ __global__ void __launch_bounds__(kContractThreads)
   if (plan_fits(p.plan, p.M, p.L, p.status) && static_cast<int>(blockIdx.x) < p.plan[3])
     tile = *reinterpret_cast<const int4 *>(rec);
   const int bin = tile.x, count = tile.y;
+  const bool run = tile.w != 0;  // neighbouring rows
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], run ? 1 : 2);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   if (bin < p.L) {
     const int slice = ((p.C + slices - 1) / slices + 63) / 64 * 64;
     const int c_lo = rank * slice;
@@ -279,14 +337,15 @@ __global__ void __launch_bounds__(kContractThreads)
     const int steps = c_hi > c_lo ? (c_hi - c_lo + 63) / 64 : 0;
     if (warp == 0) {
       // ---------------------------------------------------------- producer
-      // Scattered: lane l brings rows 4 l .. 4 l + 3; groups past the tile's
-      // last row are left out.  Whatever stands in a row past the last only
-      // meets sums that are not stored.
-      const bool run = tile.w != 0;
-      const bool brings = !run && 4 * lane < count;
-      const int4 rows = *reinterpret_cast<const int4 *>(rec + 4 + 4 * lane);
-      const uint32_t bytes = (run ? S::kIn : (count + 3) / 4 * 512) + S::kW;
+      // Rows past the tile's last are the next ones of a box, or left out:
+      // what stands there only meets sums that are not stored.
+      const int first = rec[4];
+      int32_t rows[kTileRows / 4];  // scattered: this lane copies rows 4 i + lane / 8
+#pragma unroll
+      for (int i = 0; i < kTileRows / 4; ++i) rows[i] = run ? 0 : rec[4 + i * 4 + (lane >> 3)];
+      const uint32_t bytes = (run ? S::kIn : 0) + S::kW;
       uint32_t armed = 0, armed_parity = 0;
+      LateArrival late;
       for (int step = 0; step < steps; ++step) {
         const int st = step % STAGES;
         const uint32_t phase = (step / STAGES) & 1;
@@ -297,7 +356,7 @@ __global__ void __launch_bounds__(kContractThreads)
           ok = bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
           if (ok) {
             mbar_arrive_expect_tx(&full[st], bytes);
-            if (run) tma_load_2d(in, &tm_in, &full[st], c0, rows.x);
+            if (run) tma_load_2d(in, &tm_in, &full[st], c0, first);
             if constexpr (!TRANS) {
               tma_load_3d(in + S::kIn, &tm_w, &full[st], c0, 0, bin);
             } else {
@@ -310,10 +369,24 @@ __global__ void __launch_bounds__(kContractThreads)
           }
         }
         if (!__shfl_sync(~0u, ok, 0)) break;
-        if (brings) tma_gather4(in + lane * 512, &tm_rows, &full[st], c0, rows);
-        __syncwarp();
+        if (!run) {
+          const int c = lane & 7, col = c0 + c * 8;
+          const bool in_cols = col < p.C;
+          const uint32_t to = smem_u32(in);
+#pragma unroll
+          for (int i = 0; i < kTileRows / 4; ++i) {
+            if (i * 4 >= count) break;
+            const int r = i * 4 + (lane >> 3);
+            if (r < count)
+              cp_async16(to + swz128(r, c), p.in + rows[i] * p.ld + (in_cols ? col : 0), in_cols);
+          }
+          cp_async_commit();
+          late.push(lane, &full[st]);
+        }
       }
+      late.catch_up(lane);
       // never leave with a copy in flight into this block's shared memory
+      cp_async_wait<0>();
       if (lane == 0)
         for (int s = 0; s < STAGES; ++s)
           if (armed & (1u << s)) mbar_wait(&full[s], (armed_parity >> s) & 1u, kBoundedWaitNs);
@@ -370,14 +443,8 @@ __global__ void __launch_bounds__(kContractThreads)
       const int r = e / quads, j = (e - r * quads) * 4;
       float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (TERMS == 0 || r < count) {
-        for (int q = 0; q < slices; ++q) {
-          const float *src = slices > 1 ? cluster.map_shared_rank(part, q) : part;
-          const float4 v = *reinterpret_cast<const float4 *>(src + r * PS + j);
-          s.x += v.x;
-          s.y += v.y;
-          s.z += v.z;
-          s.w += v.w;
-        }
+        s = slices > 1 ? cluster_sum(cluster, part, 0, slices - 1, [&](int) { return r * PS + j; })
+                       : *reinterpret_cast<const float4 *>(part + r * PS + j);
         s = make_float4(f * s.x, f * s.y, f * s.z, f * s.w);
       }
       const int row = rec[4 + r];
@@ -423,7 +490,8 @@ __global__ void __launch_bounds__(kContractThreads)
 // (nobody else reads them, so they need no barrier), and writes its sums back
 // in 16-byte pieces: the columns of a slab are dealt to the product's columns
 // so that the eight that a thread holds of a row in four accumulator tiles are
-// neighbours.  Column 32 b + 8 c + 2 j + e is
+// neighbours.  The products add onto base in the accumulators (the scale is in
+// t), so that an element costs its two conversions and no arithmetic.  Column 32 b + 8 c + 2 j + e is
 // column 2 c + e of tile 4 b + j; the weight slab is permuted accordingly on
 // its way into shared memory.  Rows without an adapter are copied from base
 // (left alone when out is base).
@@ -491,52 +559,60 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const Expan
 
   // A unit's weights and base -> its stage.  The thread's rows of base are
   // wm 16 + g (+ 8), its columns wn SLAB/2 + 32 b + c8 .. + 7.
-  int l_tile = tile0, l_slab = slab0, l_bin = 0, l_count = 0;
-  int32_t l_row[2] = {0, 0};
+  const int my_col = wn * (SLAB / 2) + c8;
+  int l_tile = tile0, l_slab = slab0;
+  const uint8_t *l_base[2] = {nullptr, nullptr};  // nullptr: zeros
+  const uint16_t *l_w = nullptr;                  // nullptr: no adapter
   auto next_tile = [&]() {
     const int32_t *rec = recs + static_cast<int64_t>(l_tile) * kRecWords;
-    l_bin = rec[0];
-    l_count = rec[1];
-    l_row[0] = rec[4 + wm * 16 + g];
-    l_row[1] = rec[4 + wm * 16 + g + 8];
+    const int bin = rec[0], count = rec[1];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = wm * 16 + g + h * 8;
+      l_base[h] = p.base != nullptr && r < count
+                      ? static_cast<const uint8_t *>(p.base) +
+                            (rec[4 + r] * p.ld_base + l_slab * SLAB + my_col) * E
+                      : nullptr;
+    }
+    l_w = bin < p.L ? p.w + static_cast<int64_t>(bin) * p.R * p.C : nullptr;
   };
   auto load = [&](int stage) {
     const uint32_t sw = sm + S::kT + stage * S::kStage;
-    const int c0 = l_slab * SLAB;
+    const uint32_t sb = sw + S::kW + tid * 16;
+    const int left = p.C - l_slab * SLAB;  // columns from this slab on
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int col = c0 + wn * (SLAB / 2) + b * 32 + c8;
-        const bool ok = p.base != nullptr && wm * 16 + g + h * 8 < l_count && col < p.C;
-        const uint8_t *src = static_cast<const uint8_t *>(p.base) +
-                             (l_row[h] * p.ld_base + col) * E;
+        const bool ok = l_base[h] != nullptr && my_col + b * 32 < left;
+        const uint8_t *src = ok ? l_base[h] + b * 32 * E : reinterpret_cast<const uint8_t *>(p.w);
 #pragma unroll
         for (int q = 0; q < Q; ++q)
-          cp_async16(sw + S::kW + (((h * NB + b) * Q + q) * kExpandThreads + tid) * 16,
-                     ok ? src + q * 16 : reinterpret_cast<const uint8_t *>(p.w), ok);
+          cp_async16(sb + ((h * NB + b) * Q + q) * kExpandThreads * 16, ok ? src + q * 16 : src, ok);
       }
-    if (l_bin < p.L) {
-      const uint16_t *w = p.w + static_cast<int64_t>(l_bin) * p.R * p.C;
+      if (l_base[h] != nullptr) l_base[h] += SLAB * E;
+    }
+    if (l_w != nullptr) {
       if constexpr (!TRANS) {
         constexpr int PER = RT / 8;
+        const uint16_t *w = l_w + static_cast<int64_t>(l_slab) * SLAB * p.R;
 #pragma unroll
         for (int k = tid; k < SLAB * PER; k += kExpandThreads) {
           const int r = k / PER, cc = k % PER;
           const int at = (r & ~31) | (((r >> 1) & 3) << 3) | (((r >> 3) & 3) << 1) | (r & 1);
-          const bool ok = c0 + r < p.C && cc * 8 < p.R;
-          cp_async16(sw + at * S::kWRow + cc * 16,
-                     ok ? w + static_cast<int64_t>(c0 + r) * p.R + cc * 8 : w, ok);
+          const bool ok = r < left && cc * 8 < p.R;
+          cp_async16(sw + at * S::kWRow + cc * 16, ok ? w + r * p.R + cc * 8 : p.w, ok);
         }
       } else {
         constexpr int PER = SLAB / 2;  // pairs of columns
+        const uint16_t *w = l_w + l_slab * SLAB;
 #pragma unroll 8
         for (int k = tid; k < RT * PER; k += kExpandThreads) {
           const int r = k / PER, cc = k % PER;
           const int at = (cc & ~15) | ((cc & 3) << 2) | ((cc >> 2) & 3);
-          const bool ok = r < p.R && c0 + cc * 2 < p.C;
+          const bool ok = r < p.R && cc * 2 < left;
           cp_async4(sw + r * S::kWRow + at * 4,
-                    ok ? w + static_cast<int64_t>(r) * p.C + c0 + cc * 2 : w, ok);
+                    ok ? w + static_cast<int64_t>(r) * p.C + cc * 2 : p.w, ok);
         }
       }
     }
@@ -555,19 +631,23 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const Expan
   grid_dependency_wait();
 
   int tile = tile0, slab = slab0, bin = 0, count = 0, stage = 0;
-  int32_t row[2] = {0, 0};
-  float f = 1.0f;
+  uint8_t *dst[2] = {nullptr, nullptr};  // nullptr: no row
   bool fresh = true;
   for (int i = 0; i < mine; ++i) {
     if (fresh) {
       const int32_t *rec = recs + static_cast<int64_t>(tile) * kRecWords;
       bin = rec[0];
       count = rec[1];
-      row[0] = rec[4 + wm * 16 + g];
-      row[1] = rec[4 + wm * 16 + g + 8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = wm * 16 + g + h * 8, row = rec[4 + r];
+        dst[h] = r < count && store_ok(p.status, row >= 0 && row < p.M)
+                     ? static_cast<uint8_t *>(p.out) + (row * p.ld_out + slab * SLAB + my_col) * E
+                     : nullptr;
+      }
       if (i > 0) __syncthreads();  // the last tile's t is no longer read
       if (bin < p.L) {
-        f = p.scale ? p.scale[bin] : 1.0f;
+        const float f = p.scale ? p.scale[bin] : 1.0f;
         if constexpr (TRANS) {
           for (int k = tid; k < kTileRows * (RT / 8); k += kExpandThreads) {
             const int r = k / (RT / 8), cc = k % (RT / 8);
@@ -584,6 +664,7 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const Expan
             if (r < count && cc * 4 < p.R)
               v = *reinterpret_cast<const float4 *>(
                   p.t + static_cast<int64_t>(rec[4 + r]) * p.R + cc * 4);
+            v = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
             uint2 o[S::kTerms];
             split_terms<S::kTerms>(v, o);
 #pragma unroll
@@ -601,9 +682,24 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const Expan
       const uint8_t *st = smem + S::kT + stage * S::kStage;
       float acc[4 * NB][4];
 #pragma unroll
-      for (int n = 0; n < 4 * NB; ++n)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[n][k] = 0.0f;
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(
+                st + S::kW + (((h * NB + b) * Q + q) * kExpandThreads + tid) * 16);
+            const uint32_t o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if constexpr (F32) {
+                acc[b * 4 + q * 2 + j / 2][2 * h + j % 2] = __uint_as_float(o[j]);
+              } else {
+                acc[b * 4 + j][2 * h] = bf16_lo(o[j]);
+                acc[b * 4 + j][2 * h + 1] = bf16_hi(o[j]);
+              }
+            }
+          }
       if (bin < p.L) {
         const uint32_t sw = smem_u32(st);
 #pragma unroll 1
@@ -631,42 +727,32 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const Expan
           }
         }
       }
+      const int left = p.C - slab * SLAB;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (wm * 16 + g + h * 8 >= count) continue;
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const int col = slab * SLAB + wn * (SLAB / 2) + b * 32 + c8;
-          if (col >= p.C || !store_ok(p.status, row[h] >= 0 && row[h] < p.M && col + 8 <= p.ld_out))
-            continue;
-          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) +
-                                                 (row[h] * p.ld_out + col) * E);
+          if (dst[h] == nullptr || my_col + b * 32 >= left) continue;
           uint32_t o[4 * Q];
-#pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(
-                st + S::kW + (((h * NB + b) * Q + q) * kExpandThreads + tid) * 16);
-            o[4 * q] = v.x;
-            o[4 * q + 1] = v.y;
-            o[4 * q + 2] = v.z;
-            o[4 * q + 3] = v.w;
-          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float x = acc[b * 4 + j][2 * h], y = acc[b * 4 + j][2 * h + 1];
             if constexpr (F32) {
-              o[2 * j] = __float_as_uint(fmaf(f, x, __uint_as_float(o[2 * j])));
-              o[2 * j + 1] = __float_as_uint(fmaf(f, y, __uint_as_float(o[2 * j + 1])));
+              o[2 * j] = __float_as_uint(x);
+              o[2 * j + 1] = __float_as_uint(y);
             } else {
-              o[j] = bf16x2(fmaf(f, x, bf16_lo(o[j])), fmaf(f, y, bf16_hi(o[j])));
+              o[j] = bf16x2(x, y);
             }
           }
+          uint4 *to = reinterpret_cast<uint4 *>(dst[h] + b * 32 * E);
 #pragma unroll
           for (int q = 0; q < Q; ++q)
-            dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            to[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
-      }
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (dst[h] != nullptr) dst[h] += SLAB * E;
     if (++stage == S::kStages) stage = 0;
     fresh = ++slab == slabs;
     if (fresh) {
@@ -679,34 +765,37 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const Expan
 
 // ---------------------------------------------------------------------- outer
 // out[a](c, j) = f sum_{m of a} src[m][c] v[m][j]: dB[a][n][j] (src dy, v t, f =
-// scale) and dA[a][j][k] (src x, v dt, f = 1, stored transposed).  One block
-// per adapter, slab of 128 columns c and share of the adapter's rows, 64 rows a
-// stage: TMA brings src's rows -- as a box where 64 neighbours are the
-// adapter's, else by number -- and v's box; both are operands whose rows run
-// along the contraction, M = 128 columns of src by N = RT.  v is zero in the
-// rows past a tile's last, where src repeats a row of the tile.  The
-// blocks of a cluster hold the shares and add them in a fixed order.  Rows are
-// taken from the last to the first: dy's last rows are what the contraction
-// before left in L2.
+// scale) and dA[a][j][k] (src x, v dt, f = 1, stored transposed).  A cluster
+// takes a slab of 128 columns c; its blocks take equal shares of the row tiles
+// of all adapters in order, 64 rows a stage: src's rows as a TMA box where 64
+// neighbours are the adapter's (else a warp copies them) and v's box; both are
+// operands whose rows run along the contraction, M = 128 columns of src by N =
+// RT, sums in tensor memory, one buffer in use and one being stored.  v is zero
+// in the rows past a tile's last, where src repeats a row of the tile.
+// An adapter whose tiles lie in one block goes straight to memory.  A block
+// shares at most its first and its last adapter with its neighbours: those
+// partial sums meet in distributed shared memory, added in block order.
 struct OuterSide {
-  const float *scale;  // nullptr: 1
+  const uint16_t *src;  // as the side's map
+  int64_t ld;
+  const float *scale;   // nullptr: 1
   void *out;
   int32_t C;
-  int32_t transposed;  // out [R][C] instead of [C][R]
+  int32_t transposed;   // out [R][C] instead of [C][R]
 };
 struct OuterArgs {
   OuterSide side[2];
   int32_t slabs0;  // slabs of side 0
   const int32_t *plan;
-  int64_t M, max_tiles;
+  int64_t M;
   int32_t R, L;
   int *status;
 };
 struct OuterMaps {
-  CUtensorMap src[2], rows[2], v[2];
+  CUtensorMap src[2], v[2];
 };
 
-constexpr int kOuterThreads = 128;
+constexpr int kOuterThreads = 192;  // producer, MMA issuer, four storing warps
 constexpr int kOuterSlab = 128;
 constexpr int kOuterRows = 64;  // a stage
 
@@ -716,51 +805,72 @@ struct OuterSmem {
   static constexpr int kV = TERMS * kOuterRows * RT * 2;
   static constexpr int kStage = kSrc + kV;
   static constexpr int kStages = 4 * kStage <= 104 * 1024 ? 4 : 3;
-  static constexpr int kBars = kStages * kStage;
-  static constexpr int kPartRow = RT + 1;  // floats
-  static constexpr int kBytes = kBars + (2 * kStages + 1) * 8 + 16 + 1024;
-  static_assert(kOuterSlab * kPartRow * 4 <= kBars, "partial sums reuse the stages");
+  static constexpr int kPartRow = RT + 4;  // floats
+  static constexpr int kPart = kOuterSlab * kPartRow * 4;
+  static constexpr int kData = kStages * kStage > 2 * kPart ? kStages * kStage : 2 * kPart;
+  static constexpr int kBars = (kData + 15) / 16 * 16;
+  static constexpr int kBytes = kBars + (2 * kStages + 5) * 8 + kStages * 4 + 16 + 1024;
   static_assert(kBytes <= 232448, "dynamic shared memory above the per-block limit");
+  // blocks that share an SM
+  static constexpr int kPerSm = 2 * (kBytes + 1024) <= 228 * 1024 ? 2 : 1;
+  static_assert(kPerSm * 2 * RT <= 512, "tensor memory of an SM");
 };
 
+enum { kStageFirst = 1, kStageLast = 2, kStageEnd = 4 };
+
+template <bool F32>
+__device__ __forceinline__ void store_grad(void *out, int64_t at, float v) {
+  if constexpr (F32)
+    static_cast<float *>(out)[at] = v;
+  else
+    static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v);
+}
+
 template <int RT, int TERMS>
-__global__ void __launch_bounds__(kOuterThreads)
+__global__ void __launch_bounds__(kOuterThreads, OuterSmem<RT, TERMS>::kPerSm)
     lora_outer_kernel(const __grid_constant__ OuterMaps maps, const OuterArgs p) {
   using S = OuterSmem<RT, TERMS>;
   constexpr int STAGES = S::kStages;
+  constexpr bool F32 = TERMS > 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kBars);
   uint64_t *empty = full + STAGES;
-  uint64_t *done = empty + STAGES;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  uint64_t *acc_full = empty + STAGES;
+  uint64_t *acc_empty = acc_full + 2;
+  uint64_t *done = acc_empty + 2;
+  volatile int *meta = reinterpret_cast<volatile int *>(done + 1);  // [STAGES]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1) + STAGES;
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   cg::cluster_group cluster = cg::this_cluster();
   const int shares = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool second = static_cast<int>(blockIdx.x) >= p.slabs0;
+  const int slab = static_cast<int>(blockIdx.x) / shares;
+  const bool second = slab >= p.slabs0;
   const OuterSide sd = second ? p.side[1] : p.side[0];
   const CUtensorMap *tm_src = second ? &maps.src[1] : &maps.src[0];
-  const CUtensorMap *tm_rows = second ? &maps.rows[1] : &maps.rows[0];
   const CUtensorMap *tm_v = second ? &maps.v[1] : &maps.v[0];
-  const int c0 = (static_cast<int>(blockIdx.x) - (second ? p.slabs0 : 0)) * kOuterSlab;
+  const int c0 = (slab - (second ? p.slabs0 : 0)) * kOuterSlab;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);
       mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 4);
     }
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(tm_src);
-    prefetch_tmap(tm_rows);
     prefetch_tmap(tm_v);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, RT);
+    tmem_alloc(tmem_slot, 2 * RT);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -768,150 +878,332 @@ __global__ void __launch_bounds__(kOuterThreads)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int bin = blockIdx.y;
   const bool fits = plan_fits(p.plan, p.M, p.L, p.status);
-  int tile0 = 0, steps = 0, all = 0;
+  const int32_t *tile_at = p.plan + 4;
   const int32_t *recs = p.plan + plan_recs_at(p.L);
-  if (fits) {
-    tile0 = p.plan[4 + bin];
-    const int tiles = p.plan[4 + bin + 1] - tile0;
-    // stages of 64 rows: two per full tile, one or two in the last
-    if (tiles > 0)
-      all = 2 * (tiles - 1) +
-            (recs[static_cast<int64_t>(tile0 + tiles - 1) * kRecWords + 1] + kOuterRows - 1) /
-                kOuterRows;
-    steps = all > rank ? (all - rank + shares - 1) / shares : 0;
-  }
+  const int tiles = fits ? tile_at[p.L] : 0;  // of rows with an adapter
+  const int holders = tiles < shares ? tiles : shares;  // blocks with any tile
+  auto first_tile = [&](int r) {  // of block r of the cluster
+    return r < holders ? static_cast<int>(static_cast<int64_t>(tiles) * r / holders) : tiles;
+  };
+  const int t_lo = first_tile(rank), t_hi = first_tile(rank + 1);
+  auto bin_of = [&](int tile) { return recs[static_cast<int64_t>(tile) * kRecWords]; };
   grid_dependency_wait();
 
-  if (fits) {
-    if (warp == 0) {
-      // ---------------------------------------------------------- producer
-      // lane l: rows 4 (l % 16) .. + 3 of column box l / 16
-      const bool brings = c0 + (lane >> 4) * 64 < sd.C;  // no box past the last column
-      const uint32_t bytes = S::kV + (c0 + 64 < sd.C ? 2 : 1) * 8192;
-      uint32_t armed = 0, armed_parity = 0;
-      int4 rows = make_int4(0, 0, 0, 0);
-      bool run = false;
-      auto fetch = [&](int step) {
-        const int s64 = all - 1 - (rank + step * shares);
-        const int32_t *rec = recs + static_cast<int64_t>(tile0 + s64 / 2) * kRecWords;
-        rows = *reinterpret_cast<const int4 *>(rec + 4 + (s64 & 1) * 64 + (lane & 15) * 4);
-        run = rec[3] != 0 && (s64 & 1) * 64 + kOuterRows <= rec[1];
-      };
-      if (steps > 0) fetch(0);
-      for (int step = 0; step < steps; ++step) {
-        const int st = step % STAGES;
-        const uint32_t phase = (step / STAGES) & 1;
-        const int s64 = all - 1 - (rank + step * shares);
-        uint8_t *src = smem + st * S::kStage;
-        bool ok = true;
-        if (lane == 0) {
-          ok = bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
-          if (ok) {
-            mbar_arrive_expect_tx(&full[st], bytes);
-            if (run) {
-              tma_load_2d(src, tm_src, &full[st], c0, rows.x);
-              if (c0 + 64 < sd.C) tma_load_2d(src + 8192, tm_src, &full[st], c0 + 64, rows.x);
-            }
-            const int vrow = tile0 * kTileRows + s64 * kOuterRows;
-#pragma unroll
-            for (int q = 0; q < TERMS; ++q)
-#pragma unroll
-              for (int h = 0; h < RT / 64; ++h)
-                tma_load_3d(src + S::kSrc + (q * (RT / 64) + h) * 8192, tm_v, &full[st], h * 64,
-                            vrow, q);
-            armed |= 1u << st;
-            armed_parity = (armed_parity & ~(1u << st)) | (phase << st);
-          }
-        }
-        if (!__shfl_sync(~0u, ok, 0)) break;
-        if (brings && !run)
-          tma_gather4(src + (lane >> 4) * 8192 + (lane & 15) * 512, tm_rows, &full[st],
-                      c0 + (lane >> 4) * 64, rows);
-        if (step + 1 < steps) fetch(step + 1);
-        __syncwarp();
-      }
-      if (lane == 0)
-        for (int s = 0; s < STAGES; ++s)
-          if (armed & (1u << s)) mbar_wait(&full[s], (armed_parity >> s) & 1u, kBoundedWaitNs);
-      __syncwarp();
-    } else if (warp == 1) {
-      // -------------------------------------------------------- MMA issuer
+  const int cols = sd.C - c0 < kOuterSlab ? sd.C - c0 : kOuterSlab;
+  float keep[RT];  // storing warps: the sums of a first adapter that is shared
+  bool kept = false, last_shared = false, ok_all = true;
+  uint32_t last_buf = 0;
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    uint32_t armed = 0, armed_parity = 0;
+    LateArrival late;
+    int step = 0;
+    bool ok = true;
+    // takes the next stage; lane 0 then announces `bytes` of TMA to come
+    auto take = [&](int flags, uint32_t bytes) -> int {
+      const int st = step % STAGES;
+      const uint32_t phase = (step / STAGES) & 1;
+      ++step;
       if (lane == 0) {
-        constexpr uint32_t idesc = idesc_bf16(kOuterSlab, RT) | kIdescTransA | kIdescTransB;
-        for (int step = 0; step < steps; ++step) {
-          const int st = step % STAGES;
-          if (!bounded_wait(&full[st], (step / STAGES) & 1, abort_flag, p.status,
+        ok = bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
+        if (ok) {
+          meta[st] = flags;
+          mbar_arrive_expect_tx(&full[st], bytes);
+          armed |= 1u << st;
+          armed_parity = (armed_parity & ~(1u << st)) | (phase << st);
+        }
+      }
+      ok = __shfl_sync(~0u, ok, 0);
+      return st;
+    };
+    const bool wide = c0 + 64 < sd.C;  // no box past the last column
+    // records are read two tiles ahead: {bin, rows, -, neighbours} and the row
+    // numbers, 32 k + l in lane l
+    struct Record {
+      int4 h;
+      int32_t rows[4];
+    };
+    auto read = [&](int tile, Record &r) {
+      if (tile >= t_hi) return;
+      const int32_t *rec = recs + static_cast<int64_t>(tile) * kRecWords;
+      r.h = *reinterpret_cast<const int4 *>(rec);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r.rows[k] = rec[4 + 32 * k + lane];
+    };
+    Record now = {make_int4(-1, 0, 0, 0), {0, 0, 0, 0}}, next = now, after = now;
+    int bin_before = -1;
+    read(t_lo, now);
+    read(t_lo + 1, next);
+    for (int tile = t_lo; tile < t_hi && ok; ++tile) {
+      read(tile + 2, after);
+      const int4 h = now.h;
+      const int first_row = __shfl_sync(~0u, now.rows[0], 0);
+      const int halves = (h.y + kOuterRows - 1) / kOuterRows;
+      const bool head = h.x != bin_before;
+      const bool tail = tile + 1 == t_hi || next.h.x != h.x;
+      for (int q = 0; q < halves && ok; ++q) {
+        const bool box = h.w != 0 && (q + 1) * kOuterRows <= h.y;
+        const int st = take((head && q == 0 ? kStageFirst : 0) |
+                                (tail && q == halves - 1 ? kStageLast : 0),
+                            S::kV + (box ? (wide ? 2 : 1) * 8192 : 0));
+        if (!ok) break;
+        uint8_t *src = smem + st * S::kStage;
+        if (lane == 0) {
+          if (box) {
+            const int row = first_row + q * kOuterRows;
+            tma_load_2d(src, tm_src, &full[st], c0, row);
+            if (wide) tma_load_2d(src + 8192, tm_src, &full[st], c0 + 64, row);
+          }
+#pragma unroll
+          for (int s = 0; s < TERMS; ++s)
+#pragma unroll
+            for (int b = 0; b < RT / 64; ++b)
+              tma_load_3d(src + S::kSrc + (s * (RT / 64) + b) * 8192, tm_v, &full[st], b * 64,
+                          tile * kTileRows + q * kOuterRows, s);
+        }
+        if (box) {
+          late.catch_up(lane);
+          if (lane == 0) mbar_arrive(&full[st]);
+        } else {
+          const int c = lane & 15, col = c0 + c * 8;
+          const uint32_t to = smem_u32(src) + (c >> 3) * 8192;
+          const bool in_cols = col < sd.C;
+          int32_t rows[kOuterRows / 2];  // all exchanged before the first copy
+#pragma unroll
+          for (int i = 0; i < kOuterRows / 2; ++i)
+            rows[i] = __shfl_sync(~0u, q == 0 ? now.rows[i / 16] : now.rows[2 + i / 16],
+                                  (i * 2 + (lane >> 4)) & 31);
+          if (c < 8 || wide) {
+#pragma unroll
+            for (int i = 0; i < kOuterRows / 2; ++i)
+              cp_async16(to + swz128(i * 2 + (lane >> 4), c & 7),
+                         sd.src + rows[i] * sd.ld + (in_cols ? col : 0), in_cols);
+          }
+          cp_async_commit();
+          late.push(lane, &full[st]);
+        }
+      }
+      bin_before = h.x;
+      now = next;
+      next = after;
+    }
+    late.catch_up(lane);
+    if (ok) {
+      const int st = take(kStageEnd, 0);
+      if (ok && lane == 0) mbar_arrive(&full[st]);
+    }
+    // never leave with a copy in flight into this block's shared memory
+    cp_async_wait<0>();
+    if (lane == 0)
+      for (int s = 0; s < STAGES; ++s)
+        if (armed & (1u << s)) mbar_wait(&full[s], (armed_parity >> s) & 1u, kBoundedWaitNs);
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16(kOuterSlab, RT) | kIdescTransA | kIdescTransB;
+      uint32_t seg = 0;
+      for (int step = 0;; ++step) {
+        const int st = step % STAGES;
+        if (!bounded_wait(&full[st], (step / STAGES) & 1, abort_flag, p.status,
+                          SQ_ERR_DEVICE_TIMEOUT))
+          break;
+        const int flags = meta[st];
+        if (flags & kStageEnd) break;
+        const uint32_t acc = tmem + (seg & 1) * RT;
+        if (flags & kStageFirst)
+          if (!bounded_wait(&acc_empty[seg & 1], ((seg >> 1) & 1) ^ 1, abort_flag, p.status,
                             SQ_ERR_DEVICE_TIMEOUT))
             break;
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + st * S::kStage), sb = sa + S::kSrc;
+        tc_fence_after();
+        const uint32_t sa = smem_u32(smem + st * S::kStage), sb = sa + S::kSrc;
 #pragma unroll
-          for (int q = TERMS - 1; q >= 0; --q)
+        for (int q = TERMS - 1; q >= 0; --q)
 #pragma unroll
-            for (int kk = 0; kk < kOuterRows / 16; ++kk)
-              mma_bf16_tc(tmem, sdesc_mnmajor_sw128(sa + kk * 2048, 8192),
-                          sdesc_mnmajor_sw128(sb + q * (RT / 64) * 8192 + kk * 2048, 8192), idesc,
-                          step > 0 || kk > 0 || q < TERMS - 1);
-          mma_commit(&empty[st]);
+          for (int kk = 0; kk < kOuterRows / 16; ++kk)
+            mma_bf16_tc(acc, sdesc_mnmajor_sw128(sa + kk * 2048, 8192),
+                        sdesc_mnmajor_sw128(sb + q * (RT / 64) * 8192 + kk * 2048, 8192), idesc,
+                        !(flags & kStageFirst) || kk > 0 || q < TERMS - 1);
+        mma_commit(&empty[st]);
+        if (flags & kStageLast) {
+          mma_commit(&acc_full[seg & 1]);
+          ++seg;
         }
-        mma_commit(done);
       }
-      __syncwarp();
+      mma_commit(done);
     }
-    const bool ok = bounded_wait(done, 0, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
-    tc_fence_after();
-    __syncthreads();  // nothing reads or fills the stages any more
-
-    float *part = reinterpret_cast<float *>(smem);
-    constexpr int PS = S::kPartRow;
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------ storing warps
+    // thread: column c of the slab, sums over all j
+    const int c = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint32_t seg = 0;
+    for (int tile = t_lo; tile < t_hi; ++seg) {
+      const int bin = bin_of(tile);
+      const int lo = tile_at[bin], hi = tile_at[bin + 1];
+      const bool whole = lo >= t_lo && hi <= t_hi;
+      const bool first = tile == t_lo;
+      tile = hi < t_hi ? hi : t_hi;
+      ok_all = bounded_wait(&acc_full[seg & 1], (seg >> 1) & 1, abort_flag, p.status,
+                            SQ_ERR_DEVICE_TIMEOUT);
+      if (!ok_all) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + (seg & 1) * RT + lanes;
+      if (!whole && !first) {  // the last one, shared: stays where it is
+        last_shared = true;
+        last_buf = seg & 1;
+        break;
+      }
+      if (whole) {
+        const float f = sd.scale ? sd.scale[bin] : 1.0f;
+        const int64_t obase = static_cast<int64_t>(bin) * p.R * sd.C;
 #pragma unroll
-    for (int c = 0; c < RT; c += 32) {
-      uint32_t r[32];
-      __syncwarp();
-      tmem_ld_32x32b_x32(tmem + c + (static_cast<uint32_t>(warp * 32) << 16), r);
-      tmem_ld_wait();
+        for (int j0 = 0; j0 < RT; j0 += 32) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld_32x32b_x32(acc + j0, r);
+          tmem_ld_wait();
+          if (c < cols && store_ok(p.status, c0 + c < sd.C)) {
+            if (sd.transposed) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        part[threadIdx.x * PS + c + j] = steps > 0 ? __uint_as_float(r[j]) : 0.0f;
-    }
-    if (shares > 1) cluster.sync(); else __syncthreads();
-    const float f = sd.scale ? sd.scale[bin] : 1.0f;
-    const int cols = sd.C - c0 < kOuterSlab ? sd.C - c0 : kOuterSlab;
-    const int n_out = ok ? cols * p.R : 0;
-    const int64_t obase = static_cast<int64_t>(bin) * p.R * sd.C;
-    for (int e = rank * kOuterThreads + threadIdx.x; e < n_out; e += shares * kOuterThreads) {
-      int c, j;
-      if (sd.transposed) {
-        j = e / cols;
-        c = e - j * cols;
+              for (int j = 0; j < 32; ++j)
+                if (j0 + j < p.R)
+                  store_grad<F32>(sd.out, obase + static_cast<int64_t>(j0 + j) * sd.C + c0 + c,
+                                  f * __uint_as_float(r[j]));
+            } else {
+              const int64_t at = obase + static_cast<int64_t>(c0 + c) * p.R + j0;
+#pragma unroll
+              for (int j = 0; j < 32; j += 8)
+                if (j0 + j < p.R) {  // R % 8 == 0
+                  float v[8];
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) v[e] = f * __uint_as_float(r[j + e]);
+                  if constexpr (F32) {
+                    float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(sd.out) + at + j);
+                    to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    to[1] = make_float4(v[4], v[5], v[6], v[7]);
+                  } else {
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(sd.out) + at + j) =
+                        make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                                   bf16x2(v[6], v[7]));
+                  }
+                }
+            }
+          }
+        }
       } else {
-        c = e / p.R;
-        j = e - c * p.R;
+#pragma unroll
+        for (int j0 = 0; j0 < RT; j0 += 32) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld_32x32b_x32(acc + j0, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) keep[j0 + j] = __uint_as_float(r[j]);
+        }
+        kept = true;
       }
-      float s = 0.0f;
-      for (int q = 0; q < shares; ++q) {
-        const float *src = shares > 1 ? cluster.map_shared_rank(part, q) : part;
-        s += src[c * PS + j];
-      }
-      const int64_t at = obase + (sd.transposed ? static_cast<int64_t>(j) * sd.C + c0 + c
-                                                : static_cast<int64_t>(c0 + c) * p.R + j);
-      if (!store_ok(p.status, j < p.R && c0 + c < sd.C)) continue;
-      if constexpr (TERMS > 1)
-        static_cast<float *>(sd.out)[at] = f * s;
-      else
-        static_cast<__nv_bfloat16 *>(sd.out)[at] = __float2bfloat16_rn(f * s);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[seg & 1]);
     }
-    if (shares > 1) cluster.sync();
   }
+  const bool ok = bounded_wait(done, 0, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT) && ok_all;
+  tc_fence_after();
+  __syncthreads();  // nothing reads or fills the stages any more
+
+  // partial sums of the first (0) and the last (1) adapter, [128][RT + 4]
+  constexpr int PS = S::kPartRow;
+  float *part = reinterpret_cast<float *>(smem);
+  if (warp >= 2) {
+    const int c = (warp & 3) * 32 + lane;
+    if (kept) {
+#pragma unroll
+      for (int j = 0; j < RT; j += 4)
+        *reinterpret_cast<float4 *>(part + c * PS + j) =
+            make_float4(keep[j], keep[j + 1], keep[j + 2], keep[j + 3]);
+    }
+    if (last_shared) {
+      float *to = part + kOuterSlab * PS + c * PS;
+#pragma unroll
+      for (int j0 = 0; j0 < RT; j0 += 32) {
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(tmem + last_buf * RT + (static_cast<uint32_t>((warp & 3) * 32) << 16) + j0,
+                           r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+          *reinterpret_cast<uint4 *>(to + j0 + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+      }
+    }
+  }
+  if (shares > 1) {
+    cluster.sync();
+    if (t_lo < t_hi && ok) {
+      const int b_first = bin_of(t_lo), b_last = bin_of(t_hi - 1);
+      for (int k = 0; k < 2; ++k) {
+        const int bin = k == 0 ? b_first : b_last;
+        if (k == 1 && b_last == b_first) break;
+        const int lo = tile_at[bin], hi = tile_at[bin + 1];
+        if (lo >= t_lo && hi <= t_hi) continue;  // all here: stored
+        // the blocks that hold tiles of this adapter
+        int r_lo = rank, r_hi = rank;
+        while (r_lo > 0 && first_tile(r_lo) > lo) --r_lo;
+        while (r_hi + 1 < holders && first_tile(r_hi + 1) < hi) ++r_hi;
+        const float f = sd.scale ? sd.scale[bin] : 1.0f;
+        const int64_t obase = static_cast<int64_t>(bin) * p.R * sd.C;
+        const int quads = p.R / 4, n_out = cols * quads, n_blocks = r_hi - r_lo + 1;
+        for (int e = (rank - r_lo) * kOuterThreads + threadIdx.x; e < n_out;
+             e += n_blocks * kOuterThreads) {
+          const int c = sd.transposed ? e % cols : e / quads;
+          const int j = (sd.transposed ? e / cols : e % quads) * 4;
+          // the adapter is a block's first unless the block begins before it
+          const float4 s = cluster_sum(cluster, part, r_lo, r_hi, [&](int r) {
+            return (first_tile(r) < lo ? kOuterSlab * PS : 0) + c * PS + j;
+          });
+          if (!store_ok(p.status, j + 4 <= p.R && c0 + c < sd.C)) continue;
+          const float v[4] = {f * s.x, f * s.y, f * s.z, f * s.w};
+          if (sd.transposed) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              store_grad<F32>(sd.out, obase + static_cast<int64_t>(j + q) * sd.C + c0 + c, v[q]);
+          } else {
+            const int64_t at = obase + static_cast<int64_t>(c0 + c) * p.R + j;
+            if constexpr (F32)
+              *reinterpret_cast<float4 *>(static_cast<float *>(sd.out) + at) =
+                  make_float4(v[0], v[1], v[2], v[3]);
+            else
+              *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(sd.out) + at) =
+                  make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+          }
+        }
+      }
+    }
+  }
+  // adapters without rows: zeros
+  if (fits)
+    for (int bin = rank; bin < p.L; bin += shares) {
+      if (tile_at[bin] != tile_at[bin + 1]) continue;
+      const int64_t obase = static_cast<int64_t>(bin) * p.R * sd.C;
+      for (int e = threadIdx.x; e < cols * p.R; e += kOuterThreads) {
+        const int64_t at = sd.transposed
+                               ? obase + static_cast<int64_t>(e / cols) * sd.C + c0 + e % cols
+                               : obase + static_cast<int64_t>(c0) * p.R + e;
+        if (store_ok(p.status, at < (static_cast<int64_t>(bin) + 1) * p.R * sd.C))
+          store_grad<F32>(sd.out, at, 0.0f);
+      }
+    }
+  if (shares > 1) cluster.sync();  // no block leaves while its sums are read
 
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, RT);
+    tmem_dealloc(tmem, 2 * RT);
   }
 }
 
@@ -920,18 +1212,30 @@ __global__ void __launch_bounds__(kOuterThreads)
 // grid's dimension `dim` (0 x, 1 y, 2 z).  Every kernel here waits for the one
 // ahead of it in the stream (programmatic dependent launch) before it reads
 // what that one may have written.
-template <auto Kernel, typename... Args>
-cudaError_t launch(dim3 grid, int threads, int smem, int cluster, int dim, cudaStream_t stream,
-                   const Args &...args) {
-  static bool attr_set[64] = {};  // per kernel and device
+//
+// By default the driver gives an SM as much shared memory as one block of the
+// kernel needs, not as much as would hold two or three: asking for all of it
+// doubles (triples) the blocks that run at once.
+template <auto Kernel>
+cudaError_t allow_smem(int smem) {
+  static bool set[64] = {};  // per kernel and device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    attr_set[dev] = true;
-  }
+  if (set[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess) set[dev] = true;
+  return e;
+}
+
+template <auto Kernel, typename... Args>
+cudaError_t launch(dim3 grid, int threads, int smem, int cluster, int dim, cudaStream_t stream,
+                   const Args &...args) {
+  cudaError_t e = allow_smem<Kernel>(smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -971,23 +1275,21 @@ cudaError_t bf16_map(CUtensorMap *map, const void *ptr, int64_t d0, int64_t d1, 
 }
 
 template <int RT, bool TRANS, int TERMS>
-cudaError_t run_contract(const uint16_t *in, int64_t ld, const uint16_t *w, const ContractArgs &a,
-                         cudaStream_t stream) {
-  CUtensorMap tm_in, tm_rows, tm_w;
-  cudaError_t e = bf16_map(&tm_in, in, a.C, a.M, 0, ld, kTileRows);
-  if (e == cudaSuccess) e = bf16_map(&tm_rows, in, a.C, a.M, 0, ld, 1);
+cudaError_t run_contract(const uint16_t *w, const ContractArgs &a, cudaStream_t stream) {
+  CUtensorMap tm_in, tm_w;
+  cudaError_t e = bf16_map(&tm_in, a.in, a.C, a.M, 0, a.ld, kTileRows);
   if (e == cudaSuccess)
     e = TRANS ? bf16_map(&tm_w, w, a.R, a.C, a.L, a.R, 64)
               : bf16_map(&tm_w, w, a.C, a.R, a.L, a.C, RT);
   if (e != cudaSuccess) return e;
-  // Slices of the contracted dimension: as many blocks as run at once (two per
-  // SM), none shorter than 256 columns.
+  // Slices of the contracted dimension: as many as let all tiles run at once
+  // (two blocks per SM), none shorter than 256 columns.
   int slices = 1;
-  while (slices < 8 && a.max_tiles * slices * 2 <= 2 * sm_count() && a.C >= 256 * slices * 2)
+  while (slices < 8 && a.C >= 256 * slices * 2 && a.max_tiles * slices * 2 <= 2 * sm_count())
     slices *= 2;
   return launch<lora_contract_kernel<RT, TRANS, TERMS>>(
       dim3(static_cast<unsigned>(a.max_tiles), slices), kContractThreads,
-      ContractSmem<RT>::kBytes, slices, 1, stream, tm_in, tm_rows, tm_w, a);
+      ContractSmem<RT>::kBytes, slices, 1, stream, tm_in, tm_w, a);
 }
 
 template <int RT, bool TRANS, bool F32>
@@ -1002,16 +1304,18 @@ cudaError_t run_expand(const ExpandArgs &a, cudaStream_t stream) {
 
 template <int RT, int TERMS>
 cudaError_t run_outer(const OuterMaps &maps, const OuterArgs &a, cudaStream_t stream) {
+  using S = OuterSmem<RT, TERMS>;
   const int slabs = a.slabs0 + (a.side[1].C + kOuterSlab - 1) / kOuterSlab;
-  // Shares of an adapter's rows: as many blocks as run at once (two per SM),
-  // none with fewer than two stages on average.
+  // Blocks of a slab: as many (up to the portable cluster size, and one for each
+  // two full row tiles) as let all slabs run at once.  A cluster lies within one
+  // of the GPU's partitions, which leaves some places empty: 60 slabs by 4 take
+  // 58 us, by 7 (three blocks per SM) two rounds and 80 us.
   int shares = 1;
-  while (shares < 8 && static_cast<int64_t>(slabs) * a.L * shares * 2 <= 2 * sm_count() &&
-         a.M / a.L >= 2 * kOuterRows * shares * 2)
-    shares *= 2;
-  return launch<lora_outer_kernel<RT, TERMS>>(dim3(slabs, a.L, shares), kOuterThreads,
-                                              OuterSmem<RT, TERMS>::kBytes, shares, 2, stream,
-                                              maps, a);
+  for (int n = 2; n <= 8 && a.M >= 2 * kTileRows * n; ++n)
+    if (static_cast<int64_t>(slabs) * n * 16 <= static_cast<int64_t>(S::kPerSm) * sm_count() * 15)
+      shares = n;
+  return launch<lora_outer_kernel<RT, TERMS>>(dim3(slabs * shares), kOuterThreads, S::kBytes,
+                                              shares, 0, stream, maps, a);
 }
 
 // Ranks are padded to 64 (128) columns: the boxes' columns past R read as zero.
@@ -1039,27 +1343,24 @@ cudaError_t run_backward(const LoraRequest &q, cudaStream_t stream) {
   const int64_t max_tiles = plan_max_tiles(q.M, q.L), rows = max_tiles * kTileRows;
   uint16_t *vdt = static_cast<uint16_t *>(q.workspace);
   uint16_t *vt = vdt + TERMS * rows * q.R;
-  const ContractArgs c = {q.scale, q.plan, nullptr, q.t, vt,  vdt,
-                          q.M,     max_tiles, N,    q.R, q.L, q.status};
+  const ContractArgs c = {q.dy, q.lddy, q.scale, q.plan, nullptr, q.t, vt, vdt,
+                          q.M, max_tiles, N, q.R, q.L, q.status};
   cudaError_t e = by_rank(q.R, [&](auto rt) {
-    return run_contract<decltype(rt)::value, true, TERMS>(q.dy, q.lddy, q.B, c, stream);
+    return run_contract<decltype(rt)::value, true, TERMS>(q.B, c, stream);
   });
   if (e == cudaSuccess && q.dA != nullptr) {
     OuterMaps maps;
     OuterArgs o = {};
-    o.side[0] = {q.scale, q.dB, N, 0};
-    o.side[1] = {nullptr, q.dA, K, 1};
+    o.side[0] = {q.dy, q.lddy, q.scale, q.dB, N, 0};
+    o.side[1] = {q.x, q.ldx, nullptr, q.dA, K, 1};
     o.slabs0 = (N + kOuterSlab - 1) / kOuterSlab;
     o.plan = q.plan;
     o.M = q.M;
-    o.max_tiles = max_tiles;
     o.R = q.R;
     o.L = q.L;
     o.status = q.status;
     e = bf16_map(&maps.src[0], q.dy, N, q.M, 0, q.lddy, kOuterRows);
     if (e == cudaSuccess) e = bf16_map(&maps.src[1], q.x, K, q.M, 0, q.ldx, kOuterRows);
-    if (e == cudaSuccess) e = bf16_map(&maps.rows[0], q.dy, N, q.M, 0, q.lddy, 1);
-    if (e == cudaSuccess) e = bf16_map(&maps.rows[1], q.x, K, q.M, 0, q.ldx, 1);
     if (e == cudaSuccess) e = bf16_map(&maps.v[0], vt, q.R, rows, TERMS, q.R, kOuterRows);
     if (e == cudaSuccess) e = bf16_map(&maps.v[1], vdt, q.R, rows, TERMS, q.R, kOuterRows);
     if (e == cudaSuccess)
@@ -1099,13 +1400,13 @@ cudaError_t launch_lora_plan(const int32_t *adapter, int64_t M, int32_t L, int32
 }
 
 cudaError_t launch_lora_forward(const LoraRequest &q, cudaStream_t stream) {
-  const ContractArgs c = {nullptr, q.plan, q.t, nullptr, nullptr, nullptr,
+  const ContractArgs c = {q.x, q.ldx, nullptr, q.plan, q.t, nullptr, nullptr, nullptr,
                           q.M, plan_max_tiles(q.M, q.L), static_cast<int32_t>(q.K), q.R, q.L,
                           q.status};
   const ExpandArgs e = {q.t, nullptr, q.B, q.scale, q.plan, q.base, q.ld_base, q.y, q.ldy, q.M,
                         static_cast<int32_t>(q.N), q.R, q.L, q.status};
   const cudaError_t err = by_rank(q.R, [&](auto rt) {
-    return run_contract<decltype(rt)::value, false, 0>(q.x, q.ldx, q.A, c, stream);
+    return run_contract<decltype(rt)::value, false, 0>(q.A, c, stream);
   });
   if (err != cudaSuccess) return err;
   return by_rank_fine(q.R, [&](auto rt) {

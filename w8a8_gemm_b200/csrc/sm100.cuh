@@ -121,17 +121,6 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
       : "memory");
 }
 
-// Four rows of a 2D tensor (its map's box is one row high), given by number,
-// into four neighbouring rows of the tile; columns from c0.
-__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, uint64_t *bar,
-                                            int32_t c0, const int4 &rows) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w)
-      : "memory");
-}
-
 // Tensor store from shared memory (a tile of the output).  Elements of the box
 // that fall outside the tensor are not written.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int32_t c0,
