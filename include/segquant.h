@@ -550,16 +550,25 @@ SQ_API sq_status sq_lora_plan(const int32_t *adapter, int64_t M, int32_t n_adapt
  *          may be y (with ldbase == ldy: in place); otherwise the buffers must
  *          not overlap.  y must not overlap x.
  *   t      fp32 [M][R] output (the backward pass reads it)
+ *   workspace  device memory of sq_lora_workspace_bytes(M, R, L, out_dtype)
+ *          bytes, 16-byte aligned; needs no initial value (NULL when M == 0).
+ *          One workspace may serve the forward and backward calls of all layers
+ *          that run on one stream.
  *   R 8..128, K and N >= 8, all multiples of 8; K, N <= 2^20; leading dimensions
  *   at least the row's length and multiples of 8; x, A, B, base, y, t, plan
  *   16-byte aligned, scale 4-byte; M <= 2^24, M * ld <= 2^44.
  * M == 0 is a valid no-op.  Two kernels.
+ * sq_lora_workspace_bytes: for the forward and for the backward call (there with
+ * grad_dtype); 0 for sizes out of range.
  */
+SQ_API size_t sq_lora_workspace_bytes(int64_t M, int32_t R, int32_t n_adapters,
+                                      sq_out_dtype dtype);
 SQ_API sq_status sq_lora_forward(const void *x, int64_t ldx, const void *A, const void *B,
                                  const float *scale, const int32_t *plan, const void *base,
                                  int64_t ldbase, void *y, int64_t ldy, sq_out_dtype out_dtype,
-                                 float *t, int64_t M, int64_t N, int64_t K, int32_t R,
-                                 int32_t n_adapters, sq_stream_t stream);
+                                 float *t, void *workspace, size_t workspace_bytes, int64_t M,
+                                 int64_t N, int64_t K, int32_t R, int32_t n_adapters,
+                                 sq_stream_t stream);
 
 /*
  * sq_lora_backward -- the gradients of sq_lora_forward from dy = dL/dy:
@@ -580,10 +589,7 @@ SQ_API sq_status sq_lora_forward(const void *x, int64_t ldx, const void *A, cons
  *            bytes, 16-byte aligned; needs no initial value (NULL when M == 0)
  * Alignment and limits as in the forward call; dA and dB 16-byte aligned.
  * M == 0 writes zeros to dA and dB.  Up to three kernels.
- * sq_lora_workspace_bytes: 0 for sizes out of range.
  */
-SQ_API size_t sq_lora_workspace_bytes(int64_t M, int32_t R, int32_t n_adapters,
-                                      sq_out_dtype grad_dtype);
 SQ_API sq_status sq_lora_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
                                   const float *t, const void *A, const void *B,
                                   const float *scale, const int32_t *plan, const void *dx_base,

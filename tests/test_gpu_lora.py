@@ -34,6 +34,11 @@ def _problem(M, K, N, R, L, seed, spread="runs", out=BF):
         ids = torch.randint(-1, L, (len(cuts) + 1,), generator=g, device="cuda")[req]
     elif spread == "scattered":  # any row any adapter
         ids = torch.randint(-1, L, (M,), generator=g, device="cuda")
+    elif spread == "mixed":    # long runs, and between them rows of any adapter
+        ids = (torch.arange(M, device="cuda") // 700) % (L + 1) - 1
+        loose = torch.rand(M, generator=g, device="cuda") < 0.3
+        ids = torch.where(loose & (torch.arange(M, device="cuda") % 1500 < 600),
+                          torch.randint(-1, L, (M,), generator=g, device="cuda"), ids)
     elif spread == "one":
         ids = torch.full((M,), L - 1, device="cuda")
     else:                      # no row has one; numbers out of range mean none, too
@@ -51,7 +56,7 @@ SIZES = [  # M, K, N, R, L, spread
     (63, 72, 200, 24, 3, "runs"), (64, 8, 8, 8, 2, "scattered"), (65, 128, 136, 32, 2, "one"),
     (333, 1000, 520, 48, 5, "runs"), (130, 2056, 264, 64, 3, "scattered"), (257, 512, 384, 128, 2, "runs"),
     (129, 200, 1160, 96, 7, "scattered"), (1500, 448, 640, 40, 3, "runs"), (77, 64, 128, 16, 40, "scattered"),
-    (100, 64, 72, 8, 3, "none"), (300, 96, 64, 16, 1024, "scattered"), (4100, 256, 256, 64, 1, "one"),
+    (3000, 320, 3080, 72, 2, "scattered"), (5000, 256, 2048, 64, 3, "mixed"), (100, 64, 72, 8, 3, "none"), (300, 96, 64, 16, 1024, "scattered"), (4100, 256, 256, 64, 1, "one"),
 ]
 
 
@@ -92,6 +97,7 @@ def test_backward(M, K, N, R, L, spread, grads):
         if not (p["ids"] == a).any():
             assert (dA[a] == 0).all() and (dB[a] == 0).all()
     assert torch.equal(dx[~has], p["dx_base"][~has])
+    assert B.sq_get_device_status() == B.SQ_OK
 
 
 def test_plan_orders_rows_by_adapter_and_keeps_their_order():
@@ -178,19 +184,25 @@ def test_no_rows():
     assert (dA == 0).all() and (dB == 0).all() and dx.shape == (0, 64)
 
 
-def test_same_bits_every_time_and_from_a_graph():
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("R,spread", [(32, "runs"), (64, "mixed"), (128, "mixed"), (8, "one")])
+def test_same_bits_every_time_and_from_a_graph(R, spread, out):
     """Fixed orders of all sums: repeated calls, another stream and a replayed
     graph give the same bits; new inputs in the captured buffers give theirs."""
-    M, K, N, R, L = 700, 640, 896, 32, 2
-    p = _problem(M, K, N, R, L, seed=21)
+    M, K, N, L = 2300, 640, 2296, 2
+    p = _problem(M, K, N, R, L, seed=21, spread=spread, out=out)
     plan = B.sq_lora_plan(p["ids"], L)
 
     def call():
         y, t = B.sq_lora_forward(p["x"], p["A"], p["B"], p["scale"], plan, p["base"])
         return (y, *B.sq_lora_backward(p["dy"], p["x"], t, p["A"], p["B"], p["scale"], plan,
-                                       p["dx_base"]))
+                                       p["dx_base"], grad_dtype=out))
 
     first = call()
+    for _ in range(20):         # back to back, one call's kernels behind the other's
+        again = call()
+    for u, v in zip(first, again):
+        assert torch.equal(u, v)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
@@ -209,6 +221,7 @@ def test_same_bits_every_time_and_from_a_graph():
     torch.cuda.synchronize()
     for u, w in zip(fresh, third):
         assert torch.equal(u, w)
+    assert B.sq_get_device_status() == B.SQ_OK
 
 
 def test_plan_of_another_batch_is_reported_and_nothing_written():

@@ -43,16 +43,16 @@ def test_lora_refusals(L):
     assert _call(L.sq_lora_plan, plan, plan=FAKE + 4) == ALIGNMENT
 
     fwd = dict(x=FAKE, ldx=64, A=FAKE, B=FAKE, scale=FAKE, plan=FAKE, base=FAKE, ldbase=72,
-               y=2 * FAKE, ldy=72, out=0, t=FAKE, M=4, N=72, K=64, R=8, L=2)
+               y=2 * FAKE, ldy=72, out=0, t=FAKE, workspace=FAKE, bytes=need, M=4, N=72, K=64, R=8, L=2)
     for bad in (dict(x=None), dict(A=None), dict(B=None), dict(scale=None), dict(plan=None),
-                dict(y=None), dict(t=None), dict(out=2), dict(ldx=56), dict(ldy=64),
+                dict(y=None), dict(t=None), dict(workspace=None), dict(bytes=need - 1), dict(out=2), dict(ldx=56), dict(ldy=64),
                 dict(ldbase=64), dict(M=-1), dict(N=0), dict(K=0), dict(R=0), dict(L=0),
                 dict(ldx=2 ** 43), dict(base=2 * FAKE, ldbase=80), dict(N=2 ** 20 + 8)):
         assert _call(L.sq_lora_forward, fwd, **bad) == INVALID, bad
     for bad in (dict(R=4), dict(R=136)):
         assert _call(L.sq_lora_forward, fwd, **bad) == UNSUPPORTED, bad
     for bad in (dict(R=12), dict(K=60), dict(N=68), dict(ldx=68), dict(x=FAKE + 2),
-                dict(A=FAKE + 8), dict(y=FAKE + 8), dict(t=FAKE + 8), dict(scale=FAKE + 2),
+                dict(A=FAKE + 8), dict(workspace=FAKE + 8), dict(y=FAKE + 8), dict(t=FAKE + 8), dict(scale=FAKE + 2),
                 dict(plan=FAKE + 4), dict(base=FAKE + 8)):
         assert _call(L.sq_lora_forward, fwd, **bad) == ALIGNMENT, bad
     assert _call(L.sq_lora_forward, fwd, M=0, x=None, y=None, base=None, t=None) == 0

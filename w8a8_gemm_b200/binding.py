@@ -155,8 +155,8 @@ def lib() -> ctypes.CDLL:
         L.sq_lora_plan_bytes.argtypes = [i64, i32]
         L.sq_lora_plan_bytes.restype = size
         L.sq_lora_plan.argtypes = [p, i64, i32, p, p]
-        L.sq_lora_forward.argtypes = [p, i64, p, p, p, p, p, i64, p, i64, c_int, p, i64, i64, i64,
-                                      i32, i32, p]
+        L.sq_lora_forward.argtypes = [p, i64, p, p, p, p, p, i64, p, i64, c_int, p, p, size, i64,
+                                      i64, i64, i32, i32, p]
         L.sq_lora_workspace_bytes.argtypes = [i64, i32, i32, c_int]
         L.sq_lora_workspace_bytes.restype = size
         L.sq_lora_backward.argtypes = [p, i64, p, i64, p, p, p, p, p, p, i64, p, i64, p, p, c_int,
@@ -606,7 +606,8 @@ def _lora_weights(A: torch.Tensor, Bm: torch.Tensor, scale: torch.Tensor, plan: 
 
 def sq_lora_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
                     plan: torch.Tensor, base: Optional[torch.Tensor],
-                    y: Optional[torch.Tensor] = None, t: Optional[torch.Tensor] = None):
+                    y: Optional[torch.Tensor] = None, t: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None):
     """y = base + scale[a] B[a] (A[a] x) per row with adapter a -> (y, t).  base
     bf16 or fp32 [M, N] (None: zeros, bf16 unless y says otherwise); y may be base
     (in place); t fp32 [M, R] is kept for the backward pass (rows without an
@@ -625,16 +626,22 @@ def sq_lora_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: to
     _shape(y, y.dtype, (M, N), "y", contiguous=False)
     _shape(base, y.dtype, (M, N), "base", contiguous=False)
     _shape(t, torch.float32, (M, R), "t")
-    _here(x.device, A=A, base=base, y=y, t=t)
+    if workspace is None:
+        workspace = torch.empty(sq_lora_workspace_bytes(M, R, L, y.dtype), dtype=torch.uint8,
+                                device=x.device)
+    _need(workspace, torch.uint8, "workspace")
+    _here(x.device, A=A, base=base, y=y, t=t, workspace=workspace)
     _check(lib().sq_lora_forward(_ptr(x), _ld(x), _ptr(A), _ptr(B), _ptr(scale), _ptr(plan),
                                  _ptr(base), 0 if base is None else _ld(base), _ptr(y), _ld(y),
-                                 out, _ptr(t), M, N, K, R, L, _stream()), "sq_lora_forward")
+                                 out, _ptr(t), _ptr(workspace), workspace.numel(), M, N, K, R, L,
+                                 _stream()), "sq_lora_forward")
     return y, t
 
 
-def sq_lora_workspace_bytes(M: int, R: int, n_adapters: int, grad_dtype=torch.bfloat16) -> int:
-    """Workspace bytes of sq_lora_backward (0: sizes out of range)."""
-    return lib().sq_lora_workspace_bytes(M, R, n_adapters, _out_dtype(grad_dtype, "grad_dtype"))
+def sq_lora_workspace_bytes(M: int, R: int, n_adapters: int, dtype=torch.bfloat16) -> int:
+    """Workspace bytes of sq_lora_forward (dtype of y) and sq_lora_backward (0:
+    sizes out of range)."""
+    return lib().sq_lora_workspace_bytes(M, R, n_adapters, _out_dtype(dtype, "dtype"))
 
 
 def sq_lora_backward(dy: torch.Tensor, x: torch.Tensor, t: torch.Tensor, A: torch.Tensor,

@@ -174,16 +174,19 @@ sq_status sq_lora_plan(const int32_t *adapter, int64_t M, int32_t n_adapters, in
 sq_status sq_lora_forward(const void *x, int64_t ldx, const void *A, const void *B,
                           const float *scale, const int32_t *plan, const void *base,
                           int64_t ldbase, void *y, int64_t ldy, sq_out_dtype out_dtype, float *t,
-                          int64_t M, int64_t N, int64_t K, int32_t R, int32_t n_adapters,
-                          sq_stream_t stream) {
+                          void *workspace, size_t workspace_bytes, int64_t M, int64_t N,
+                          int64_t K, int32_t R, int32_t n_adapters, sq_stream_t stream) {
   if (out_dtype != SQ_OUT_BF16 && out_dtype != SQ_OUT_F32) return SQ_ERR_INVALID_ARG;
   SQ_TRY(check_lora(M, N, K, R, n_adapters, A, B, scale, plan));
   SQ_TRY(check_rows(x, M, K, ldx));
   SQ_TRY(check_rows(y, M, N, ldy));
   if (base != nullptr) SQ_TRY(check_rows(base, M, N, ldbase));
   if (M == 0) return SQ_OK;
+  const bool f32 = out_dtype == SQ_OUT_F32;
   if (t == nullptr || (base == y && ldbase != ldy)) return SQ_ERR_INVALID_ARG;
-  if (!aligned(t, 16)) return SQ_ERR_ALIGNMENT;
+  if (workspace == nullptr || workspace_bytes < lora_workspace_bytes(M, R, n_adapters, f32))
+    return SQ_ERR_INVALID_ARG;
+  if (!aligned(t, 16) || !aligned(workspace, 16)) return SQ_ERR_ALIGNMENT;
   LoraRequest q = {};
   SQ_TRY(device_word(&q.status));
   q.x = static_cast<const uint16_t *>(x);
@@ -202,7 +205,8 @@ sq_status sq_lora_forward(const void *x, int64_t ldx, const void *A, const void 
   q.K = K;
   q.R = R;
   q.L = n_adapters;
-  q.f32 = out_dtype == SQ_OUT_F32;
+  q.workspace = workspace;
+  q.f32 = f32;
   return from_cuda(launch_lora_forward(q, cs(stream)));
 }
 

@@ -17,7 +17,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "mma.cuh"
+#include "bf16.cuh"
 #include "sq_internal.h"
 
 namespace sq {

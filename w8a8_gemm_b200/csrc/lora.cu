@@ -26,7 +26,7 @@
 
 #include <type_traits>
 
-#include "mma.cuh"
+#include "bf16.cuh"
 #include "sq_internal.h"
 
 namespace sq {
@@ -203,6 +203,14 @@ struct LateArrival {
     arrive<0>(lane, newer);
     older = newer = nullptr;
   }
+  // Before a wait for a free stage: whoever frees it may itself be waiting for
+  // a stage whose copies have landed without being announced, so nothing is
+  // held back unless the stage is free already.
+  __device__ __forceinline__ void before_wait(int lane, uint64_t *bar, uint32_t parity) {
+    if (older == nullptr && newer == nullptr) return;
+    bool ready = lane == 0 ? mbar_try_wait(bar, parity) : true;
+    if (!__all_sync(~0u, ready)) catch_up(lane);
+  }
 };
 
 // Sum over blocks lo .. hi (at most 8) of a cluster of the four floats at
@@ -240,25 +248,25 @@ __device__ __forceinline__ void split_terms(float4 v, uint2 (&out)[TERMS]) {
 }
 
 // ------------------------------------------------------------------- contract
-// out[m][j] = f sum_c in[m][c] W(j, c), f = scale[a] or 1; W(j, c) = w[a][j][c]
-// (TRANS false: A) or w[a][c][j] (TRANS true: B, an operand whose rows run
-// along the contraction).  One block per row tile and slice of the contracted
+// t[m][j] = sum_c in[m][c] W(j, c), W(j, c) = w[a][j][c] (TRANS false: A), or
+// dt[m][j] = scale[a] sum_c in[m][c] W(j, c), W(j, c) = w[a][c][j] (TRANS true:
+// B, an operand whose rows run along the contraction).  One block per row tile and slice of the contracted
 // dimension: TMA brings the tile's rows as a box, 64 columns a stage, where they
 // are neighbours (else a warp copies them), and the weight's box beside them;
 // one thread issues tcgen05.mma (M = 128, N = RT, sums in tensor memory), so that
 // reading the rows costs the SM next to no instructions.  The blocks of a cluster hold the slices of one tile and add
 // their partial sums through distributed shared memory in a fixed order.  The
-// forward pass stores t by row in fp32; the backward pass stores dt, and beside
-// it t, as bf16 terms by tile, 128 rows each with zeros past the tile's last:
-// the operand that the outer products and dx read.
+// operand of the second products is stored as bf16 terms by tile, 128 rows each
+// with zeros past the tile's last: scale t (forward, beside t by row in fp32),
+// or dt and t (backward).
 struct ContractArgs {
   const uint16_t *in;  // as tm_in
   int64_t ld;
   const float *scale;  // nullptr: 1
   const int32_t *plan;
-  float *out;             // forward: t [M][R]
-  const float *t;         // backward: t [M][R]
-  uint16_t *vt, *vdt;     // backward: [TERMS][max_tiles][128][R]
+  float *t;               // [M][R]; forward writes it, backward reads it
+  uint16_t *v;            // [TERMS][max_tiles][128][R]: scale t (forward), dt
+  uint16_t *vt;           // backward: t, laid out as v
   int64_t M, max_tiles;
   int32_t C, R, L;
   int *status;
@@ -278,7 +286,7 @@ struct ContractSmem {
   static_assert(kTileRows * kPartRow * 4 <= kBars, "partial sums reuse the stages");
 };
 
-// TERMS 0: the forward pass.
+// TRANS false: the forward pass, true: the backward pass.
 template <int RT, bool TRANS, int TERMS>
 __global__ void __launch_bounds__(kContractThreads)
     lora_contract_kernel(const __grid_constant__ CUtensorMap tm_in,
@@ -352,6 +360,7 @@ __global__ void __launch_bounds__(kContractThreads)
         bool ok = true;
         uint8_t *in = smem + st * S::kStage;
         const int c0 = c_lo + step * 64;
+        late.before_wait(lane, &empty[st], phase ^ 1);
         if (lane == 0) {
           ok = bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
           if (ok) {
@@ -435,37 +444,37 @@ __global__ void __launch_bounds__(kContractThreads)
             steps > 0 ? make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]) : make_uint4(0, 0, 0, 0);
     }
     if (slices > 1) cluster.sync(); else __syncthreads();
-    const float f = p.scale ? p.scale[bin] : 1.0f;
+    const float f = p.scale[bin];
     const int quads = p.R / 4;
-    const int total = ok ? (TERMS > 0 ? kTileRows : count) * quads : 0;
+    const int total = ok ? kTileRows * quads : 0;
     for (int e = rank * kContractThreads + threadIdx.x; e < total;
          e += slices * kContractThreads) {
       const int r = e / quads, j = (e - r * quads) * 4;
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (TERMS == 0 || r < count) {
-        s = slices > 1 ? cluster_sum(cluster, part, 0, slices - 1, [&](int) { return r * PS + j; })
-                       : *reinterpret_cast<const float4 *>(part + r * PS + j);
-        s = make_float4(f * s.x, f * s.y, f * s.z, f * s.w);
-      }
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f), t = s;
       const int row = rec[4 + r];
       const int64_t at = static_cast<int64_t>(row) * p.R + j;
-      if constexpr (TERMS == 0) {
-        if (store_ok(p.status, row >= 0 && row < p.M))
-          *reinterpret_cast<float4 *>(p.out + at) = s;
-      } else {
-        const int64_t place = static_cast<int64_t>(blockIdx.x) * kTileRows + r;
-        if (!store_ok(p.status, place < p.max_tiles * kTileRows)) continue;
-        float4 tv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (r < count) tv = *reinterpret_cast<const float4 *>(p.t + at);
-        uint2 d[TERMS], t[TERMS];
-        split_terms<TERMS>(s, d);
-        split_terms<TERMS>(tv, t);
-#pragma unroll
-        for (int q = 0; q < TERMS; ++q) {
-          const int64_t to = (q * p.max_tiles * kTileRows + place) * p.R + j;
-          *reinterpret_cast<uint2 *>(p.vdt + to) = d[q];
-          *reinterpret_cast<uint2 *>(p.vt + to) = t[q];
+      if (r < count) {
+        s = slices > 1 ? cluster_sum(cluster, part, 0, slices - 1, [&](int) { return r * PS + j; })
+                       : *reinterpret_cast<const float4 *>(part + r * PS + j);
+        if constexpr (TRANS) {
+          t = *reinterpret_cast<const float4 *>(p.t + at);
+        } else if (store_ok(p.status, row >= 0 && row < p.M)) {
+          *reinterpret_cast<float4 *>(p.t + at) = s;
         }
+        s = make_float4(f * s.x, f * s.y, f * s.z, f * s.w);
+      }
+      const int64_t place = static_cast<int64_t>(blockIdx.x) * kTileRows + r;
+      if (!store_ok(p.status, place < p.max_tiles * kTileRows)) continue;
+      uint2 d[TERMS];
+      split_terms<TERMS>(s, d);
+#pragma unroll
+      for (int q = 0; q < TERMS; ++q)
+        *reinterpret_cast<uint2 *>(p.v + (q * p.max_tiles * kTileRows + place) * p.R + j) = d[q];
+      if constexpr (TRANS) {
+        split_terms<TERMS>(t, d);
+#pragma unroll
+        for (int q = 0; q < TERMS; ++q)
+          *reinterpret_cast<uint2 *>(p.vt + (q * p.max_tiles * kTileRows + place) * p.R + j) = d[q];
       }
     }
     if (slices > 1) cluster.sync();  // no block leaves while its sums are read
@@ -481,286 +490,451 @@ __global__ void __launch_bounds__(kContractThreads)
 }
 
 // --------------------------------------------------------------------- expand
-// out[m][c] = base[m][c] + f sum_j t[m][j] W(j, c); W(j, c) = w[a][c][j] (TRANS
-// false: B, t fp32 by row) or w[a][j][c] (TRANS true: A, t bf16 by tile).
-// Persistent blocks, one per SM, take equal shares of the units (row tile, slab
-// of 128 columns), neighbouring slabs of a tile in a row, so that t is loaded
-// once for many slabs.  Every thread copies the pieces of base that it will
-// add to, 16 bytes each, asynchronously into slots of its own some units ahead
-// (nobody else reads them, so they need no barrier), and writes its sums back
-// in 16-byte pieces: the columns of a slab are dealt to the product's columns
-// so that the eight that a thread holds of a row in four accumulator tiles are
-// neighbours.  The products add onto base in the accumulators (the scale is in
-// t), so that an element costs its two conversions and no arithmetic.  Column 32 b + 8 c + 2 j + e is
-// column 2 c + e of tile 4 b + j; the weight slab is permuted accordingly on
-// its way into shared memory.  Rows without an adapter are copied from base
-// (left alone when out is base).
+// out[m][c] = base[m][c] + sum_j v[m][j] W(j, c); W(j, c) = w[a][c][j] (TRANS
+// false: B, v = scale t) or w[a][j][c] (TRANS true: A, v = dt); v as TERMS bf16
+// terms by tile.  Persistent blocks, one per SM, take equal shares of the units
+// (row tile, slab of 256 bytes of columns), neighbouring slabs of a tile in a
+// row.  Per unit TMA brings base and the weight slab into a stage, one thread
+// issues the products (M = 128 rows, sums in tensor memory, two buffers), and
+// eight warps add the sums into base where it stands in the stage and store it
+// from there, by TMA where a warp's 32 rows are neighbours.  On its way through
+// the SM an element meets one 16-byte shared load and store and an addition:
+// with the products on the warp-level path, whose operands pass through the
+// same load pipe, that pipe was the bound (8858 x 6144, rank 64: 59 us).
+// Scattered rows of base are copied by two warps.  Rows without an adapter are
+// copied from base (left alone when out is base).
 struct ExpandArgs {
-  const float *t;      // TRANS false: [M][R]
-  const uint16_t *vt;  // TRANS true: [max_tiles][128][R]
-  const uint16_t *w;
-  const float *scale;  // nullptr: 1
   const int32_t *plan;
   const void *base;    // nullptr: 0
   int64_t ld_base;
   void *out;
   int64_t ld_out;
-  int64_t M;
+  int64_t M, max_tiles;
   int32_t C, R, L;
   int *status;
 };
+struct ExpandMaps {
+  CUtensorMap base, out, w, v;
+};
 
-constexpr int kExpandThreads = 512;
+constexpr int kExpandWarps = 8;                            // adding and storing
+constexpr int kExpandThreads = 64 + 32 * kExpandWarps + 64;  // producer, MMA, two copying
 
-template <int RT, bool TRANS, bool F32>
+template <int RT, bool F32>
 struct ExpandSmem {
-  static constexpr int kTerms = F32 ? 3 : 1;  // bf16 terms of t
-  static constexpr int kSlab = F32 || RT > 64 ? 64 : 128;  // columns of a unit
-  static constexpr int kTRow = RT * 2 + 16;
-  static constexpr int kT = kTerms * kTileRows * kTRow;
-  static constexpr int kWRow = TRANS ? kSlab * 2 + 16 : RT * 2 + 16;
-  static constexpr int kW = TRANS ? RT * kWRow : kSlab * kWRow;
-  static constexpr int kPieces = kTileRows * kSlab * (F32 ? 4 : 2) / 16 / kExpandThreads;
-  static constexpr int kBase = kPieces * kExpandThreads * 16;
-  static constexpr int kStage = kW + kBase;
-  static constexpr int kFit = (224 * 1024 - kT) / kStage;
+  static constexpr int kTerms = F32 ? 3 : 1;
+  static constexpr int kSlab = F32 ? 64 : 128;  // columns of a unit
+  static constexpr int kBase = kTileRows * 256;
+  static constexpr int kW = kSlab * RT * 2;
+  static constexpr int kStage = kBase + kW;
+  static constexpr int kA = kTerms * kTileRows * RT * 2;
+  static constexpr int kABufs = kA <= 48 * 1024 ? 2 : 1;
+  static constexpr int kFit = (226 * 1024 - kABufs * kA) / kStage;
   static constexpr int kStages = kFit > 4 ? 4 : kFit;
-  static constexpr int kBytes = kT + kStages * kStage;
+  static constexpr int kAAt = kStages * kStage;
+  static constexpr int kBars = kAAt + kABufs * kA;
+  static constexpr int kBytes = kBars + (2 * kStages + 9) * 8 + kStages * 4 + 16 + 1024;
   static_assert(kStages >= 2, "one unit ahead at least");
   static_assert(kBytes <= 232448, "dynamic shared memory above the per-block limit");
 };
 
+enum { kUnitNone = 1, kUnitFirst = 2, kUnitLast = 4, kUnitEnd = 8 };
+
+// A block's walk over its units; every role makes the same one.  Units of rows
+// without an adapter are left out when out is base.
+struct Units {
+  const int32_t *recs;
+  int slabs, tile, slab, left;
+  __device__ __forceinline__ void init(const int32_t *plan, int tiles, int L, int n_slabs) {
+    recs = plan + plan_recs_at(L);
+    slabs = n_slabs;
+    const int64_t units = static_cast<int64_t>(tiles) * n_slabs;
+    const int64_t lo = units * blockIdx.x / gridDim.x;
+    left = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x - lo);
+    tile = static_cast<int>(lo / n_slabs);
+    slab = static_cast<int>(lo - static_cast<int64_t>(tile) * n_slabs);
+  }
+  // slabs of the current tile that are this block's
+  __device__ __forceinline__ int here() const { return left < slabs - slab ? left : slabs - slab; }
+  __device__ __forceinline__ void next_tile() {
+    left -= here();
+    slab = 0;
+    ++tile;
+  }
+  __device__ __forceinline__ const int32_t *rec(int t) const {
+    return recs + static_cast<int64_t>(t) * kRecWords;
+  }
+};
+
 template <int RT, bool TRANS, bool F32>
-__global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const ExpandArgs p) {
-  using S = ExpandSmem<RT, TRANS, F32>;
-  constexpr int E = F32 ? 4 : 2;
-  constexpr int Q = F32 ? 2 : 1;       // 16-byte pieces of eight columns
-  constexpr int SLAB = S::kSlab;
-  constexpr int NB = SLAB / 64;        // blocks of 32 columns of a warp
-  constexpr int KK = RT / 16;
-  static_assert(S::kPieces == 2 * NB * Q, "a thread's share of a unit");
-  extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t sm = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int wm = warp & 7, wn = warp >> 3;  // 16 rows, half of the slab
-  const int g = lane >> 2, c8 = (lane & 3) * 8;
+__global__ void __launch_bounds__(kExpandThreads, 1)
+    lora_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs p) {
+  using S = ExpandSmem<RT, F32>;
+  constexpr int STAGES = S::kStages, SLAB = S::kSlab, E = F32 ? 4 : 2;
+  constexpr int BOX = 128 / E;  // columns of a 128-byte box
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kBars);
+  uint64_t *empty = full + STAGES;
+  uint64_t *acc_full = empty + STAGES;
+  uint64_t *acc_empty = acc_full + 2;
+  uint64_t *a_full = acc_empty + 2;
+  uint64_t *a_empty = a_full + 2;
+  uint64_t *done = a_empty + 2;
+  volatile int *meta = reinterpret_cast<volatile int *>(done + 1);  // [STAGES]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1) + STAGES;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kTimeout = SQ_ERR_DEVICE_TIMEOUT;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 3);                  // producer, two copying warps
+      mbar_init(&empty[s], kExpandWarps + 1);  // storing warps, MMA issuer
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], kExpandWarps);
+      mbar_init(&a_full[b], 1);
+      mbar_init(&a_empty[b], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.base);
+    prefetch_tmap(&maps.w);
+    prefetch_tmap(&maps.v);
+    prefetch_tmap(&maps.out);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 2 * SLAB);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
 
   // base, weights and plan were complete before the kernel ahead of this one
-  // began; only its own output, t, has to be waited for
-  const int32_t *recs = p.plan + plan_recs_at(p.L);
-  const int slabs = (p.C + SLAB - 1) / SLAB;
+  // began; only its own output, v, has to be waited for
   const bool fits = plan_fits(p.plan, p.M, p.L, p.status);
-  const int tiles = fits ? p.plan[3] : 0;
-  const int64_t units = static_cast<int64_t>(tiles) * slabs;
-  const int64_t u_lo = units * blockIdx.x / gridDim.x;
-  const int mine = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x - u_lo);
-  const bool in_place = p.base == p.out;
-  const int tile0 = static_cast<int>(u_lo / slabs), slab0 = static_cast<int>(u_lo % slabs);
+  Units u;
+  u.init(p.plan, fits ? p.plan[3] : 0, p.L, (p.C + SLAB - 1) / SLAB);
+  const bool has_base = p.base != nullptr, in_place = p.base == p.out;
+  if (warp != 0) grid_dependency_wait();
 
-  // A unit's weights and base -> its stage.  The thread's rows of base are
-  // wm 16 + g (+ 8), its columns wn SLAB/2 + 32 b + c8 .. + 7.
-  const int my_col = wn * (SLAB / 2) + c8;
-  int l_tile = tile0, l_slab = slab0;
-  const uint8_t *l_base[2] = {nullptr, nullptr};  // nullptr: zeros
-  const uint16_t *l_w = nullptr;                  // nullptr: no adapter
-  auto next_tile = [&]() {
-    const int32_t *rec = recs + static_cast<int64_t>(l_tile) * kRecWords;
-    const int bin = rec[0], count = rec[1];
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    uint32_t armed = 0, armed_parity = 0;
+    int step = 0, a_tiles = 0;
+    bool ok = true, waited = false;
+    int pending_tile[STAGES], pending = 0;  // tiles met before v may be read
+    // v of a tile -> its buffer
+    auto load_v = [&](int tile) {
+      const int b = a_tiles % S::kABufs;
+      if (!bounded_wait(&a_empty[b], ((a_tiles / S::kABufs) & 1) ^ 1, abort_flag, p.status,
+                        kTimeout))
+        return false;
+      mbar_arrive_expect_tx(&a_full[b], S::kA);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = wm * 16 + g + h * 8;
-      l_base[h] = p.base != nullptr && r < count
-                      ? static_cast<const uint8_t *>(p.base) +
-                            (rec[4 + r] * p.ld_base + l_slab * SLAB + my_col) * E
-                      : nullptr;
-    }
-    l_w = bin < p.L ? p.w + static_cast<int64_t>(bin) * p.R * p.C : nullptr;
-  };
-  auto load = [&](int stage) {
-    const uint32_t sw = sm + S::kT + stage * S::kStage;
-    const uint32_t sb = sw + S::kW + tid * 16;
-    const int left = p.C - l_slab * SLAB;  // columns from this slab on
+      for (int s = 0; s < S::kTerms; ++s)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const bool ok = l_base[h] != nullptr && my_col + b * 32 < left;
-        const uint8_t *src = ok ? l_base[h] + b * 32 * E : reinterpret_cast<const uint8_t *>(p.w);
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-          cp_async16(sb + ((h * NB + b) * Q + q) * kExpandThreads * 16, ok ? src + q * 16 : src, ok);
-      }
-      if (l_base[h] != nullptr) l_base[h] += SLAB * E;
-    }
-    if (l_w != nullptr) {
-      if constexpr (!TRANS) {
-        constexpr int PER = RT / 8;
-        const uint16_t *w = l_w + static_cast<int64_t>(l_slab) * SLAB * p.R;
-#pragma unroll
-        for (int k = tid; k < SLAB * PER; k += kExpandThreads) {
-          const int r = k / PER, cc = k % PER;
-          const int at = (r & ~31) | (((r >> 1) & 3) << 3) | (((r >> 3) & 3) << 1) | (r & 1);
-          const bool ok = r < left && cc * 8 < p.R;
-          cp_async16(sw + at * S::kWRow + cc * 16, ok ? w + r * p.R + cc * 8 : p.w, ok);
-        }
-      } else {
-        constexpr int PER = SLAB / 2;  // pairs of columns
-        const uint16_t *w = l_w + l_slab * SLAB;
-#pragma unroll 8
-        for (int k = tid; k < RT * PER; k += kExpandThreads) {
-          const int r = k / PER, cc = k % PER;
-          const int at = (cc & ~15) | ((cc & 3) << 2) | ((cc >> 2) & 3);
-          const bool ok = r < p.R && cc * 2 < left;
-          cp_async4(sw + r * S::kWRow + at * 4,
-                    ok ? w + static_cast<int64_t>(r) * p.C + cc * 2 : p.w, ok);
-        }
-      }
-    }
-    if (++l_slab == slabs) {
-      l_slab = 0;
-      if (++l_tile < tiles) next_tile();
-    }
-  };
-
-  if (mine > 0) next_tile();
-#pragma unroll
-  for (int s = 0; s < S::kStages - 1; ++s) {
-    if (s < mine) load(s);
-    cp_async_commit();
-  }
-  grid_dependency_wait();
-
-  int tile = tile0, slab = slab0, bin = 0, count = 0, stage = 0;
-  uint8_t *dst[2] = {nullptr, nullptr};  // nullptr: no row
-  bool fresh = true;
-  for (int i = 0; i < mine; ++i) {
-    if (fresh) {
-      const int32_t *rec = recs + static_cast<int64_t>(tile) * kRecWords;
-      bin = rec[0];
-      count = rec[1];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = wm * 16 + g + h * 8, row = rec[4 + r];
-        dst[h] = r < count && store_ok(p.status, row >= 0 && row < p.M)
-                     ? static_cast<uint8_t *>(p.out) + (row * p.ld_out + slab * SLAB + my_col) * E
-                     : nullptr;
-      }
-      if (i > 0) __syncthreads();  // the last tile's t is no longer read
-      if (bin < p.L) {
-        const float f = p.scale ? p.scale[bin] : 1.0f;
-        if constexpr (TRANS) {
-          for (int k = tid; k < kTileRows * (RT / 8); k += kExpandThreads) {
-            const int r = k / (RT / 8), cc = k % (RT / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (cc * 8 < p.R)
-              v = *reinterpret_cast<const uint4 *>(
-                  p.vt + (static_cast<int64_t>(tile) * kTileRows + r) * p.R + cc * 8);
-            *reinterpret_cast<uint4 *>(smem + r * S::kTRow + cc * 16) = v;
+        for (int h = 0; h < RT / 64; ++h)
+          tma_load_3d(smem + S::kAAt + b * S::kA + (s * (RT / 64) + h) * 16384, &maps.v,
+                      &a_full[b], h * 64, tile * kTileRows, s);
+      ++a_tiles;
+      return true;
+    };
+    auto catch_up = [&]() {
+      grid_dependency_wait();
+      waited = true;
+      for (int i = 0; i < pending && ok; ++i) ok = load_v(pending_tile[i]);
+    };
+    if (lane == 0) {
+      for (; u.left > 0 && ok; u.next_tile()) {
+        const int32_t *rec = u.rec(u.tile);
+        const int4 h = *reinterpret_cast<const int4 *>(rec);
+        const int first = rec[4];
+        const bool none = h.x >= p.L, run = h.w != 0;
+        if (none && in_place) continue;
+        const int n = u.here();
+        for (int i = 0; i < n && ok; ++i, ++step) {
+          if (!waited && step == STAGES) catch_up();
+          const int st = step % STAGES;
+          const uint32_t phase = (step / STAGES) & 1;
+          ok = ok && bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, kTimeout);
+          if (!ok) break;
+          meta[st] = (none ? kUnitNone : 0) | (i == 0 ? kUnitFirst : 0) |
+                     (i == n - 1 ? kUnitLast : 0);
+          const bool box = has_base && run;
+          mbar_arrive_expect_tx(&full[st], (box ? S::kBase : 0) + (none ? 0 : S::kW));
+          uint8_t *to = smem + st * S::kStage;
+          const int c0 = (u.slab + i) * SLAB;
+          if (box) {
+            tma_load_2d(to, &maps.base, &full[st], c0, first);
+            // a box past the last column reads as zeros
+            tma_load_2d(to + 16384, &maps.base, &full[st], c0 + BOX, first);
           }
-        } else {
-          for (int k = tid; k < kTileRows * (RT / 4); k += kExpandThreads) {
-            const int r = k / (RT / 4), cc = k % (RT / 4);
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (r < count && cc * 4 < p.R)
-              v = *reinterpret_cast<const float4 *>(
-                  p.t + static_cast<int64_t>(rec[4 + r]) * p.R + cc * 4);
-            v = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
-            uint2 o[S::kTerms];
-            split_terms<S::kTerms>(v, o);
+          if (!none) {
+            if constexpr (!TRANS) {
 #pragma unroll
-            for (int s = 0; s < S::kTerms; ++s)
-              *reinterpret_cast<uint2 *>(smem + (s * kTileRows + r) * S::kTRow + cc * 8) = o[s];
-          }
-        }
-      }
-    }
-    cp_async_wait<S::kStages - 2>();
-    __syncthreads();
-    if (i + S::kStages - 1 < mine) load(stage == 0 ? S::kStages - 1 : stage - 1);
-    cp_async_commit();
-    if (wm * 16 < count && (bin < p.L || !in_place)) {
-      const uint8_t *st = smem + S::kT + stage * S::kStage;
-      float acc[4 * NB][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(
-                st + S::kW + (((h * NB + b) * Q + q) * kExpandThreads + tid) * 16);
-            const uint32_t o[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if constexpr (F32) {
-                acc[b * 4 + q * 2 + j / 2][2 * h + j % 2] = __uint_as_float(o[j]);
-              } else {
-                acc[b * 4 + j][2 * h] = bf16_lo(o[j]);
-                acc[b * 4 + j][2 * h + 1] = bf16_hi(o[j]);
-              }
-            }
-          }
-      if (bin < p.L) {
-        const uint32_t sw = smem_u32(st);
-#pragma unroll 1
-        for (int s = S::kTerms - 1; s >= 0; --s) {  // the smallest terms first
-#pragma unroll
-          for (int kk = 0; kk < KK; ++kk) {
-            uint32_t a[4];
-            ldsm_x4(sm + (s * kTileRows + wm * 16 + (lane & 15)) * S::kTRow +
-                        (kk * 16 + (lane >> 4) * 8) * 2,
-                    a);
-#pragma unroll
-            for (int n = 0; n < 4 * NB; n += 2) {
-              uint32_t b[4];
-              const int col = wn * (SLAB / 2) + n * 8;
-              if constexpr (!TRANS)
-                ldsm_x4(sw + (col + (lane & 7) + ((lane >> 4) << 3)) * S::kWRow +
-                            (kk * 16 + ((lane >> 3) & 1) * 8) * 2,
-                        b);
-              else
-                ldsm_x4_t(sw + (kk * 16 + (lane & 15)) * S::kWRow + (col + (lane >> 4) * 8) * 2,
-                          b);
-              mma_bf16(acc[n], a, b[0], b[1]);
-              mma_bf16(acc[n + 1], a, b[2], b[3]);
-            }
-          }
-        }
-      }
-      const int left = p.C - slab * SLAB;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          if (dst[h] == nullptr || my_col + b * 32 >= left) continue;
-          uint32_t o[4 * Q];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x = acc[b * 4 + j][2 * h], y = acc[b * 4 + j][2 * h + 1];
-            if constexpr (F32) {
-              o[2 * j] = __float_as_uint(x);
-              o[2 * j + 1] = __float_as_uint(y);
+              for (int q = 0; q < RT / 64; ++q)
+                tma_load_3d(to + S::kBase + q * SLAB * 128, &maps.w, &full[st], q * 64, c0, h.x);
             } else {
-              o[j] = bf16x2(x, y);
+#pragma unroll
+              for (int q = 0; q < SLAB / 64; ++q)
+                tma_load_3d(to + S::kBase + q * RT * 128, &maps.w, &full[st], c0 + q * 64, 0, h.x);
             }
           }
-          uint4 *to = reinterpret_cast<uint4 *>(dst[h] + b * 32 * E);
-#pragma unroll
-          for (int q = 0; q < Q; ++q)
-            to[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          armed |= 1u << st;
+          armed_parity = (armed_parity & ~(1u << st)) | (phase << st);
+          if (i == 0 && !none) {
+            if (waited)
+              ok = load_v(u.tile);
+            else
+              pending_tile[pending++] = u.tile;
+          }
         }
+      }
+      if (!waited) catch_up();
+      if (ok) {
+        const int st = step % STAGES;
+        const uint32_t phase = (step / STAGES) & 1;
+        if (bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, kTimeout)) {
+          meta[st] = kUnitEnd;
+          armed &= ~(1u << st);  // its last copy has been read
+          mbar_arrive(&full[st]);
+          mbar_arrive(&full[st]);
+          mbar_arrive(&full[st]);
+        }
+      }
+      // never leave with a copy in flight into this block's shared memory
+      for (int s = 0; s < STAGES; ++s)
+        if (armed & (1u << s)) mbar_wait(&full[s], (armed_parity >> s) & 1u, kBoundedWaitNs);
+      for (int t = a_tiles > S::kABufs ? a_tiles - S::kABufs : 0; t < a_tiles; ++t)
+        mbar_wait(&a_full[t % S::kABufs], (t / S::kABufs) & 1, kBoundedWaitNs);
     }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16(kTileRows, SLAB) | (TRANS ? kIdescTransB : 0u);
+      const int ks = (p.R + 15) / 16;
+      int a_tiles = -1, unit = 0;
+      for (int step = 0;; ++step) {
+        const int st = step % STAGES;
+        if (!bounded_wait(&full[st], (step / STAGES) & 1, abort_flag, p.status, kTimeout)) break;
+        const int flags = meta[st];
+        if (flags & kUnitEnd) break;
+        if (flags & kUnitNone) {
+          mbar_arrive(&empty[st]);
+          continue;
+        }
+        if (flags & kUnitFirst) {
+          ++a_tiles;
+          if (!bounded_wait(&a_full[a_tiles % S::kABufs], (a_tiles / S::kABufs) & 1, abort_flag,
+                            p.status, kTimeout))
+            break;
+        }
+        const int buf = unit & 1;
+        if (!bounded_wait(&acc_empty[buf], ((unit >> 1) & 1) ^ 1, abort_flag, p.status, kTimeout))
+          break;
+        ++unit;
+        tc_fence_after();
+        const uint32_t sa = smem_u32(smem + S::kAAt + (a_tiles % S::kABufs) * S::kA);
+        const uint32_t sb = smem_u32(smem + st * S::kStage + S::kBase);
+#pragma unroll 1
+        for (int s = S::kTerms - 1; s >= 0; --s)  // the smallest terms first
+#pragma unroll 1
+          for (int kk = 0; kk < ks; ++kk)
+            mma_bf16_tc(tmem + buf * SLAB,
+                        sdesc_kmajor_sw128(sa + (s * (RT / 64) + kk / 4) * 16384 + (kk & 3) * 32),
+                        TRANS ? sdesc_mnmajor_sw128(sb + kk * 2048, RT * 128)
+                              : sdesc_kmajor_sw128(sb + kk / 4 * (SLAB * 128) + (kk & 3) * 32),
+                        idesc, s < S::kTerms - 1 || kk > 0);
+        mma_commit(&empty[st]);
+        mma_commit(&acc_full[buf]);
+        if (flags & kUnitLast) mma_commit(&a_empty[a_tiles % S::kABufs]);
+      }
+      mma_commit(done);
+    }
+    __syncwarp();
+  } else if (warp < 2 + kExpandWarps) {
+    // ------------------------------------------- adding and storing warps
+    // thread: row of the tile; warp: a quarter of the rows, half of the slab
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int r = quarter * 32 + lane;
+    int step = 0, unit = 0, storing = -1;  // storing: stage whose tensor store is under way
+    bool ok = true;
+    int4 h = make_int4(0, 0, 0, 0);
+    int my_row = 0;
+    auto read = [&](int tile) {
+      const int32_t *rec = u.rec(tile);
+      h = *reinterpret_cast<const int4 *>(rec);
+      my_row = rec[4 + r];
+    };
+    if (u.left > 0) read(u.tile);
+    while (u.left > 0 && ok) {
+      const int bin = h.x, count = h.y, row = my_row;
+      const int n = u.here(), slab = u.slab;
+      // this warp's rows: how many, and whether one box holds them
+      const int mine = count - quarter * 32 < 32 ? count - quarter * 32 : 32;
+      const bool box = h.w != 0 && mine == 32;
+      const int first = __shfl_sync(~0u, row, 0);
+      u.next_tile();
+      if (u.left > 0) read(u.tile);
+      const bool none = bin >= p.L;
+      if (none && in_place) continue;
+      for (int i = 0; i < n; ++i, ++step) {
+        const int st = step % STAGES;
+        ok = bounded_wait(&full[st], (step / STAGES) & 1, abort_flag, p.status, kTimeout);
+        if (!ok) break;
+        uint8_t *data = smem + st * S::kStage + half * 16384;
+        const int c0 = (slab + i) * SLAB + half * BOX;
+        if (!none) {
+          const int buf = unit & 1;
+          ok = bounded_wait(&acc_full[buf], (unit >> 1) & 1, abort_flag, p.status, kTimeout);
+          if (!ok) break;
+          ++unit;
+          tc_fence_after();
+          const uint32_t src =
+              tmem + buf * SLAB + half * BOX + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (dst[h] != nullptr) dst[h] += SLAB * E;
-    if (++stage == S::kStages) stage = 0;
-    fresh = ++slab == slabs;
-    if (fresh) {
-      slab = 0;
-      ++tile;
+          for (int c = 0; c < BOX; c += 32) {
+            uint32_t a[32];
+            __syncwarp();
+            tmem_ld_32x32b_x32(src + c, a);
+            tmem_ld_wait();
+            if (c + 32 == BOX) {  // the sums are out of tensor memory
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            }
+#pragma unroll
+            for (int q = 0; q < 2 * E; ++q) {  // 16-byte chunks of 32 columns
+              uint4 *at = reinterpret_cast<uint4 *>(data + swz128(r, c * E / 16 + q));
+              uint4 v = has_base ? *at : make_uint4(0, 0, 0, 0);
+              if constexpr (F32) {
+                v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(a[q * 4]));
+                v.y = __float_as_uint(__uint_as_float(v.y) + __uint_as_float(a[q * 4 + 1]));
+                v.z = __float_as_uint(__uint_as_float(v.z) + __uint_as_float(a[q * 4 + 2]));
+                v.w = __float_as_uint(__uint_as_float(v.w) + __uint_as_float(a[q * 4 + 3]));
+              } else {
+                auto add = [&](uint32_t o, int j) {
+                  return bf16x2(bf16_lo(o) + __uint_as_float(a[q * 8 + j]),
+                                bf16_hi(o) + __uint_as_float(a[q * 8 + j + 1]));
+                };
+                v = make_uint4(add(v.x, 0), add(v.y, 2), add(v.z, 4), add(v.w, 6));
+              }
+              *at = v;
+            }
+          }
+        } else if (!has_base) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4 *>(data + swz128(r, q)) = make_uint4(0, 0, 0, 0);
+        }
+        if (storing >= 0 && !box) {  // settle the last tensor store first
+          if (lane == 0) {
+            bulk_wait_read_all();
+            mbar_arrive(&empty[storing]);
+          }
+          storing = -1;
+        }
+        if (box) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (c0 < p.C) tma_store_2d(&maps.out, data + quarter * 4096, c0, first);
+            bulk_commit_group();
+            if (storing >= 0) {
+              bulk_wait_read_but_one();
+              mbar_arrive(&empty[storing]);
+            }
+          }
+          storing = st;
+        } else {
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rr = k * 4 + (lane >> 3), q = lane & 7;
+            const int64_t to = __shfl_sync(~0u, row, rr);
+            const int col = c0 + q * (16 / E);
+            if (rr < mine && col < p.C &&
+                store_ok(p.status, to >= 0 && to < p.M && col + 16 / E <= p.ld_out))
+              *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) +
+                                         (to * p.ld_out + col) * E) =
+                  *reinterpret_cast<const uint4 *>(data + swz128(quarter * 32 + rr, q));
+          }
+          // the stage is next written by TMA
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[st]);
+        }
+      }
     }
+    if (lane == 0) {
+      bulk_wait_all();  // every tensor store of this warp is complete
+      if (storing >= 0) mbar_arrive(&empty[storing]);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------- copying warps
+    // scattered base: 64 rows each, lane: rows 2 i + lane / 16, chunk lane % 16
+    const int r0 = (warp - 2 - kExpandWarps) * 64 + (lane >> 4);
+    const int q = lane & 15;
+    int step = 0;
+    bool ok = true;
+    LateArrival late;
+    for (; u.left > 0 && ok; u.next_tile()) {
+      const int32_t *rec = u.rec(u.tile);
+      const int4 h = *reinterpret_cast<const int4 *>(rec);
+      if (h.x >= p.L && in_place) continue;
+      const bool copies = has_base && h.w == 0;
+      int32_t rows[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) rows[i] = copies ? rec[4 + r0 + 2 * i] : 0;
+      const int n = u.here();
+      for (int i = 0; i < n; ++i, ++step) {
+        const int st = step % STAGES;
+        const uint32_t parity = ((step / STAGES) & 1) ^ 1;
+        late.before_wait(lane, &empty[st], parity);
+        if (lane == 0) ok = bounded_wait(&empty[st], parity, abort_flag, p.status, kTimeout);
+        ok = __shfl_sync(~0u, ok, 0);
+        if (!ok) break;
+        if (!copies) {
+          late.catch_up(lane);
+          if (lane == 0) mbar_arrive(&full[st]);
+          continue;
+        }
+        const int col = (u.slab + i) * SLAB + q * (16 / E);
+        const uint32_t to = smem_u32(smem + st * S::kStage) + (q >> 3) * 16384;
+        const uint8_t *src = static_cast<const uint8_t *>(p.base) + static_cast<int64_t>(col) * E;
+        if (col < p.C) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (r0 - (lane >> 4) + 2 * k >= h.y) break;
+            if (r0 + 2 * k < h.y)
+              cp_async16(to + swz128(r0 + 2 * k, q & 7), src + rows[k] * p.ld_base * E, true);
+          }
+        }
+        cp_async_commit();
+        late.push(lane, &full[st]);
+      }
+    }
+    late.catch_up(lane);
+    cp_async_wait<0>();
   }
-  cp_async_wait<0>();
+  bounded_wait(done, 0, abort_flag, p.status, kTimeout);
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * SLAB);
+  }
 }
 
 // ---------------------------------------------------------------------- outer
@@ -905,6 +1079,7 @@ __global__ void __launch_bounds__(kOuterThreads, OuterSmem<RT, TERMS>::kPerSm)
       const int st = step % STAGES;
       const uint32_t phase = (step / STAGES) & 1;
       ++step;
+      late.before_wait(lane, &empty[st], phase ^ 1);
       if (lane == 0) {
         ok = bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
         if (ok) {
@@ -1254,24 +1429,30 @@ cudaError_t launch(dim3 grid, int threads, int smem, int cluster, int dim, cudaS
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Tensor map of bf16 [d2][d1][d0] with row stride ld (elements), boxes of 64
-// columns by `rows`, 128-byte swizzle; d2 == 0: two dimensions.
-cudaError_t bf16_map(CUtensorMap *map, const void *ptr, int64_t d0, int64_t d1, int64_t d2,
-                     int64_t ld, int rows) {
+// Tensor map of [d2][d1][d0] with row stride ld (elements), boxes of 128 bytes by
+// `rows`, 128-byte swizzle; d2 == 0: two dimensions.
+cudaError_t tile_map(CUtensorMap *map, bool f32, const void *ptr, int64_t d0, int64_t d1,
+                     int64_t d2, int64_t ld, int rows) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (enc == nullptr) return cudaErrorNotSupported;
+  const int elem = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1),
                               static_cast<cuuint64_t>(d2)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2,
-                                 static_cast<cuuint64_t>(ld) * 2 * static_cast<cuuint64_t>(d1)};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), 1};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * elem,
+                                 static_cast<cuuint64_t>(ld) * elem * static_cast<cuuint64_t>(d1)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem), static_cast<cuuint32_t>(rows), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 == 0 ? 2 : 3, const_cast<void *>(ptr),
-             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+             d2 == 0 ? 2 : 3, const_cast<void *>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
+}
+cudaError_t bf16_map(CUtensorMap *map, const void *ptr, int64_t d0, int64_t d1, int64_t d2,
+                     int64_t ld, int rows) {
+  return tile_map(map, false, ptr, d0, d1, d2, ld, rows);
 }
 
 template <int RT, bool TRANS, int TERMS>
@@ -1293,13 +1474,25 @@ cudaError_t run_contract(const uint16_t *w, const ContractArgs &a, cudaStream_t 
 }
 
 template <int RT, bool TRANS, bool F32>
-cudaError_t run_expand(const ExpandArgs &a, cudaStream_t stream) {
-  using S = ExpandSmem<RT, TRANS, F32>;
-  const int64_t units = plan_max_tiles(a.M, a.L) * ((a.C + S::kSlab - 1) / S::kSlab);
+cudaError_t run_expand(const uint16_t *w, const uint16_t *v, const ExpandArgs &a,
+                       cudaStream_t stream) {
+  using S = ExpandSmem<RT, F32>;
+  ExpandMaps maps;
+  const void *base = a.base ? a.base : a.out;  // not read without a base
+  cudaError_t e = tile_map(&maps.base, F32, base, a.C, a.M, 0, a.base ? a.ld_base : a.ld_out,
+                           kTileRows);
+  if (e == cudaSuccess) e = tile_map(&maps.out, F32, a.out, a.C, a.M, 0, a.ld_out, 32);
+  if (e == cudaSuccess)
+    e = TRANS ? bf16_map(&maps.w, w, a.C, a.R, a.L, a.C, RT)
+              : bf16_map(&maps.w, w, a.R, a.C, a.L, a.R, S::kSlab);
+  if (e == cudaSuccess)
+    e = bf16_map(&maps.v, v, a.R, a.max_tiles * kTileRows, S::kTerms, a.R, kTileRows);
+  if (e != cudaSuccess) return e;
+  const int64_t units = a.max_tiles * ((a.C + S::kSlab - 1) / S::kSlab);
   const int sms = sm_count();
   return launch<lora_expand_kernel<RT, TRANS, F32>>(
       dim3(static_cast<unsigned>(units < sms ? units : sms)), kExpandThreads, S::kBytes, 1, 0,
-      stream, a);
+      stream, maps, a);
 }
 
 template <int RT, int TERMS>
@@ -1324,14 +1517,6 @@ cudaError_t by_rank(int R, F &&f) {
   if (R <= 64) return f(std::integral_constant<int, 64>());
   return f(std::integral_constant<int, 128>());
 }
-// The expansion's inner dimension, in which padding costs products.
-template <typename F>
-cudaError_t by_rank_fine(int R, F &&f) {
-  if (R <= 16) return f(std::integral_constant<int, 16>());
-  if (R <= 32) return f(std::integral_constant<int, 32>());
-  return by_rank(R, f);
-}
-
 template <int TERMS>
 cudaError_t run_backward(const LoraRequest &q, cudaStream_t stream) {
   if (q.M == 0) {
@@ -1343,7 +1528,7 @@ cudaError_t run_backward(const LoraRequest &q, cudaStream_t stream) {
   const int64_t max_tiles = plan_max_tiles(q.M, q.L), rows = max_tiles * kTileRows;
   uint16_t *vdt = static_cast<uint16_t *>(q.workspace);
   uint16_t *vt = vdt + TERMS * rows * q.R;
-  const ContractArgs c = {q.dy, q.lddy, q.scale, q.plan, nullptr, q.t, vt, vdt,
+  const ContractArgs c = {q.dy, q.lddy, q.scale, q.plan, q.t, vdt, vt,
                           q.M, max_tiles, N, q.R, q.L, q.status};
   cudaError_t e = by_rank(q.R, [&](auto rt) {
     return run_contract<decltype(rt)::value, true, TERMS>(q.B, c, stream);
@@ -1369,13 +1554,28 @@ cudaError_t run_backward(const LoraRequest &q, cudaStream_t stream) {
       });
   }
   if (e == cudaSuccess && q.dx != nullptr) {
-    const ExpandArgs x = {nullptr, vdt, q.A, nullptr, q.plan, q.base, q.ld_base, q.dx, q.lddx,
-                          q.M, K, q.R, q.L, q.status};
-    e = by_rank_fine(q.R, [&](auto rt) {
-      return run_expand<decltype(rt)::value, true, false>(x, stream);
+    const ExpandArgs x = {q.plan, q.base, q.ld_base, q.dx, q.lddx, q.M,
+                          max_tiles, K, q.R, q.L, q.status};
+    e = by_rank(q.R, [&](auto rt) {
+      return run_expand<decltype(rt)::value, true, false>(q.A, vdt, x, stream);
     });
   }
   return e;
+}
+
+template <bool F32>
+cudaError_t run_forward(const LoraRequest &q, cudaStream_t stream) {
+  const int64_t max_tiles = plan_max_tiles(q.M, q.L);
+  uint16_t *v = static_cast<uint16_t *>(q.workspace);
+  const ContractArgs c = {q.x, q.ldx, q.scale, q.plan, q.t, v, nullptr, q.M,
+                          max_tiles, static_cast<int32_t>(q.K), q.R, q.L, q.status};
+  const ExpandArgs x = {q.plan, q.base, q.ld_base, q.y, q.ldy, q.M,
+                        max_tiles, static_cast<int32_t>(q.N), q.R, q.L, q.status};
+  return by_rank(q.R, [&](auto rt) {
+    constexpr int RT = decltype(rt)::value;
+    const cudaError_t e = run_contract<RT, false, F32 ? 3 : 1>(q.A, c, stream);
+    return e != cudaSuccess ? e : run_expand<RT, false, F32>(q.B, v, x, stream);
+  });
 }
 
 }  // namespace
@@ -1400,19 +1600,7 @@ cudaError_t launch_lora_plan(const int32_t *adapter, int64_t M, int32_t L, int32
 }
 
 cudaError_t launch_lora_forward(const LoraRequest &q, cudaStream_t stream) {
-  const ContractArgs c = {q.x, q.ldx, nullptr, q.plan, q.t, nullptr, nullptr, nullptr,
-                          q.M, plan_max_tiles(q.M, q.L), static_cast<int32_t>(q.K), q.R, q.L,
-                          q.status};
-  const ExpandArgs e = {q.t, nullptr, q.B, q.scale, q.plan, q.base, q.ld_base, q.y, q.ldy, q.M,
-                        static_cast<int32_t>(q.N), q.R, q.L, q.status};
-  const cudaError_t err = by_rank(q.R, [&](auto rt) {
-    return run_contract<decltype(rt)::value, false, 0>(q.A, c, stream);
-  });
-  if (err != cudaSuccess) return err;
-  return by_rank_fine(q.R, [&](auto rt) {
-    constexpr int RT = decltype(rt)::value;
-    return q.f32 ? run_expand<RT, false, true>(e, stream) : run_expand<RT, false, false>(e, stream);
-  });
+  return q.f32 ? run_forward<true>(q, stream) : run_forward<false>(q, stream);
 }
 
 cudaError_t launch_lora_backward(const LoraRequest &q, cudaStream_t stream) {

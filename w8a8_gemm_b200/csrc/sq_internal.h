@@ -110,7 +110,7 @@ struct LoraRequest {
   uint16_t *dx;          // backward, may be nullptr
   void *dA, *dB;         // backward, both or neither
   float *t;              // [M][R]
-  void *workspace;       // backward
+  void *workspace;
   int64_t ldx, lddy, ld_base, ldy, lddx;
   int64_t M, N, K;
   int32_t R, L;
@@ -118,6 +118,7 @@ struct LoraRequest {
   int *status;
 };
 size_t lora_plan_words(int64_t M, int32_t L);
+// Of the backward call; the forward call uses half of it.
 size_t lora_workspace_bytes(int64_t M, int32_t R, int32_t L, bool f32);
 cudaError_t launch_lora_plan(const int32_t *adapter, int64_t M, int32_t L, int32_t *plan,
                              int *status, cudaStream_t stream);
