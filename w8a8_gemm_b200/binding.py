@@ -10,6 +10,7 @@ library returned SQ_OK.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -522,47 +523,95 @@ def sq_dualscale_seglinear_host_noalloc(x_host: torch.Tensor, d: Optional[torch.
 
 
 # ------------------------------------------- operators around the quantized linear
-_OUT = {torch.bfloat16: SQ_OUT_BF16, torch.float32: SQ_OUT_F32}
+# These calls are short on the GPU (a few microseconds for a decoding step), so
+# their checks are written to be short on the host: one comparison per tensor,
+# and an explanation looked for only when it fails.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_OUT = {_BF16: SQ_OUT_BF16, _F32: SQ_OUT_F32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _out_dtype(t, name: str) -> int:
-    """The ABI's number of a tensor's (or a dtype's) type, bf16 or fp32."""
-    dtype = t.dtype if isinstance(t, torch.Tensor) else t
+def _explain(name: str, t, dtype, shape, dev: int, contiguous: bool):
+    """Raises the reason for which t is not a tensor of this type and shape, with
+    contiguous elements (or unit column stride), on device `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} is required" if t is None else f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if contiguous:
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must have unit column stride")
+
+
+def _whole(name: str, t, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of this type and shape on device `dev`."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                and t.get_device() == dev):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _explain(name, t, dtype, shape, dev, True)
+
+
+def _matrix(name: str, t, dtype, shape, dev: int):
+    """(address, leading dimension) of a tensor of rows with unit column stride; a
+    single row's stride says nothing and is taken as its length."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            ld, unit = t.stride()
+            if shape[0] <= 1:
+                ld = max(ld, (shape[1] + 7) // 8 * 8)
+            if unit == 1 or shape[1] <= 1 or shape[0] == 0:
+                return t.data_ptr(), ld
+    except AttributeError:
+        pass
+    _explain(name, t, dtype, shape, dev, False)
+
+
+def _rows_of(name: str, t, dtype):
+    """(rows, columns, device) of the tensor that gives a call its sizes."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _explain(name, t, dtype, (), -1, False)
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, not on the current device")
+    return t.shape[0], t.shape[1], dev
+
+
+def _out_dtype(dtype, name: str) -> int:
+    """The ABI's number of a type, bf16 or fp32."""
     if dtype not in _OUT:
         raise ValueError(f"{name} must be bf16 or fp32, got {dtype}")
     return _OUT[dtype]
 
 
-def _here(dev, **tensors):
-    """Every given tensor is a CUDA tensor on `dev`, the current device."""
-    if dev.type != "cuda":
-        raise ValueError("expected CUDA tensors")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, not on the current device")
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+def _stream_on(dev: int) -> int:
+    """torch's current stream on a device whose tensors exist (CUDA is up)."""
+    return (_raw_stream(dev) if _raw_stream is not None
+            else torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _shape(t: Optional[torch.Tensor], dtype, shape, name: str, contiguous: bool = True):
-    """t (where given) has this type and shape, and is contiguous or, for rows,
-    has unit column stride."""
+def _workspace(t, nbytes: int, dev: int):
+    """(tensor, address, bytes) of the caller's workspace or a new one.  A new one
+    is freed when the call returns: torch hands its memory out again to later
+    work of the same stream only."""
     if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if not contiguous and t.numel() and t.stride(1) != 1:
-        raise ValueError(f"{name} must have unit column stride")
+        t = torch.empty(nbytes, dtype=_U8, device=dev)
+    elif t.dtype is not _U8 or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError("workspace must be a contiguous uint8 tensor on the call's device")
+    return t, t.data_ptr(), t.numel()
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Leading dimension of rows; a single row's stride says nothing."""
-    cols = t.shape[1]
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (cols + 7) // 8 * 8)
-
-
+@functools.lru_cache(maxsize=512)
 def sq_lora_plan_bytes(M: int, n_adapters: int) -> int:
     """Bytes of the plan of M rows and n_adapters adapters (0: out of range)."""
     return lib().sq_lora_plan_bytes(M, n_adapters)
@@ -572,36 +621,38 @@ def sq_lora_plan(adapter: torch.Tensor, n_adapters: int,
                  plan: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The plan of a batch whose row m has adapter[m] (int32 [M]; outside
     0 .. n_adapters - 1: none).  One plan serves all adapted layers of the batch."""
-    _need(adapter, torch.int32, "adapter")
-    if adapter.dim() != 1 or not adapter.is_contiguous():
-        raise ValueError("adapter must be a contiguous 1-D tensor")
-    _here(adapter.device, plan=plan)
-    M = adapter.shape[0]
+    _need(adapter, _I32, "adapter")
+    if adapter.dim() != 1:
+        raise ValueError("adapter must have one dimension")
+    M, dev = adapter.shape[0], adapter.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"adapter is on cuda:{dev}, not on the current device")
     nbytes = sq_lora_plan_bytes(M, n_adapters)
     if nbytes == 0:
         raise SegQuantError(SQ_ERR_INVALID_ARG, "sq_lora_plan")
     if plan is None:
-        plan = torch.empty(nbytes // 4, dtype=torch.int32, device=adapter.device)
-    _shape(plan, torch.int32, (nbytes // 4,), "plan")
-    _check(lib().sq_lora_plan(_ptr(adapter), M, n_adapters, _ptr(plan), _stream()),
-           "sq_lora_plan")
+        plan = torch.empty(nbytes // 4, dtype=_I32, device=dev)
+    _check(lib().sq_lora_plan(_whole("adapter", adapter, _I32, (M,), dev), M, n_adapters,
+                              _whole("plan", plan, _I32, (nbytes // 4,), dev),
+                              _stream_on(dev)), "sq_lora_plan")
     return plan
 
 
-def _lora_weights(A: torch.Tensor, Bm: torch.Tensor, scale: torch.Tensor, plan: torch.Tensor,
-                  M: int):
-    _need(A, torch.bfloat16, "A")
-    _need(Bm, torch.bfloat16, "B")
-    if A.dim() != 3 or Bm.dim() != 3:
-        raise ValueError("A must be [L, R, K] and B [L, N, R]")
-    L, R, K = A.shape
-    N = Bm.shape[1]
-    _shape(A, torch.bfloat16, (L, R, K), "A")
-    _shape(Bm, torch.bfloat16, (L, N, R), "B")
-    _shape(scale, torch.float32, (L,), "scale")
-    _here(A.device, B=Bm, scale=scale, plan=plan)
-    _shape(plan, torch.int32, (sq_lora_plan_bytes(M, L) // 4,), "plan")
-    return L, R, K, N
+@functools.lru_cache(maxsize=512)
+def sq_lora_workspace_bytes(M: int, R: int, n_adapters: int, dtype=torch.bfloat16) -> int:
+    """Workspace bytes of sq_lora_forward (dtype of y) and sq_lora_backward (0:
+    sizes out of range)."""
+    return lib().sq_lora_workspace_bytes(M, R, n_adapters, _out_dtype(dtype, "dtype"))
+
+
+def _lora_sizes(A, B):
+    """(L, R, K, N) of A [L, R, K] and B [L, N, R]."""
+    try:
+        L, R, K = A.shape
+        _, N, _ = B.shape
+        return L, R, K, N
+    except (AttributeError, ValueError):
+        raise ValueError("A must be [L, R, K] and B [L, N, R]") from None
 
 
 def sq_lora_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
@@ -612,36 +663,28 @@ def sq_lora_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: to
     bf16 or fp32 [M, N] (None: zeros, bf16 unless y says otherwise); y may be base
     (in place); t fp32 [M, R] is kept for the backward pass (rows without an
     adapter are not written)."""
-    _need(x, torch.bfloat16, "x")
-    M, K, _ = _rows(x)
-    L, R, Ka, N = _lora_weights(A, B, scale, plan, M)
+    M, K, dev = _rows_of("x", x, _BF16)
+    L, R, Ka, N = _lora_sizes(A, B)
     if Ka != K:
         raise ValueError(f"A has K = {Ka}, x has {K}")
     if y is None:
-        y = torch.empty(M, N, dtype=torch.bfloat16 if base is None else base.dtype,
-                        device=x.device)
+        y = torch.empty(M, N, dtype=_BF16 if base is None else base.dtype, device=dev)
     if t is None:
-        t = torch.empty(M, R, dtype=torch.float32, device=x.device)
-    out = _out_dtype(y, "y")
-    _shape(y, y.dtype, (M, N), "y", contiguous=False)
-    _shape(base, y.dtype, (M, N), "base", contiguous=False)
-    _shape(t, torch.float32, (M, R), "t")
-    if workspace is None:
-        workspace = torch.empty(sq_lora_workspace_bytes(M, R, L, y.dtype), dtype=torch.uint8,
-                                device=x.device)
-    _need(workspace, torch.uint8, "workspace")
-    _here(x.device, A=A, base=base, y=y, t=t, workspace=workspace)
-    _check(lib().sq_lora_forward(_ptr(x), _ld(x), _ptr(A), _ptr(B), _ptr(scale), _ptr(plan),
-                                 _ptr(base), 0 if base is None else _ld(base), _ptr(y), _ld(y),
-                                 out, _ptr(t), _ptr(workspace), workspace.numel(), M, N, K, R, L,
-                                 _stream()), "sq_lora_forward")
+        t = torch.empty(M, R, dtype=_F32, device=dev)
+    kind = y.dtype
+    out = _out_dtype(kind, "y")
+    ws, wp, wn = _workspace(workspace, sq_lora_workspace_bytes(M, R, L, kind)
+                            if workspace is None else 0, dev)
+    px, ldx = _matrix("x", x, _BF16, (M, K), dev)
+    pb, ldb = (None, 0) if base is None else _matrix("base", base, kind, (M, N), dev)
+    py, ldy = _matrix("y", y, kind, (M, N), dev)
+    _check(lib().sq_lora_forward(
+        px, ldx, _whole("A", A, _BF16, (L, R, K), dev), _whole("B", B, _BF16, (L, N, R), dev),
+        _whole("scale", scale, _F32, (L,), dev),
+        _whole("plan", plan, _I32, (sq_lora_plan_bytes(M, L) // 4,), dev), pb, ldb, py, ldy, out,
+        _whole("t", t, _F32, (M, R), dev), wp, wn, M, N, K, R, L, _stream_on(dev)),
+        "sq_lora_forward")
     return y, t
-
-
-def sq_lora_workspace_bytes(M: int, R: int, n_adapters: int, dtype=torch.bfloat16) -> int:
-    """Workspace bytes of sq_lora_forward (dtype of y) and sq_lora_backward (0:
-    sizes out of range)."""
-    return lib().sq_lora_workspace_bytes(M, R, n_adapters, _out_dtype(dtype, "dtype"))
 
 
 def sq_lora_backward(dy: torch.Tensor, x: torch.Tensor, t: torch.Tensor, A: torch.Tensor,
@@ -653,43 +696,39 @@ def sq_lora_backward(dy: torch.Tensor, x: torch.Tensor, t: torch.Tensor, A: torc
     """Gradients of sq_lora_forward -> (dA, dB, dx): dA [L, R, K] and dB [L, N, R]
     of grad_dtype (bf16 or fp32; None without need_weights), dx = dx_base + the
     adapters' part (dx_base None: zeros; dx may be dx_base; None without need_dx)."""
-    _need(dy, torch.bfloat16, "dy")
-    _need(x, torch.bfloat16, "x")
-    M, N, _ = _rows(dy)
-    L, R, K, Nb = _lora_weights(A, B, scale, plan, M)
+    M, N, dev = _rows_of("dy", dy, _BF16)
+    L, R, K, Nb = _lora_sizes(A, B)
     if Nb != N:
         raise ValueError(f"B has N = {Nb}, dy has {N}")
-    dev = dy.device
-    if need_dx and dx is None:
-        dx = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
-    if not need_dx:
-        if dx is not None or dx_base is not None:
-            raise ValueError("dx and dx_base are of no use without need_dx")
+    out = _out_dtype(grad_dtype, "grad_dtype")
+    pb, ldb, pd, ldd, pA, pB = None, 0, None, 0, None, None
+    if need_dx:
+        if dx is None:
+            dx = torch.empty(M, K, dtype=_BF16, device=dev)
+        pd, ldd = _matrix("dx", dx, _BF16, (M, K), dev)
+        if dx_base is not None:
+            pb, ldb = _matrix("dx_base", dx_base, _BF16, (M, K), dev)
+    elif dx is not None or dx_base is not None:
+        raise ValueError("dx and dx_base are of no use without need_dx")
     if need_weights:
         if dA is None:
             dA = torch.empty(L, R, K, dtype=grad_dtype, device=dev)
         if dB is None:
             dB = torch.empty(L, N, R, dtype=grad_dtype, device=dev)
+        pA = _whole("dA", dA, grad_dtype, (L, R, K), dev)
+        pB = _whole("dB", dB, grad_dtype, (L, N, R), dev)
     elif dA is not None or dB is not None:
         raise ValueError("dA and dB are of no use without need_weights")
-    out = _out_dtype(grad_dtype, "grad_dtype")
-    if workspace is None:
-        workspace = torch.empty(sq_lora_workspace_bytes(M, R, L, grad_dtype), dtype=torch.uint8,
-                                device=dev)
-    _need(workspace, torch.uint8, "workspace")
-    _shape(x, torch.bfloat16, (M, K), "x", contiguous=False)
-    _shape(t, torch.float32, (M, R), "t")
-    _shape(dx_base, torch.bfloat16, (M, K), "dx_base", contiguous=False)
-    _shape(dx, torch.bfloat16, (M, K), "dx", contiguous=False)
-    _shape(dA, grad_dtype, (L, R, K), "dA")
-    _shape(dB, grad_dtype, (L, N, R), "dB")
-    _here(dev, x=x, t=t, A=A, dx_base=dx_base, dx=dx, dA=dA, dB=dB,
-          workspace=workspace)
+    ws, wp, wn = _workspace(workspace, sq_lora_workspace_bytes(M, R, L, grad_dtype)
+                            if workspace is None else 0, dev)
+    pdy, lddy = _matrix("dy", dy, _BF16, (M, N), dev)
+    px, ldx = _matrix("x", x, _BF16, (M, K), dev)
     _check(lib().sq_lora_backward(
-        _ptr(dy), _ld(dy), _ptr(x), _ld(x), _ptr(t), _ptr(A), _ptr(B), _ptr(scale), _ptr(plan),
-        _ptr(dx_base), 0 if dx_base is None else _ld(dx_base), _ptr(dx),
-        0 if dx is None else _ld(dx), _ptr(dA), _ptr(dB), out, _ptr(workspace),
-        workspace.numel(), M, N, K, R, L, _stream()), "sq_lora_backward")
+        pdy, lddy, px, ldx, _whole("t", t, _F32, (M, R), dev),
+        _whole("A", A, _BF16, (L, R, K), dev), _whole("B", B, _BF16, (L, N, R), dev),
+        _whole("scale", scale, _F32, (L,), dev),
+        _whole("plan", plan, _I32, (sq_lora_plan_bytes(M, L) // 4,), dev), pb, ldb, pd, ldd, pA,
+        pB, out, wp, wn, M, N, K, R, L, _stream_on(dev)), "sq_lora_backward")
     return dA, dB, dx
 
 
@@ -700,36 +739,44 @@ def sq_rope_frequencies(rot: int, base: float = 10000.0, scaling: int = SQ_ROPE_
     calls; evaluated on the host in fp64."""
     if rot < 2 or rot % 2 or rot > 1024:
         raise SegQuantError(SQ_ERR_INVALID_ARG, "sq_rope_frequencies")
-    inv_freq = torch.empty(rot // 2, dtype=torch.float32)
+    inv_freq = torch.empty(rot // 2, dtype=_F32)
     factor = ctypes.c_float(1.0)
     _check(lib().sq_rope_frequencies(rot, base, scaling, scale, original_context, beta_fast,
-                                     beta_slow, _ptr(inv_freq), ctypes.byref(factor)),
+                                     beta_slow, inv_freq.data_ptr(), ctypes.byref(factor)),
            "sq_rope_frequencies")
     return inv_freq, factor.value
 
 
+@functools.lru_cache(maxsize=64)
+def _int_array(values: tuple):
+    """A C int array of these values (read only by the calls)."""
+    return (ctypes.c_int32 * len(values))(*values)
+
+
 def _rope(call: str, x, positions, inv_freq, head_dim, out, layout, axis_pairs, factor):
-    dtype = _out_dtype(x, "x")
-    M, cols, _ = _rows(x)
-    _need(positions, torch.int32, "positions")
-    _need(inv_freq, torch.float32, "inv_freq")
-    if cols % head_dim != 0:
+    if not isinstance(x, torch.Tensor):
+        raise ValueError("x must be a tensor")
+    kind = x.dtype
+    dtype = _out_dtype(kind, "x")
+    M, cols, dev = _rows_of("x", x, kind)
+    if head_dim < 1 or cols % head_dim != 0:
         raise ValueError(f"{cols} columns are no whole number of heads of {head_dim}")
     axes = 1 if axis_pairs is None else len(axis_pairs)
-    if positions.dim() == 1 and axes == 1:
+    if axes == 1 and positions.dim() == 1:
         positions = positions[:, None]
-    _shape(positions, torch.int32, (M, axes), "positions")
-    _shape(inv_freq, torch.float32, (inv_freq.numel(),), "inv_freq")
+    pairs = inv_freq.numel()
     if out is None:
-        out = torch.empty(M, cols, dtype=x.dtype, device=x.device)
-    _shape(out, x.dtype, (M, cols), "out", contiguous=False)
-    _here(x.device, positions=positions, inv_freq=inv_freq, out=out)
-    arr = None if axis_pairs is None else (ctypes.c_int32 * axes)(*[int(v) for v in axis_pairs])
-    ldx = _ld(x)
-    ldo = ldx if out.data_ptr() == x.data_ptr() and M <= 1 else _ld(out)
-    _check(getattr(lib(), call)(_ptr(x), ldx, _ptr(out), ldo, dtype, _ptr(positions),
-                                _ptr(inv_freq), arr, axes, float(factor), M, cols // head_dim,
-                                head_dim, 2 * inv_freq.numel(), layout, _stream()), call)
+        out = torch.empty(M, cols, dtype=kind, device=dev)
+    px, ldx = _matrix("x", x, kind, (M, cols), dev)
+    po, ldo = _matrix("out", out, kind, (M, cols), dev)
+    if px == po and M == 1:
+        ldo = ldx
+    _check(getattr(lib(), call)(px, ldx, po, ldo, dtype,
+                                _whole("positions", positions, _I32, (M, axes), dev),
+                                _whole("inv_freq", inv_freq, _F32, (pairs,), dev),
+                                None if axis_pairs is None else _int_array(tuple(axis_pairs)),
+                                axes, factor, M, cols // head_dim, head_dim, 2 * pairs, layout,
+                                _stream_on(dev)), call)
     return out
 
 
@@ -755,37 +802,37 @@ def sq_rope_backward(dout: torch.Tensor, positions: torch.Tensor, inv_freq: torc
                  factor)
 
 
+@functools.lru_cache(maxsize=512)
 def sq_group_norm_workspace_bytes(B: int, S: int, C: int, G: int) -> int:
     """Workspace bytes of the group norm calls (0: sizes out of range, or B = 0)."""
     return lib().sq_group_norm_workspace_bytes(B, S, C, G)
 
 
-def _samples(t: Optional[torch.Tensor], shape, name: str):
-    """A [B, S, C] bf16 tensor whose samples and rows lie at one row stride -> ld."""
-    if t is None:
-        return 0
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be bf16 {list(shape)}, got {t.dtype} {list(t.shape)}")
+def _samples(name: str, t, shape, dev: int):
+    """(address, row stride) of a [B, S, C] bf16 tensor whose samples and rows lie
+    at one row stride."""
     B, S, C = shape
-    if t.numel() == 0:
-        return (C + 7) // 8 * 8
-    if S > 1:
-        ld = t.stride(1)
-    elif B > 1:
-        ld = t.stride(0)
-    else:
-        ld = (C + 7) // 8 * 8
-    if (C > 1 and t.stride(2) != 1) or (B > 1 and t.stride(0) != S * ld):
+    if (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.shape == shape
+            and t.get_device() == dev):
+        sb, sr, sc = t.stride()
+        if B * S <= 1:
+            return t.data_ptr(), (C + 7) // 8 * 8
+        ld = sr if S > 1 else sb
+        if (sc == 1 or C == 1) and (B == 1 or S == 1 or sb == S * ld):
+            return t.data_ptr(), ld
         raise ValueError(f"{name} must have unit channel stride and one row stride")
-    return ld
+    _explain(name, t, _BF16, shape, dev, False)
 
 
-def _gn_workspace(workspace, B, S, C, G, device):
-    if workspace is None:
-        return torch.empty(sq_group_norm_workspace_bytes(B, S, C, G), dtype=torch.uint8,
-                           device=device)
-    _need(workspace, torch.uint8, "workspace")
-    return workspace
+def _gn_sizes(x):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        _explain("x", x, _BF16, (), -1, False)
+    if x.dim() != 3:
+        raise ValueError("x must be [B, S, C]")
+    dev = x.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"x is on cuda:{dev}, not on the current device")
+    return (*x.shape, dev)
 
 
 def sq_group_norm_forward(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor],
@@ -795,23 +842,19 @@ def sq_group_norm_forward(x: torch.Tensor, groups: int, gamma: Optional[torch.Te
     """y = act(group norm of x) over channels-last samples x bf16 [B, S, C] ->
     (y, mean, rstd); mean and rstd fp32 [B, groups] are kept for the backward
     pass.  gamma, beta bf16 [C] or None; y may be x (in place)."""
-    _need(x, torch.bfloat16, "x")
-    if x.dim() != 3:
-        raise ValueError("x must be [B, S, C]")
-    B, S, C = x.shape
+    B, S, C, dev = _gn_sizes(x)
     if y is None:
-        y = torch.empty(B, S, C, dtype=torch.bfloat16, device=x.device)
-    ldx, ldy = _samples(x, (B, S, C), "x"), _samples(y, (B, S, C), "y")
-    _shape(gamma, torch.bfloat16, (C,), "gamma")
-    _shape(beta, torch.bfloat16, (C,), "beta")
-    stats = torch.empty(2, B, groups, dtype=torch.float32, device=x.device)
-    workspace = _gn_workspace(workspace, B, S, C, groups, x.device)
-    _here(x.device, gamma=gamma, beta=beta, y=y, workspace=workspace)
-    _check(lib().sq_group_norm_forward(_ptr(x), ldx, B, S, C, groups, _ptr(gamma), _ptr(beta),
-                                       float(eps), act, _ptr(y), ldy, _ptr(stats[0]),
-                                       _ptr(stats[1]), _ptr(workspace), workspace.numel(),
-                                       _stream()), "sq_group_norm_forward")
-    return y, stats[0], stats[1]
+        y = torch.empty(B, S, C, dtype=_BF16, device=dev)
+    mean, rstd = torch.empty(2, B, max(groups, 0), dtype=_F32, device=dev).unbind(0)
+    ws, wp, wn = _workspace(workspace, sq_group_norm_workspace_bytes(B, S, C, groups)
+                            if workspace is None else 0, dev)
+    px, ldx = _samples("x", x, (B, S, C), dev)
+    py, ldy = _samples("y", y, (B, S, C), dev)
+    _check(lib().sq_group_norm_forward(
+        px, ldx, B, S, C, groups, None if gamma is None else _whole("gamma", gamma, _BF16, (C,), dev),
+        None if beta is None else _whole("beta", beta, _BF16, (C,), dev), eps, act, py, ldy,
+        mean.data_ptr(), rstd.data_ptr(), wp, wn, _stream_on(dev)), "sq_group_norm_forward")
+    return y, mean, rstd
 
 
 def sq_group_norm_backward(dy: torch.Tensor, x: torch.Tensor, groups: int,
@@ -821,35 +864,32 @@ def sq_group_norm_backward(dy: torch.Tensor, x: torch.Tensor, groups: int,
                            workspace: Optional[torch.Tensor] = None, need_dx: bool = True):
     """Gradients of sq_group_norm_forward -> (dx, dgamma, dbeta); dgamma and dbeta
     [C] of grad_dtype (None where gamma or beta is None); dx may be dy."""
-    _need(dy, torch.bfloat16, "dy")
-    _need(x, torch.bfloat16, "x")
-    if x.dim() != 3:
-        raise ValueError("x must be [B, S, C]")
-    B, S, C = x.shape
+    B, S, C, dev = _gn_sizes(x)
+    shape = (B, S, C)
+    out = _out_dtype(grad_dtype, "grad_dtype")
     if need_dx and dx is None:
-        dx = torch.empty(B, S, C, dtype=torch.bfloat16, device=x.device)
+        dx = torch.empty(shape, dtype=_BF16, device=dev)
     if not need_dx and dx is not None:
         raise ValueError("dx is of no use without need_dx")
-    lddy, ldx = _samples(dy, (B, S, C), "dy"), _samples(x, (B, S, C), "x")
-    lddx = _samples(dx, (B, S, C), "dx")
-    _shape(gamma, torch.bfloat16, (C,), "gamma")
-    _shape(beta, torch.bfloat16, (C,), "beta")
-    _shape(mean, torch.float32, (B, groups), "mean")
-    _shape(rstd, torch.float32, (B, groups), "rstd")
-    out = _out_dtype(grad_dtype, "grad_dtype")
-    dgamma = None if gamma is None else torch.empty(C, dtype=grad_dtype, device=x.device)
-    dbeta = None if beta is None else torch.empty(C, dtype=grad_dtype, device=x.device)
-    workspace = _gn_workspace(workspace, B, S, C, groups, x.device)
-    _here(x.device, dy=dy, gamma=gamma, beta=beta, mean=mean, rstd=rstd, dx=dx,
-          workspace=workspace)
-    _check(lib().sq_group_norm_backward(_ptr(dy), lddy, _ptr(x), ldx, B, S, C, groups,
-                                        _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd), act,
-                                        _ptr(dx), lddx, _ptr(dgamma), _ptr(dbeta), out,
-                                        _ptr(workspace), workspace.numel(), _stream()),
-           "sq_group_norm_backward")
+    dgamma = None if gamma is None else torch.empty(C, dtype=grad_dtype, device=dev)
+    dbeta = None if beta is None else torch.empty(C, dtype=grad_dtype, device=dev)
+    ws, wp, wn = _workspace(workspace, sq_group_norm_workspace_bytes(B, S, C, groups)
+                            if workspace is None else 0, dev)
+    pdy, lddy = _samples("dy", dy, shape, dev)
+    px, ldx = _samples("x", x, shape, dev)
+    pdx, lddx = (None, 0) if dx is None else _samples("dx", dx, shape, dev)
+    _check(lib().sq_group_norm_backward(
+        pdy, lddy, px, ldx, B, S, C, groups,
+        None if gamma is None else _whole("gamma", gamma, _BF16, (C,), dev),
+        None if beta is None else _whole("beta", beta, _BF16, (C,), dev),
+        _whole("mean", mean, _F32, (B, groups), dev),
+        _whole("rstd", rstd, _F32, (B, groups), dev), act, pdx, lddx,
+        None if dgamma is None else dgamma.data_ptr(), None if dbeta is None else dbeta.data_ptr(),
+        out, wp, wn, _stream_on(dev)), "sq_group_norm_backward")
     return dx, dgamma, dbeta
 
 
+@functools.lru_cache(maxsize=512)
 def sq_input_grad_workspace_bytes(N: int, K: int) -> int:
     """Workspace bytes of sq_dualscale_seglinear_input_grad (0: out of range)."""
     return lib().sq_input_grad_workspace_bytes(N, K)
@@ -863,28 +903,22 @@ def sq_dualscale_seglinear_input_grad(dy: torch.Tensor, wq: torch.Tensor, s_w: t
     to its input (dy bf16 [M, N] -> dx bf16 [M, K]), straight through the
     activation quantizer.  workspace: uint8, sq_input_grad_workspace_bytes(N, K);
     layers on one stream may share one."""
-    _need(dy, torch.bfloat16, "dy")
-    _need(wq, torch.int8, "wq")
-    if wq.dim() != 2:
+    M, N, dev = _rows_of("dy", dy, _BF16)
+    if not isinstance(wq, torch.Tensor) or wq.dim() != 2:
         raise ValueError("wq must be [N, K]")
-    M, N, _ = _rows(dy)
     K = wq.shape[1]
-    _shape(wq, torch.int8, (N, K), "wq")
-    _shape(s_w, torch.float32, (seg.S, N), "s_w")
-    _shape(d, torch.float32, (seg.n_groups, K), "d")
     if dx is None:
-        dx = torch.empty(M, K, dtype=torch.bfloat16, device=dy.device)
-    _shape(dx, torch.bfloat16, (M, K), "dx", contiguous=False)
-    if workspace is None:
-        workspace = torch.empty(sq_input_grad_workspace_bytes(N, K), dtype=torch.uint8,
-                                device=dy.device)
-    _need(workspace, torch.uint8, "workspace")
-    _here(dy.device, wq=wq, s_w=s_w, d=d, dx=dx, workspace=workspace)
+        dx = torch.empty(M, K, dtype=_BF16, device=dev)
+    ws, wp, wn = _workspace(workspace, sq_input_grad_workspace_bytes(N, K)
+                            if workspace is None else 0, dev)
+    pdy, lddy = _matrix("dy", dy, _BF16, (M, N), dev)
+    pdx, lddx = _matrix("dx", dx, _BF16, (M, K), dev)
     cs, keep = seg._c()
     _check(lib().sq_dualscale_seglinear_input_grad(
-        _ptr(dy), _ld(dy), _ptr(wq), _ptr(s_w), _ptr(d), ctypes.byref(cs), _ptr(dx), _ld(dx), M,
-        N, K, _ptr(workspace), workspace.numel(), _stream()),
-        "sq_dualscale_seglinear_input_grad")
+        pdy, lddy, _whole("wq", wq, torch.int8, (N, K), dev),
+        _whole("s_w", s_w, _F32, (seg.S, N), dev),
+        None if d is None else _whole("d", d, _F32, (seg.n_groups, K), dev), ctypes.byref(cs),
+        pdx, lddx, M, N, K, wp, wn, _stream_on(dev)), "sq_dualscale_seglinear_input_grad")
     return dx
 
 
