@@ -53,11 +53,6 @@ __host__ __device__ inline Split split_of(int C) {
   return o >= kThreads ? Split{kThreads, 1} : Split{o, kThreads / o};
 }
 
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  return v;
-}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
@@ -91,91 +86,83 @@ __device__ __forceinline__ float act_grad(float v) {
 // ------------------------------------------------------------------- forward
 // Chunk statistics: part[b][chunk][g] = {mean, sum of squares about it}.
 __global__ void __launch_bounds__(kThreads) gn_stats_kernel(const GroupNormArgs p) {
-  extern __shared__ float2 sh[];
-  float2 *lane_buf = sh;                   // [lanes][oct * 8] {mean, M2}
-  float2 *chan = sh + kThreads * 8;        // [C]
+  extern __shared__ float2 sh[];  // a pass: [lanes][oct * 8] {mean, M2} of each thread's rows
+  grid_dependency_wait();
+  grid_dependency_launch();
   const int b = blockIdx.y;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_chunk;
   const int rows = p.S - r0 < p.rows_per_chunk ? static_cast<int>(p.S - r0) : p.rows_per_chunk;
   const Split sp = split_of(p.C);
   const int lane = threadIdx.x / sp.oct, oct = threadIdx.x % sp.oct;
   const uint16_t *x = p.x + (static_cast<int64_t>(b) * p.S + r0) * p.ldx;
-
-  for (int o0 = 0; o0 < p.C / 8; o0 += sp.oct) {
-    const int here = p.C / 8 - o0 < sp.oct ? p.C / 8 - o0 : sp.oct;
-    if (lane < sp.lanes && oct < here) {
-      float mean[8], m2[8];
+  const int octs = p.C / 8, width = octs * 8;  // of a lane's row in shared memory
+  for (int o = oct; o < octs; o += sp.oct) {
+    if (lane >= sp.lanes) break;
+    float mean[8], m2[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) mean[j] = m2[j] = 0.0f;
-      float n = 0.0f;
-      const uint16_t *src = x + (o0 + oct) * 8;
-      for (int r = lane; r < rows; r += sp.lanes * kBatch) {
-        uint4 v[kBatch];
-        int k = 0;
+    for (int j = 0; j < 8; ++j) mean[j] = m2[j] = 0.0f;
+    float n = 0.0f;
+    const uint16_t *src = x + o * 8;
+    for (int r = lane; r < rows; r += sp.lanes * kBatch) {
+      uint4 v[kBatch];
+      int k = 0;
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const int rr = r + q * sp.lanes;
+        const bool in = rr < rows;
+        v[q] = in ? load8(src + rr * p.ldx) : make_uint4(0, 0, 0, 0);
+        k += in;
+      }
+      const float fk = static_cast<float>(k), inv = 1.0f / fk;
+      const float total = n + fk, w = fk / total;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float s = 0.0f;
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
-          const int rr = r + q * sp.lanes;
-          const bool in = rr < rows;
-          v[q] = in ? load8(src + rr * p.ldx) : make_uint4(0, 0, 0, 0);
-          k += in;
+          const uint32_t word = j < 2 ? v[q].x : j < 4 ? v[q].y : j < 6 ? v[q].z : v[q].w;
+          s += (j & 1) ? bf16_hi(word) : bf16_lo(word);
         }
-        const float fk = static_cast<float>(k), inv = 1.0f / fk;
-        const float total = n + fk, w = fk / total;
+        const float bm = s * inv;
+        float bs = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float s = 0.0f;
-#pragma unroll
-          for (int q = 0; q < kBatch; ++q) {
-            const uint32_t word = j < 2 ? v[q].x : j < 4 ? v[q].y : j < 6 ? v[q].z : v[q].w;
-            s += (j & 1) ? bf16_hi(word) : bf16_lo(word);
-          }
-          const float bm = s * inv;
-          float bs = 0.0f;
-#pragma unroll
-          for (int q = 0; q < kBatch; ++q) {
-            const uint32_t word = j < 2 ? v[q].x : j < 4 ? v[q].y : j < 6 ? v[q].z : v[q].w;
-            const float d = ((j & 1) ? bf16_hi(word) : bf16_lo(word)) - bm;
-            bs = q < k ? fmaf(d, d, bs) : bs;
-          }
-          const float delta = bm - mean[j];
-          mean[j] = fmaf(delta, w, mean[j]);
-          m2[j] += bs + delta * delta * n * w;
+        for (int q = 0; q < kBatch; ++q) {
+          const uint32_t word = j < 2 ? v[q].x : j < 4 ? v[q].y : j < 6 ? v[q].z : v[q].w;
+          const float d = ((j & 1) ? bf16_hi(word) : bf16_lo(word)) - bm;
+          bs = q < k ? fmaf(d, d, bs) : bs;
         }
-        n = total;
+        const float delta = bm - mean[j];
+        mean[j] = fmaf(delta, w, mean[j]);
+        m2[j] += bs + delta * delta * n * w;
       }
+      n = total;
+    }
+    float4 *to = reinterpret_cast<float4 *>(sh + lane * width + o * 8);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        lane_buf[(lane * sp.oct + oct) * 8 + j] = make_float2(mean[j], m2[j]);
-    }
-    __syncthreads();
-    // join the lanes of each channel
-    for (int c = threadIdx.x; c < here * 8; c += kThreads) {
-      float mean = 0.0f, m2 = 0.0f, n = 0.0f;
-      for (int l = 0; l < sp.lanes && l < rows; ++l) {
-        const float k = static_cast<float>((rows - l + sp.lanes - 1) / sp.lanes);
-        const float2 v = lane_buf[l * sp.oct * 8 + c];
-        const float total = n + k, w = k / total, delta = v.x - mean;
-        mean = fmaf(delta, w, mean);
-        m2 += v.y + delta * delta * n * w;
-        n = total;
-      }
-      chan[o0 * 8 + c] = make_float2(mean, m2);
-    }
-    __syncthreads();
+    for (int j = 0; j < 8; j += 2)
+      to[j / 2] = make_float4(mean[j], m2[j], mean[j + 1], m2[j + 1]);
   }
-  // join the channels of each group (equal counts)
+  __syncthreads();
+  // join lanes and channels of each group: first the mean, then the squares about it
   const int cg = p.C / p.G;
   const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
+  const int lanes = rows < sp.lanes ? rows : sp.lanes;  // with rows
   const int64_t slot = (static_cast<int64_t>(b) * p.chunks + blockIdx.x) * p.G;
   for (int g = warp; g < p.G; g += kWarps) {
     float s = 0.0f;
-    for (int c = ln; c < cg; c += 32) s += chan[g * cg + c].x;
-    const float mean = warp_sum(s) / static_cast<float>(cg);
+    for (int l = 0; l < lanes; ++l) {
+      const float n = static_cast<float>((rows - l + sp.lanes - 1) / sp.lanes);
+      for (int c = ln; c < cg; c += 32) s = fmaf(n, sh[l * width + g * cg + c].x, s);
+    }
+    const float mean = warp_sum(s) / (static_cast<float>(cg) * static_cast<float>(rows));
     float m2 = 0.0f;
-    for (int c = ln; c < cg; c += 32) {
-      const float2 v = chan[g * cg + c];
-      const float d = v.x - mean;
-      m2 += v.y + d * d * static_cast<float>(rows);
+    for (int l = 0; l < lanes; ++l) {
+      const float n = static_cast<float>((rows - l + sp.lanes - 1) / sp.lanes);
+      for (int c = ln; c < cg; c += 32) {
+        const float2 v = sh[l * width + g * cg + c];
+        const float d = v.x - mean;
+        m2 += fmaf(n * d, d, v.y);
+      }
     }
     m2 = warp_sum(m2);
     if (ln == 0 && store_ok(p.status, slot + g < static_cast<int64_t>(p.B) * p.chunks * p.G))
@@ -183,40 +170,71 @@ __global__ void __launch_bounds__(kThreads) gn_stats_kernel(const GroupNormArgs 
   }
 }
 
-// Joins a sample's chunk statistics into {mean, rstd} of each group.
-__device__ __forceinline__ void join_stats(const GroupNormArgs &p, int b, float2 *stat) {
-  const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
-  const int cg = p.C / p.G;
-  for (int g = warp; g < p.G; g += kWarps) {
-    const float2 *src = p.part + static_cast<int64_t>(b) * p.chunks * p.G + g;
-    double s = 0.0;
-    for (int k = ln; k < p.chunks; k += 32) {
-      const int64_t left = p.S - static_cast<int64_t>(k) * p.rows_per_chunk;
-      const double n = left < p.rows_per_chunk ? left : p.rows_per_chunk;
-      s += n * src[static_cast<int64_t>(k) * p.G].x;
-    }
-    const double mean = warp_sum(s) / static_cast<double>(p.S);
-    double m2 = 0.0;
-    for (int k = ln; k < p.chunks; k += 32) {
-      const int64_t left = p.S - static_cast<int64_t>(k) * p.rows_per_chunk;
-      const double n = left < p.rows_per_chunk ? left : p.rows_per_chunk;
+// Sums over a sample's chunks of {f(v, n), g(v, n)} of each group's partials, n
+// rows in the chunk, in fp64: all threads load (thread t: group t % G of every
+// (t / G)-th chunk), and a group's partial sums are added in a fixed order.
+// `sums` [kThreads] in shared memory; ends with sums[g] ready for all.
+template <typename F>
+__device__ __forceinline__ void chunk_sums(const GroupNormArgs &p, int b, double2 *sums, int g0,
+                                           int width, F &&f) {
+  const int lanes = kThreads / width;
+  const int g = threadIdx.x % width, l = threadIdx.x / width;
+  double2 s = make_double2(0.0, 0.0);
+  if (l < lanes) {
+    const float2 *src = p.part + static_cast<int64_t>(b) * p.chunks * p.G + g0 + g;
+#pragma unroll 8
+    for (int k = l; k < p.chunks; k += lanes) {
       const float2 v = src[static_cast<int64_t>(k) * p.G];
-      const double d = v.x - mean;
-      m2 += v.y + n * cg * d * d;
+      const double2 a = f(v, k + 1 < p.chunks ? p.rows_per_chunk
+                                              : p.S - static_cast<int64_t>(k) * p.rows_per_chunk);
+      s.x += a.x;
+      s.y += a.y;
     }
-    const double var = warp_sum(m2) / (static_cast<double>(p.S) * cg);
-    if (ln == 0)
-      stat[g] = make_float2(static_cast<float>(mean),
-                            static_cast<float>(1.0 / sqrt(var + static_cast<double>(p.eps))));
   }
+  __syncthreads();  // the last user of `sums` is done
+  if (l < lanes) sums[l * width + g] = s;
+  __syncthreads();
+  if (threadIdx.x < width) {
+    for (int q = 1; q < lanes; ++q) {
+      s.x += sums[q * width + g].x;
+      s.y += sums[q * width + g].y;
+    }
+    sums[g] = s;
+  }
+  __syncthreads();
+}
+
+// Joins a sample's chunk statistics into {mean, rstd} of each group.  The sum of
+// squares about zero loses nothing that matters in fp64: bf16 values have means
+// of at most 2^9 deviations or so.
+__device__ __forceinline__ void join_stats(const GroupNormArgs &p, int b, float2 *stat,
+                                           double2 *sums) {
+  const double cg = p.C / p.G, n = static_cast<double>(p.S);
+  for (int g0 = 0; g0 < p.G; g0 += kThreads) {
+    const int width = p.G - g0 < kThreads ? p.G - g0 : kThreads;
+    chunk_sums(p, b, sums, g0, width, [&](float2 v, double rows) {
+      const double m = v.x;
+      return make_double2(rows * m, v.y + rows * cg * m * m);
+    });
+    if (threadIdx.x < width) {
+      const double mean = sums[threadIdx.x].x / n;
+      double var = sums[threadIdx.x].y / (n * cg) - mean * mean;
+      if (var < 0.0) var = 0.0;
+      stat[g0 + threadIdx.x] =
+          make_float2(static_cast<float>(mean),
+                      static_cast<float>(1.0 / sqrt(var + static_cast<double>(p.eps))));
+    }
+  }
+  __syncthreads();
 }
 
 template <int ACT>
 __global__ void __launch_bounds__(kThreads) gn_apply_kernel(const GroupNormArgs p) {
   extern __shared__ float2 sh[];  // [G] {mean, rstd}
+  __shared__ double2 sums[kThreads];
+  grid_dependency_wait();
   const int b = blockIdx.y;
-  join_stats(p, b, sh);
-  __syncthreads();
+  join_stats(p, b, sh, sums);
   if (blockIdx.x == 0)
     for (int g = threadIdx.x; g < p.G; g += kThreads)
       if (store_ok(p.status, b < p.B)) {
@@ -275,9 +293,9 @@ __device__ __forceinline__ Chan chan_of(const GroupNormArgs &p, int b, int c, in
 // part[b][chunk][g] = {sum h, sum h xh}.
 template <int ACT>
 __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const GroupNormArgs p) {
-  extern __shared__ float2 sh[];
-  float2 *lane_buf = sh;             // [lanes][oct * 8]
-  float2 *chan = sh + kThreads * 8;  // [C]
+  extern __shared__ float2 sh[];  // [lanes][C], then the channels' sums in its first row
+  grid_dependency_wait();
+  grid_dependency_launch();
   const int b = blockIdx.y;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_chunk;
   const int rows = p.S - r0 < p.rows_per_chunk ? static_cast<int>(p.S - r0) : p.rows_per_chunk;
@@ -287,66 +305,64 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const GroupNormAr
   const int64_t row0 = static_cast<int64_t>(b) * p.S + r0;
   const int64_t slot = static_cast<int64_t>(b) * p.chunks + blockIdx.x;
 
-  for (int o0 = 0; o0 < p.C / 8; o0 += sp.oct) {
-    const int here = p.C / 8 - o0 < sp.oct ? p.C / 8 - o0 : sp.oct;
-    if (lane < sp.lanes && oct < here) {
-      const int c0 = (o0 + oct) * 8;
-      Chan ch[8];
-      float sd[8], sx[8];
+  for (int o = oct; o < p.C / 8; o += sp.oct) {
+    if (lane >= sp.lanes) break;
+    const int c0 = o * 8;
+    Chan ch[8];
+    float sd[8], sx[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        ch[j] = chan_of(p, b, c0 + j, cg);
-        sd[j] = sx[j] = 0.0f;
+    for (int j = 0; j < 8; ++j) {
+      ch[j] = chan_of(p, b, c0 + j, cg);
+      sd[j] = sx[j] = 0.0f;
+    }
+    for (int r = lane; r < rows; r += sp.lanes * 4) {
+      uint4 vx[4], vd[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t row = row0 + r + q * sp.lanes;
+        const bool in = r + q * sp.lanes < rows;
+        vx[q] = in ? load8(p.x + row * p.ldx + c0) : make_uint4(0, 0, 0, 0);
+        vd[q] = in ? load8(p.dy + row * p.lddy + c0) : make_uint4(0, 0, 0, 0);
       }
-      for (int r = lane; r < rows; r += sp.lanes * 4) {
-        uint4 vx[4], vd[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t row = row0 + r + q * sp.lanes;
-          const bool in = r + q * sp.lanes < rows;
-          vx[q] = in ? load8(p.x + row * p.ldx + c0) : make_uint4(0, 0, 0, 0);
-          vd[q] = in ? load8(p.dy + row * p.lddy + c0) : make_uint4(0, 0, 0, 0);
-        }
+      for (int q = 0; q < 4; ++q) {
+        if (r + q * sp.lanes >= rows) break;
+        float x[8], d[8];
+        unpack8(vx[q], x);
+        unpack8(vd[q], d);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (r + q * sp.lanes >= rows) break;
-          float x[8], d[8];
-          unpack8(vx[q], x);
-          unpack8(vd[q], d);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float xh = (x[j] - ch[j].mean) * ch[j].rstd;
-            const float dv = d[j] * act_grad<ACT>(fmaf(xh, ch[j].gamma, ch[j].beta));
-            sd[j] += dv;
-            sx[j] = fmaf(dv, xh, sx[j]);
-          }
+        for (int j = 0; j < 8; ++j) {
+          const float xh = (x[j] - ch[j].mean) * ch[j].rstd;
+          const float dv = d[j] * act_grad<ACT>(fmaf(xh, ch[j].gamma, ch[j].beta));
+          sd[j] += dv;
+          sx[j] = fmaf(dv, xh, sx[j]);
         }
       }
+    }
+    float4 *to = reinterpret_cast<float4 *>(sh + lane * p.C + c0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        lane_buf[(lane * sp.oct + oct) * 8 + j] = make_float2(sd[j], sx[j]);
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < here * 8; c += kThreads) {
-      float2 s = make_float2(0.0f, 0.0f);
-      for (int l = 0; l < sp.lanes; ++l) {
-        const float2 v = lane_buf[l * sp.oct * 8 + c];
-        s.x += v.x;
-        s.y += v.y;
-      }
-      chan[o0 * 8 + c] = s;
-      if (store_ok(p.status, slot < static_cast<int64_t>(p.B) * p.chunks && o0 * 8 + c < p.C))
-        p.chan_part[slot * p.C + o0 * 8 + c] = s;
-    }
-    __syncthreads();
+    for (int j = 0; j < 8; j += 2) to[j / 2] = make_float4(sd[j], sx[j], sd[j + 1], sx[j + 1]);
   }
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.C; c += kThreads) {
+    float2 s = sh[c];
+    for (int l = 1; l < sp.lanes; ++l) {
+      const float2 v = sh[l * p.C + c];
+      s.x += v.x;
+      s.y += v.y;
+    }
+    sh[c] = s;
+    if (store_ok(p.status, slot < static_cast<int64_t>(p.B) * p.chunks))
+      p.chan_part[slot * p.C + c] = s;
+  }
+  __syncthreads();
   const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
   for (int g = warp; g < p.G; g += kWarps) {
     float s1 = 0.0f, s2 = 0.0f;
     for (int c = g * cg + ln; c < (g + 1) * cg; c += 32) {
       const float gm = p.gamma ? bf16_lo(p.gamma[c]) : 1.0f;
-      s1 = fmaf(gm, chan[c].x, s1);
-      s2 = fmaf(gm, chan[c].y, s2);
+      s1 = fmaf(gm, sh[c].x, s1);
+      s2 = fmaf(gm, sh[c].y, s2);
     }
     s1 = warp_sum(s1);
     s2 = warp_sum(s2);
@@ -360,23 +376,26 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const GroupNormAr
 template <int ACT, bool GF32>
 __global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs p) {
   extern __shared__ float2 sh[];
+  __shared__ double2 sums[kThreads];
   const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
+  grid_dependency_wait();
   if (static_cast<int>(blockIdx.x) < p.grad_blocks) {
     const int c = blockIdx.x * 32 + ln;
     double s = 0.0, sx = 0.0;
-    if (c < p.C)
+    if (c < p.C) {
+#pragma unroll 8
       for (int64_t k = warp; k < static_cast<int64_t>(p.B) * p.chunks; k += kWarps) {
         const float2 v = p.chan_part[k * p.C + c];
         s += v.x;
         sx += v.y;
       }
-    double2 *buf = reinterpret_cast<double2 *>(sh);
-    buf[warp * 32 + ln] = make_double2(s, sx);
+    }
+    sums[warp * 32 + ln] = make_double2(s, sx);
     __syncthreads();
     if (warp != 0 || c >= p.C) return;
     for (int w = 1; w < kWarps; ++w) {
-      s += buf[w * 32 + ln].x;
-      sx += buf[w * 32 + ln].y;
+      s += sums[w * 32 + ln].x;
+      sx += sums[w * 32 + ln].y;
     }
     if (!store_ok(p.status, c < p.C)) return;
     if constexpr (GF32) {
@@ -395,17 +414,13 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs
   const int cg = p.C / p.G;
   const double n = static_cast<double>(p.S) * cg;
   // group sums over n
-  for (int g = warp; g < p.G; g += kWarps) {
-    const float2 *src = p.part + static_cast<int64_t>(b) * p.chunks * p.G + g;
-    double s1 = 0.0, s2 = 0.0;
-    for (int k = ln; k < p.chunks; k += 32) {
-      const float2 v = src[static_cast<int64_t>(k) * p.G];
-      s1 += v.x;
-      s2 += v.y;
-    }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if (ln == 0) sh[g] = make_float2(static_cast<float>(s1 / n), static_cast<float>(s2 / n));
+  for (int g0 = 0; g0 < p.G; g0 += kThreads) {
+    const int width = p.G - g0 < kThreads ? p.G - g0 : kThreads;
+    chunk_sums(p, b, sums, g0, width,
+               [](float2 v, double) { return make_double2(v.x, v.y); });
+    if (threadIdx.x < width)
+      sh[g0 + threadIdx.x] = make_float2(static_cast<float>(sums[threadIdx.x].x / n),
+                                         static_cast<float>(sums[threadIdx.x].y / n));
   }
   __syncthreads();
   const int64_t r0 = static_cast<int64_t>(chunk) * p.rows_per_chunk;
@@ -456,31 +471,56 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs
 }
 
 // ------------------------------------------------------------------ host side
-// Rows of a chunk: about four blocks per SM of a 148-SM device over all
-// samples, but at least eight rows (one batch) per thread where S allows.  A
+// Rows of a chunk: two blocks per SM of a 148-SM device over all samples, but at
+// least eight rows (one batch) per thread where S allows.  Fewer, longer chunks
+// also mean fewer partials to join in every block of the second kernel.  A
 // fixed rule, so that the workspace size and the order of every sum depend on
 // the sizes only.
 int64_t chunk_rows(int64_t B, int64_t S, int64_t C) {
-  const int64_t want = (4 * 148 + B - 1) / B;
+  const int64_t want = (2 * 148 + B - 1) / B;
   const int64_t least = static_cast<int64_t>(split_of(static_cast<int>(C)).lanes) * kBatch;
   int64_t rows = (S + want - 1) / want;
   if (rows < least) rows = least;
   return rows;
 }
 
-int stats_smem(int C) { return (kThreads * 8 + C) * static_cast<int>(sizeof(float2)); }
+// Shared memory of the first kernels: every thread's eight channels (or all
+// channels, where they are more).
+int lane_smem(int C) {
+  return (split_of(C).lanes * C) * static_cast<int>(sizeof(float2));
+}
 
+// Launch behind the kernel ahead in the stream (programmatic dependent launch:
+// every kernel here waits for it before it reads anything).
 template <auto Kernel>
-cudaError_t allow(int smem) {
-  static bool done[64] = {};
+cudaError_t launch(dim3 grid, size_t smem, size_t max_smem, const GroupNormArgs &p,
+                   cudaStream_t stream) {
+  static bool done[64] = {};  // per kernel and device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) done[dev] = true;
-  return e;
+  if (!done[dev]) {
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(max_smem));
+    if (e != cudaSuccess) return e;
+    done[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, Kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
+
+constexpr size_t kMaxLaneSmem = kGroupNormMaxC * sizeof(float2);
+constexpr size_t kMaxGroupSmem = kGroupNormMaxG * sizeof(float2);
 
 void fill_chunks(GroupNormArgs &p) {
   p.rows_per_chunk = static_cast<int32_t>(chunk_rows(p.B, p.S, p.C));
@@ -489,34 +529,23 @@ void fill_chunks(GroupNormArgs &p) {
 
 template <int ACT>
 cudaError_t run_forward(const GroupNormArgs &p, cudaStream_t stream) {
-  cudaError_t e = allow<gn_stats_kernel>(stats_smem(kGroupNormMaxC));
-  if (e != cudaSuccess) return e;
   const dim3 grid(p.chunks, p.B);
-  gn_stats_kernel<<<grid, kThreads, stats_smem(p.C), stream>>>(p);
-  e = cudaGetLastError();
+  const cudaError_t e = launch<gn_stats_kernel>(grid, lane_smem(p.C), kMaxLaneSmem, p, stream);
   if (e != cudaSuccess) return e;
-  gn_apply_kernel<ACT><<<grid, kThreads, p.G * sizeof(float2), stream>>>(p);
-  return cudaGetLastError();
+  return launch<gn_apply_kernel<ACT>>(grid, p.G * sizeof(float2), kMaxGroupSmem, p, stream);
 }
 
 template <int ACT>
 cudaError_t run_backward(GroupNormArgs p, bool gf32, cudaStream_t stream) {
-  cudaError_t e = allow<gn_bwd_sums_kernel<ACT>>(stats_smem(kGroupNormMaxC));
-  if (e != cudaSuccess) return e;
-  gn_bwd_sums_kernel<ACT><<<dim3(p.chunks, p.B), kThreads, stats_smem(p.C), stream>>>(p);
-  e = cudaGetLastError();
+  const cudaError_t e = launch<gn_bwd_sums_kernel<ACT>>(dim3(p.chunks, p.B), lane_smem(p.C),
+                                                        kMaxLaneSmem, p, stream);
   if (e != cudaSuccess) return e;
   p.grad_blocks = (p.dgamma || p.dbeta) ? (p.C + 31) / 32 : 0;
-  const int dx_blocks = p.dx ? p.chunks * p.B : 0;
-  const int grid = p.grad_blocks + dx_blocks;
+  const int grid = p.grad_blocks + (p.dx ? p.chunks * p.B : 0);
   if (grid == 0) return cudaSuccess;
-  size_t smem = kThreads * sizeof(double2);
-  if (smem < p.G * sizeof(float2)) smem = p.G * sizeof(float2);
-  if (gf32)
-    gn_bwd_dx_kernel<ACT, true><<<grid, kThreads, smem, stream>>>(p);
-  else
-    gn_bwd_dx_kernel<ACT, false><<<grid, kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  const size_t smem = p.G * sizeof(float2);
+  return gf32 ? launch<gn_bwd_dx_kernel<ACT, true>>(dim3(grid), smem, kMaxGroupSmem, p, stream)
+              : launch<gn_bwd_dx_kernel<ACT, false>>(dim3(grid), smem, kMaxGroupSmem, p, stream);
 }
 
 }  // namespace

@@ -317,11 +317,16 @@ sq_status launch_input_grad(const InputGradRequest &r, cudaStream_t stream) {
                                                r.status);
   if (cudaGetLastError() != cudaSuccess) return SQ_ERR_CUDA;
   const int sms = sm_count();
-  // The widest tile that still gives every SM one: a wide tile reads fewer
-  // operand bytes per product, a narrow one spreads a small layer.
+  // Tile width: a block's time goes with the operand rows of its tiles, 128 + BN
+  // each, times the rounds of tiles (1109 x 1536 x 1536: 108 tiles of 128 columns
+  // in one round beat 216 of 64 in two, 12 us against 20).
   const int64_t mt = (r.M + BM - 1) / BM;
-  if (mt * ((r.K + 255) / 256) >= sms) return run_gemm<256>(r, wt, ldw, sms, stream);
-  if (mt * ((r.K + 127) / 128) >= sms) return run_gemm<128>(r, wt, ldw, sms, stream);
+  auto cost = [&](int64_t bn) {
+    return (mt * ((r.K + bn - 1) / bn) + sms - 1) / sms * (BM + bn);
+  };
+  const int64_t c64 = cost(64), c128 = cost(128), c256 = cost(256);
+  if (c256 <= c128 && c256 <= c64) return run_gemm<256>(r, wt, ldw, sms, stream);
+  if (c128 <= c64) return run_gemm<128>(r, wt, ldw, sms, stream);
   return run_gemm<64>(r, wt, ldw, sms, stream);
 }
 

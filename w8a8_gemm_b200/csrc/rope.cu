@@ -197,12 +197,15 @@ template <typename T>
 cudaError_t run(RopeArgs p, bool half, cudaStream_t stream) {
   constexpr int N = Vec<T>::N;
   const bool vec = p.rot % (half ? 2 * N : N) == 0;
-  // Rows of a block: enough for one full round of units, with at most 32 KB of
-  // cosines and sines.
+  // Rows of a block: enough for every thread to have an angle to form and two
+  // units to turn, with at most 32 KB of cosines and sines, but no more than
+  // leave every SM four blocks.
   const int64_t units = static_cast<int64_t>(p.H) * p.D / (vec && half ? 2 * N : N);
-  int64_t rows = units > 0 ? kThreads * kMaxUnits / 2 / units : 1;
+  int64_t rows = kThreads / (p.rot / 2);
+  if (rows * units < 2 * kThreads) rows = 2 * kThreads / units;
   const int64_t most = 32768 / (static_cast<int64_t>(p.rot / 2) * 8);
   if (rows > most) rows = most;
+  if (rows > p.M / (4 * 148)) rows = p.M / (4 * 148);
   if (rows < 1) rows = 1;
   p.rows_per_block = static_cast<int>(rows);
   const int64_t blocks = (p.M + rows - 1) / rows;
