@@ -7,13 +7,21 @@
 //   dbeta = sum dv, dgamma = sum dv xh over samples and rows,
 //   dx = rstd (h - (sum_group h + xh sum_group h xh) / n).
 //
-// Both directions are bound by memory traffic and take two kernels: one reads
-// the rows and leaves partial results of its chunk of rows, the other joins the
-// partials (a few KB) and reads the rows again, from L2 where they fit.  The
-// statistics are Welford-style (count, mean, sum of squares about the mean):
-// eight rows at a time about their own mean, then joined, in fp32 and in fp64
-// for the last join, so that a mean far above the deviation costs no digits.
-// Every join runs in a fixed order.
+// Both directions are bound by memory traffic and the special-function unit
+// (two operations an element for SiLU and GELU).  Where a slab of whole groups of
+// one sample fits the shared memory of a cluster of at most eight blocks, one
+// kernel does it all: TMA brings every row once, the blocks' statistics meet in
+// distributed shared memory, and the result goes out by TMA from where the rows
+// stand.  Larger samples take two kernels: one reads the rows and leaves partial
+// results of its chunk of rows, the other joins the partials (a few KB) and reads
+// the rows again.
+//
+// The statistics are (count, mean, sum of squares about the mean): eight rows
+// at a time about their own mean, then joined, in fp32 and in fp64 for the last
+// join, so that a mean far above the deviation costs no digits.  Every join runs
+// in a fixed order.
+#include <cooperative_groups.h>
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -22,6 +30,8 @@
 
 namespace sq {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -59,15 +69,20 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + __expf(-v)); }
+// v / (1 + e^-u): v sigmoid(u).  The quick division is within two steps of fp32
+// and gives 0 where e^-u is past the largest number.
+__device__ __forceinline__ float times_sigmoid(float v, float u) {
+  return __fdividef(v, 1.0f + __expf(-u));
+}
+__device__ __forceinline__ float sigmoid(float u) { return times_sigmoid(1.0f, u); }
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 
 template <int ACT>
 __device__ __forceinline__ float act(float v) {
-  if constexpr (ACT == SQ_ACT_SILU) return v * sigmoid(v);
+  if constexpr (ACT == SQ_ACT_SILU) return times_sigmoid(v, v);
   // tanh GELU: v/2 (1 + tanh u) = v sigmoid(2u)
   if constexpr (ACT == SQ_ACT_GELU)
-    return v * sigmoid(2.0f * kGeluC * (v + 0.044715f * v * v * v));
+    return times_sigmoid(v, 2.0f * kGeluC * (v + 0.044715f * v * v * v));
   return v;
 }
 template <int ACT>
@@ -83,10 +98,106 @@ __device__ __forceinline__ float act_grad(float v) {
   return 1.0f;
 }
 
+// Running statistics of eight channels over the rows a thread has seen.
+struct Running {
+  F2 mean[4], m2[4];
+  float n;
+  __device__ __forceinline__ void clear() {
+    n = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mean[j] = m2[j] = f2(0.0f, 0.0f);
+  }
+  // joins `rows` rows of mean bm and squares bs about it
+  __device__ __forceinline__ void join(float rows, const F2 (&bm)[4], const F2 (&bs)[4]) {
+    const float total = n + rows, w = __fdividef(rows, total);
+    const F2 w2 = f2(w, w), nw = f2(n * w, n * w), minus = f2(-1.0f, -1.0f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const F2 delta = f2_fma(mean[j], minus, bm[j]);
+      mean[j] = f2_fma(delta, w2, mean[j]);
+      m2[j] = f2_fma(f2_mul(delta, delta), nw, f2_add(m2[j], bs[j]));
+    }
+    n = total;
+  }
+  __device__ __forceinline__ void batch(const uint4 (&v)[kBatch]) {
+    F2 bm[4], bs[4];
+    const F2 inv = f2(1.0f / kBatch, 1.0f / kBatch), minus = f2(-1.0f, -1.0f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      F2 x[kBatch];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q)
+        x[q] = f2_of_bf16(j == 0 ? v[q].x : j == 1 ? v[q].y : j == 2 ? v[q].z : v[q].w);
+      F2 s = x[0];
+#pragma unroll
+      for (int q = 1; q < kBatch; ++q) s = f2_add(s, x[q]);
+      bm[j] = f2_mul(s, inv);
+      bs[j] = f2(0.0f, 0.0f);
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const F2 d = f2_fma(bm[j], minus, x[q]);
+        bs[j] = f2_fma(d, d, bs[j]);
+      }
+    }
+    join(static_cast<float>(kBatch), bm, bs);
+  }
+  __device__ __forceinline__ void row(const uint4 &v) {
+    const F2 bm[4] = {f2_of_bf16(v.x), f2_of_bf16(v.y), f2_of_bf16(v.z), f2_of_bf16(v.w)};
+    const F2 zero = f2(0.0f, 0.0f), bs[4] = {zero, zero, zero, zero};
+    join(1.0f, bm, bs);
+  }
+  // {mean, squares} of each channel
+  __device__ __forceinline__ void store(float2 *to) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 a = f2_get(mean[j]), b = f2_get(m2[j]);
+      reinterpret_cast<float4 *>(to)[j] = make_float4(a.x, b.x, a.y, b.y);
+    }
+  }
+};
+
+// Joins the threads' statistics sh[lanes][width] (lane l saw the rows l, l + lanes,
+// ... of `rows`) into `out`(g, mean, squares) for each of `groups` groups of cg
+// channels: first the mean, then the squares about it.  Eight threads a group.
+template <int THREADS, typename Out>
+__device__ __forceinline__ void join_lanes(const float2 *sh, float *chan, int lanes, int width,
+                                           int rows, int groups, int cg, Out &&out) {
+  const int each = rows / lanes, more = rows % lanes;  // rows of a lane
+  __syncthreads();
+  for (int c = threadIdx.x; c < width; c += THREADS) {
+    float s = 0.0f;
+    for (int l = 0; l < lanes; ++l)
+      s = fmaf(static_cast<float>(each + (l < more)), sh[l * width + c].x, s);
+    chan[c] = s;
+  }
+  __syncthreads();
+  const int t = threadIdx.x & 7;
+  for (int g0 = 0; g0 < groups; g0 += THREADS / 8) {
+    const int g = g0 + (threadIdx.x >> 3);
+    float mean = 0.0f;
+    if (g < groups)
+      for (int c = t; c < cg; c += 8) mean += chan[g * cg + c];
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) mean += __shfl_xor_sync(~0u, mean, o);
+    mean /= static_cast<float>(cg) * static_cast<float>(rows);
+    float m2 = 0.0f;
+    if (g < groups)
+      for (int c = t; c < cg; c += 8)
+        for (int l = 0; l < lanes; ++l) {
+          const float2 v = sh[l * width + g * cg + c];
+          const float d = v.x - mean;
+          if (l < rows) m2 += fmaf(static_cast<float>(each + (l < more)) * d, d, v.y);
+        }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m2 += __shfl_xor_sync(~0u, m2, o);
+    if (g < groups && t == 0) out(g, mean, m2);
+  }
+}
+
 // ------------------------------------------------------------------- forward
 // Chunk statistics: part[b][chunk][g] = {mean, sum of squares about it}.
 __global__ void __launch_bounds__(kThreads) gn_stats_kernel(const GroupNormArgs p) {
-  extern __shared__ float2 sh[];  // a pass: [lanes][oct * 8] {mean, M2} of each thread's rows
+  extern __shared__ float2 sh[];  // [lanes][C] {mean, squares} of each thread's rows
   grid_dependency_wait();
   grid_dependency_launch();
   const int b = blockIdx.y;
@@ -95,79 +206,27 @@ __global__ void __launch_bounds__(kThreads) gn_stats_kernel(const GroupNormArgs 
   const Split sp = split_of(p.C);
   const int lane = threadIdx.x / sp.oct, oct = threadIdx.x % sp.oct;
   const uint16_t *x = p.x + (static_cast<int64_t>(b) * p.S + r0) * p.ldx;
-  const int octs = p.C / 8, width = octs * 8;  // of a lane's row in shared memory
-  for (int o = oct; o < octs; o += sp.oct) {
-    if (lane >= sp.lanes) break;
-    float mean[8], m2[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) mean[j] = m2[j] = 0.0f;
-    float n = 0.0f;
+  for (int o = oct; o < p.C / 8 && lane < sp.lanes; o += sp.oct) {
+    Running st;
+    st.clear();
     const uint16_t *src = x + o * 8;
-    for (int r = lane; r < rows; r += sp.lanes * kBatch) {
+    int r = lane;
+    for (; r + (kBatch - 1) * sp.lanes < rows; r += sp.lanes * kBatch) {
       uint4 v[kBatch];
-      int k = 0;
 #pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        const int rr = r + q * sp.lanes;
-        const bool in = rr < rows;
-        v[q] = in ? load8(src + rr * p.ldx) : make_uint4(0, 0, 0, 0);
-        k += in;
-      }
-      const float fk = static_cast<float>(k), inv = 1.0f / fk;
-      const float total = n + fk, w = fk / total;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float s = 0.0f;
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          const uint32_t word = j < 2 ? v[q].x : j < 4 ? v[q].y : j < 6 ? v[q].z : v[q].w;
-          s += (j & 1) ? bf16_hi(word) : bf16_lo(word);
-        }
-        const float bm = s * inv;
-        float bs = 0.0f;
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          const uint32_t word = j < 2 ? v[q].x : j < 4 ? v[q].y : j < 6 ? v[q].z : v[q].w;
-          const float d = ((j & 1) ? bf16_hi(word) : bf16_lo(word)) - bm;
-          bs = q < k ? fmaf(d, d, bs) : bs;
-        }
-        const float delta = bm - mean[j];
-        mean[j] = fmaf(delta, w, mean[j]);
-        m2[j] += bs + delta * delta * n * w;
-      }
-      n = total;
+      for (int q = 0; q < kBatch; ++q) v[q] = load8(src + (r + q * sp.lanes) * p.ldx);
+      st.batch(v);
     }
-    float4 *to = reinterpret_cast<float4 *>(sh + lane * width + o * 8);
-#pragma unroll
-    for (int j = 0; j < 8; j += 2)
-      to[j / 2] = make_float4(mean[j], m2[j], mean[j + 1], m2[j + 1]);
+    for (; r < rows; r += sp.lanes) st.row(load8(src + r * p.ldx));
+    st.store(sh + lane * p.C + o * 8);
   }
-  __syncthreads();
-  // join lanes and channels of each group: first the mean, then the squares about it
-  const int cg = p.C / p.G;
-  const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
-  const int lanes = rows < sp.lanes ? rows : sp.lanes;  // with rows
   const int64_t slot = (static_cast<int64_t>(b) * p.chunks + blockIdx.x) * p.G;
-  for (int g = warp; g < p.G; g += kWarps) {
-    float s = 0.0f;
-    for (int l = 0; l < lanes; ++l) {
-      const float n = static_cast<float>((rows - l + sp.lanes - 1) / sp.lanes);
-      for (int c = ln; c < cg; c += 32) s = fmaf(n, sh[l * width + g * cg + c].x, s);
-    }
-    const float mean = warp_sum(s) / (static_cast<float>(cg) * static_cast<float>(rows));
-    float m2 = 0.0f;
-    for (int l = 0; l < lanes; ++l) {
-      const float n = static_cast<float>((rows - l + sp.lanes - 1) / sp.lanes);
-      for (int c = ln; c < cg; c += 32) {
-        const float2 v = sh[l * width + g * cg + c];
-        const float d = v.x - mean;
-        m2 += fmaf(n * d, d, v.y);
-      }
-    }
-    m2 = warp_sum(m2);
-    if (ln == 0 && store_ok(p.status, slot + g < static_cast<int64_t>(p.B) * p.chunks * p.G))
-      p.part[slot + g] = make_float2(mean, m2);
-  }
+  join_lanes<kThreads>(sh, reinterpret_cast<float *>(sh + sp.lanes * p.C), sp.lanes, p.C, rows,
+                       p.G, p.C / p.G, [&](int g, float mean, float m2) {
+                         if (store_ok(p.status,
+                                      slot + g < static_cast<int64_t>(p.B) * p.chunks * p.G))
+                           p.part[slot + g] = make_float2(mean, m2);
+                       });
 }
 
 // Sums over a sample's chunks of {f(v, n), g(v, n)} of each group's partials, n
@@ -479,15 +538,15 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs
 int64_t chunk_rows(int64_t B, int64_t S, int64_t C) {
   const int64_t want = (2 * 148 + B - 1) / B;
   const int64_t least = static_cast<int64_t>(split_of(static_cast<int>(C)).lanes) * kBatch;
-  int64_t rows = (S + want - 1) / want;
-  if (rows < least) rows = least;
-  return rows;
+  const int64_t rows = (S + want - 1) / want;
+  return (rows + least - 1) / least * least;  // whole batches
 }
 
 // Shared memory of the first kernels: every thread's eight channels (or all
-// channels, where they are more).
+// channels, where they are more), and a float per channel.
 int lane_smem(int C) {
-  return (split_of(C).lanes * C) * static_cast<int>(sizeof(float2));
+  return split_of(C).lanes * C * static_cast<int>(sizeof(float2)) +
+         C * static_cast<int>(sizeof(float));
 }
 
 // Launch behind the kernel ahead in the stream (programmatic dependent launch:
@@ -519,7 +578,7 @@ cudaError_t launch(dim3 grid, size_t smem, size_t max_smem, const GroupNormArgs 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-constexpr size_t kMaxLaneSmem = kGroupNormMaxC * sizeof(float2);
+constexpr size_t kMaxLaneSmem = kGroupNormMaxC * (sizeof(float2) + sizeof(float));
 constexpr size_t kMaxGroupSmem = kGroupNormMaxG * sizeof(float2);
 
 void fill_chunks(GroupNormArgs &p) {
