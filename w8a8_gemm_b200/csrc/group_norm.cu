@@ -8,20 +8,17 @@
 //   dx = rstd (h - (sum_group h + xh sum_group h xh) / n).
 //
 // Both directions are bound by memory traffic and the special-function unit
-// (two operations an element for SiLU and GELU).  Where a slab of whole groups of
-// one sample fits the shared memory of a cluster of at most eight blocks, one
-// kernel does it all: TMA brings every row once, the blocks' statistics meet in
-// distributed shared memory, and the result goes out by TMA from where the rows
-// stand.  Larger samples take two kernels: one reads the rows and leaves partial
-// results of its chunk of rows, the other joins the partials (a few KB) and reads
-// the rows again.
+// (two operations an element for SiLU and GELU) and take two kernels: one reads
+// the rows and leaves partial results of its chunk of rows, the other joins the
+// partials (a few KB) and reads the rows again, from L2 where they fit.  (One
+// kernel with the rows kept in a cluster's shared memory was measured: clusters
+// of eight with 200 KB a block find room for 120 of 148 SMs, and 2 x 16384 x 320
+// took 34 us in two rounds, 19 in two kernels.)
 //
 // The statistics are (count, mean, sum of squares about the mean): eight rows
 // at a time about their own mean, then joined, in fp32 and in fp64 for the last
 // join, so that a mean far above the deviation costs no digits.  Every join runs
 // in a fixed order.
-#include <cooperative_groups.h>
-#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -31,11 +28,10 @@
 namespace sq {
 namespace {
 
-namespace cg = cooperative_groups;
-
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 8;  // rows whose values a thread holds at once
+constexpr int kBatch = 8;  // rows of one step of the statistics
+constexpr int kAhead = 4;  // rows whose loads a thread has under way elsewhere
 
 __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -158,40 +154,82 @@ struct Running {
 
 // Joins the threads' statistics sh[lanes][width] (lane l saw the rows l, l + lanes,
 // ... of `rows`) into `out`(g, mean, squares) for each of `groups` groups of cg
-// channels: first the mean, then the squares about it.  Eight threads a group.
+// channels: first the mean, then the squares about it.  A warp a group.
 template <int THREADS, typename Out>
-__device__ __forceinline__ void join_lanes(const float2 *sh, float *chan, int lanes, int width,
-                                           int rows, int groups, int cg, Out &&out) {
+__device__ __forceinline__ void join_lanes(const float2 *sh, int lanes, int width, int rows,
+                                           int groups, int cg, Out &&out) {
   const int each = rows / lanes, more = rows % lanes;  // rows of a lane
+  const int used = rows < lanes ? rows : lanes;        // lanes with any
+  const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
+  const int dl = 32 / cg, dc = 32 % cg, l0 = ln / cg, k0 = ln % cg;
   __syncthreads();
-  for (int c = threadIdx.x; c < width; c += THREADS) {
+  for (int g = warp; g < groups; g += THREADS / 32) {
+    const float2 *src = sh + g * cg;
     float s = 0.0f;
-    for (int l = 0; l < lanes; ++l)
-      s = fmaf(static_cast<float>(each + (l < more)), sh[l * width + c].x, s);
-    chan[c] = s;
+    int l = l0, c = k0;
+    while (l < used) {
+      s = fmaf(static_cast<float>(each + (l < more)), src[l * width + c].x, s);
+      l += dl;
+      c += dc;
+      if (c >= cg) {
+        c -= cg;
+        ++l;
+      }
+    }
+    const float mean = warp_sum(s) / (static_cast<float>(cg) * static_cast<float>(rows));
+    float m2 = 0.0f;
+    l = l0;
+    c = k0;
+    while (l < used) {
+      const float2 v = src[l * width + c];
+      const float d = v.x - mean;
+      m2 += fmaf(static_cast<float>(each + (l < more)) * d, d, v.y);
+      l += dl;
+      c += dc;
+      if (c >= cg) {
+        c -= cg;
+        ++l;
+      }
+    }
+    m2 = warp_sum(m2);
+    if (ln == 0) out(g, mean, m2);
+  }
+}
+
+// chan[c] = sum over l of sh[l][c], c < width, by all threads in a fixed order.
+template <int THREADS>
+__device__ __forceinline__ void channel_sums(float2 *sh, float2 *chan, int lanes, int width) {
+  __syncthreads();
+  if (width > THREADS) {  // few lanes
+    for (int c = threadIdx.x; c < width; c += THREADS) {
+      float2 s = sh[c];
+      for (int l = 1; l < lanes; ++l) {
+        s.x += sh[l * width + c].x;
+        s.y += sh[l * width + c].y;
+      }
+      chan[c] = s;
+    }
+  } else {
+    const int parts = THREADS / width < lanes ? THREADS / width : lanes;
+    const int part = threadIdx.x / width, c = threadIdx.x % width;
+    float2 s = make_float2(0.0f, 0.0f);
+    if (part < parts)
+      for (int l = part; l < lanes; l += parts) {
+        s.x += sh[l * width + c].x;
+        s.y += sh[l * width + c].y;
+      }
+    __syncthreads();
+    if (part < parts) sh[part * width + c] = s;
+    __syncthreads();
+    if (part == 0) {
+      for (int q = 1; q < parts; ++q) {
+        s.x += sh[q * width + c].x;
+        s.y += sh[q * width + c].y;
+      }
+      chan[c] = s;
+    }
   }
   __syncthreads();
-  const int t = threadIdx.x & 7;
-  for (int g0 = 0; g0 < groups; g0 += THREADS / 8) {
-    const int g = g0 + (threadIdx.x >> 3);
-    float mean = 0.0f;
-    if (g < groups)
-      for (int c = t; c < cg; c += 8) mean += chan[g * cg + c];
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) mean += __shfl_xor_sync(~0u, mean, o);
-    mean /= static_cast<float>(cg) * static_cast<float>(rows);
-    float m2 = 0.0f;
-    if (g < groups)
-      for (int c = t; c < cg; c += 8)
-        for (int l = 0; l < lanes; ++l) {
-          const float2 v = sh[l * width + g * cg + c];
-          const float d = v.x - mean;
-          if (l < rows) m2 += fmaf(static_cast<float>(each + (l < more)) * d, d, v.y);
-        }
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) m2 += __shfl_xor_sync(~0u, m2, o);
-    if (g < groups && t == 0) out(g, mean, m2);
-  }
 }
 
 // ------------------------------------------------------------------- forward
@@ -221,8 +259,7 @@ __global__ void __launch_bounds__(kThreads) gn_stats_kernel(const GroupNormArgs 
     st.store(sh + lane * p.C + o * 8);
   }
   const int64_t slot = (static_cast<int64_t>(b) * p.chunks + blockIdx.x) * p.G;
-  join_lanes<kThreads>(sh, reinterpret_cast<float *>(sh + sp.lanes * p.C), sp.lanes, p.C, rows,
-                       p.G, p.C / p.G, [&](int g, float mean, float m2) {
+  join_lanes<kThreads>(sh, sp.lanes, p.C, rows, p.G, p.C / p.G, [&](int g, float mean, float m2) {
                          if (store_ok(p.status,
                                       slot + g < static_cast<int64_t>(p.B) * p.chunks * p.G))
                            p.part[slot + g] = make_float2(mean, m2);
@@ -288,7 +325,7 @@ __device__ __forceinline__ void join_stats(const GroupNormArgs &p, int b, float2
 }
 
 template <int ACT>
-__global__ void __launch_bounds__(kThreads) gn_apply_kernel(const GroupNormArgs p) {
+__global__ void __launch_bounds__(kThreads, 4) gn_apply_kernel(const GroupNormArgs p) {
   extern __shared__ float2 sh[];  // [G] {mean, rstd}
   __shared__ double2 sums[kThreads];
   grid_dependency_wait();
@@ -300,8 +337,8 @@ __global__ void __launch_bounds__(kThreads) gn_apply_kernel(const GroupNormArgs 
         p.mean[b * p.G + g] = sh[g].x;
         p.rstd[b * p.G + g] = sh[g].y;
       }
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_chunk;
-  const int rows = p.S - r0 < p.rows_per_chunk ? static_cast<int>(p.S - r0) : p.rows_per_chunk;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows2;
+  const int rows = p.S - r0 < p.rows2 ? static_cast<int>(p.S - r0) : p.rows2;
   const Split sp = split_of(p.C);
   const int lane = threadIdx.x / sp.oct, oct = threadIdx.x % sp.oct;
   if (lane >= sp.lanes) return;
@@ -309,50 +346,96 @@ __global__ void __launch_bounds__(kThreads) gn_apply_kernel(const GroupNormArgs 
   const int64_t row0 = static_cast<int64_t>(b) * p.S + r0;
   for (int o = oct; o < p.C / 8; o += sp.oct) {
     const int c0 = o * 8;
-    float mean[8], a[8], beta[8];
+    F2 minus_mean[4], scale[4], shift[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 s = sh[(c0 + j) / cg];
-      mean[j] = s.x;
-      a[j] = s.y * (p.gamma ? bf16_lo(p.gamma[c0 + j]) : 1.0f);
-      beta[j] = p.beta ? bf16_lo(p.beta[c0 + j]) : 0.0f;
+    for (int j = 0; j < 4; ++j) {
+      float m[2], k[2], t[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = c0 + 2 * j + e;
+        const float2 v = sh[c / cg];
+        m[e] = -v.x;
+        k[e] = v.y * (p.gamma ? bf16_lo(p.gamma[c]) : 1.0f);
+        t[e] = p.beta ? bf16_lo(p.beta[c]) : 0.0f;
+      }
+      minus_mean[j] = f2(m[0], m[1]);
+      scale[j] = f2(k[0], k[1]);
+      shift[j] = f2(t[0], t[1]);
     }
-    for (int r = lane; r < rows; r += sp.lanes * 4) {
-      uint4 v[4];
+    for (int r = lane; r < rows; r += sp.lanes * kAhead) {
+      uint4 v[kAhead];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < kAhead; ++q)
         if (r + q * sp.lanes < rows) v[q] = load8(p.x + (row0 + r + q * sp.lanes) * p.ldx + c0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < kAhead; ++q) {
         if (r + q * sp.lanes >= rows) break;
-        float f[8];
-        unpack8(v[q], f);
+        const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+        uint32_t y[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = act<ACT>(fmaf(f[j] - mean[j], a[j], beta[j]));
+        for (int j = 0; j < 4; ++j) {
+          const float2 z =
+              f2_get(f2_fma(f2_add(f2_of_bf16(w[j]), minus_mean[j]), scale[j], shift[j]));
+          y[j] = bf16x2(act<ACT>(z.x), act<ACT>(z.y));
+        }
         const int64_t row = row0 + r + q * sp.lanes;
         if (store_ok(p.status, row < static_cast<int64_t>(p.B) * p.S && c0 + 8 <= p.ldy))
-          *reinterpret_cast<uint4 *>(p.y + row * p.ldy + c0) = pack8(f);
+          *reinterpret_cast<uint4 *>(p.y + row * p.ldy + c0) = make_uint4(y[0], y[1], y[2], y[3]);
       }
     }
   }
 }
 
 // ------------------------------------------------------------------ backward
-// One channel's fixed values.
-struct Chan {
-  float mean, rstd, gamma, beta;
+// The fixed values of a thread's eight channels.
+struct Octet {
+  F2 minus_mean[4], rstd[4], gamma[4], beta[4];
+  __device__ __forceinline__ void load(const GroupNormArgs &p, int b, int c0, int cg) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float m[2], r[2], g[2], t[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = c0 + 2 * j + e, at = b * p.G + c / cg;
+        m[e] = -p.mean[at];
+        r[e] = p.rstd[at];
+        g[e] = p.gamma ? bf16_lo(p.gamma[c]) : 1.0f;
+        t[e] = p.beta ? bf16_lo(p.beta[c]) : 0.0f;
+      }
+      minus_mean[j] = f2(m[0], m[1]);
+      rstd[j] = f2(r[0], r[1]);
+      gamma[j] = f2(g[0], g[1]);
+      beta[j] = f2(t[0], t[1]);
+    }
+  }
+  // xh and dv of the channels 2 j, 2 j + 1
+  template <int ACT>
+  __device__ __forceinline__ void at(uint32_t x, uint32_t dy, int j, F2 &xh, F2 &dv) const {
+    xh = f2_mul(f2_add(f2_of_bf16(x), minus_mean[j]), rstd[j]);
+    dv = f2_of_bf16(dy);
+    if constexpr (ACT != SQ_ACT_NONE) {
+      const float2 v = f2_get(f2_fma(xh, gamma[j], beta[j]));
+      dv = f2_mul(dv, f2(act_grad<ACT>(v.x), act_grad<ACT>(v.y)));
+    }
+  }
 };
-__device__ __forceinline__ Chan chan_of(const GroupNormArgs &p, int b, int c, int cg) {
-  const int g = c / cg;
-  return {p.mean[b * p.G + g], p.rstd[b * p.G + g], p.gamma ? bf16_lo(p.gamma[c]) : 1.0f,
-          p.beta ? bf16_lo(p.beta[c]) : 0.0f};
+
+template <bool GF32>
+__device__ __forceinline__ void store_param_grads(const GroupNormArgs &p, int c, float s, float sx) {
+  if constexpr (GF32) {
+    if (p.dgamma) static_cast<float *>(p.dgamma)[c] = sx;
+    if (p.dbeta) static_cast<float *>(p.dbeta)[c] = s;
+  } else {
+    if (p.dgamma) static_cast<__nv_bfloat16 *>(p.dgamma)[c] = __float2bfloat16_rn(sx);
+    if (p.dbeta) static_cast<__nv_bfloat16 *>(p.dbeta)[c] = __float2bfloat16_rn(s);
+  }
 }
 
 // Chunk sums: chan_part[b][chunk][c] = {sum dv, sum dv xh} and
 // part[b][chunk][g] = {sum h, sum h xh}.
 template <int ACT>
 __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const GroupNormArgs p) {
-  extern __shared__ float2 sh[];  // [lanes][C], then the channels' sums in its first row
+  extern __shared__ float2 sh[];  // [lanes][C], then the channels' sums
   grid_dependency_wait();
   grid_dependency_launch();
   const int b = blockIdx.y;
@@ -364,64 +447,56 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const GroupNormAr
   const int64_t row0 = static_cast<int64_t>(b) * p.S + r0;
   const int64_t slot = static_cast<int64_t>(b) * p.chunks + blockIdx.x;
 
-  for (int o = oct; o < p.C / 8; o += sp.oct) {
-    if (lane >= sp.lanes) break;
+  for (int o = oct; o < p.C / 8 && lane < sp.lanes; o += sp.oct) {
     const int c0 = o * 8;
-    Chan ch[8];
-    float sd[8], sx[8];
+    Octet ch;
+    ch.load(p, b, c0, cg);
+    F2 sd[4], sx[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      ch[j] = chan_of(p, b, c0 + j, cg);
-      sd[j] = sx[j] = 0.0f;
-    }
-    for (int r = lane; r < rows; r += sp.lanes * 4) {
-      uint4 vx[4], vd[4];
+    for (int j = 0; j < 4; ++j) sd[j] = sx[j] = f2(0.0f, 0.0f);
+    for (int r = lane; r < rows; r += sp.lanes * kAhead) {
+      uint4 vx[kAhead], vd[kAhead];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < kAhead; ++q) {
         const int64_t row = row0 + r + q * sp.lanes;
-        const bool in = r + q * sp.lanes < rows;
-        vx[q] = in ? load8(p.x + row * p.ldx + c0) : make_uint4(0, 0, 0, 0);
-        vd[q] = in ? load8(p.dy + row * p.lddy + c0) : make_uint4(0, 0, 0, 0);
+        if (r + q * sp.lanes < rows) {
+          vx[q] = load8(p.x + row * p.ldx + c0);
+          vd[q] = load8(p.dy + row * p.lddy + c0);
+        }
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < kAhead; ++q) {
         if (r + q * sp.lanes >= rows) break;
-        float x[8], d[8];
-        unpack8(vx[q], x);
-        unpack8(vd[q], d);
+        const uint32_t x[4] = {vx[q].x, vx[q].y, vx[q].z, vx[q].w};
+        const uint32_t d[4] = {vd[q].x, vd[q].y, vd[q].z, vd[q].w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float xh = (x[j] - ch[j].mean) * ch[j].rstd;
-          const float dv = d[j] * act_grad<ACT>(fmaf(xh, ch[j].gamma, ch[j].beta));
-          sd[j] += dv;
-          sx[j] = fmaf(dv, xh, sx[j]);
+        for (int j = 0; j < 4; ++j) {
+          F2 xh, dv;
+          ch.at<ACT>(x[j], d[j], j, xh, dv);
+          sd[j] = f2_add(sd[j], dv);
+          sx[j] = f2_fma(dv, xh, sx[j]);
         }
       }
     }
     float4 *to = reinterpret_cast<float4 *>(sh + lane * p.C + c0);
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) to[j / 2] = make_float4(sd[j], sx[j], sd[j + 1], sx[j + 1]);
-  }
-  __syncthreads();
-  for (int c = threadIdx.x; c < p.C; c += kThreads) {
-    float2 s = sh[c];
-    for (int l = 1; l < sp.lanes; ++l) {
-      const float2 v = sh[l * p.C + c];
-      s.x += v.x;
-      s.y += v.y;
+    for (int j = 0; j < 4; ++j) {
+      const float2 u = f2_get(sd[j]), v = f2_get(sx[j]);
+      to[j] = make_float4(u.x, v.x, u.y, v.y);
     }
-    sh[c] = s;
-    if (store_ok(p.status, slot < static_cast<int64_t>(p.B) * p.chunks))
-      p.chan_part[slot * p.C + c] = s;
   }
-  __syncthreads();
+  float2 *chan = sh + sp.lanes * p.C;
+  channel_sums<kThreads>(sh, chan, sp.lanes, p.C);
+  for (int c = threadIdx.x; c < p.C; c += kThreads)
+    if (store_ok(p.status, slot < static_cast<int64_t>(p.B) * p.chunks))
+      p.chan_part[slot * p.C + c] = chan[c];
   const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
   for (int g = warp; g < p.G; g += kWarps) {
     float s1 = 0.0f, s2 = 0.0f;
     for (int c = g * cg + ln; c < (g + 1) * cg; c += 32) {
       const float gm = p.gamma ? bf16_lo(p.gamma[c]) : 1.0f;
-      s1 = fmaf(gm, sh[c].x, s1);
-      s2 = fmaf(gm, sh[c].y, s2);
+      s1 = fmaf(gm, chan[c].x, s1);
+      s2 = fmaf(gm, chan[c].y, s2);
     }
     s1 = warp_sum(s1);
     s2 = warp_sum(s2);
@@ -457,73 +532,66 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs
       sx += sums[w * 32 + ln].y;
     }
     if (!store_ok(p.status, c < p.C)) return;
-    if constexpr (GF32) {
-      if (p.dgamma) static_cast<float *>(p.dgamma)[c] = static_cast<float>(sx);
-      if (p.dbeta) static_cast<float *>(p.dbeta)[c] = static_cast<float>(s);
-    } else {
-      if (p.dgamma)
-        static_cast<__nv_bfloat16 *>(p.dgamma)[c] = __float2bfloat16_rn(static_cast<float>(sx));
-      if (p.dbeta)
-        static_cast<__nv_bfloat16 *>(p.dbeta)[c] = __float2bfloat16_rn(static_cast<float>(s));
-    }
+    store_param_grads<GF32>(p, c, static_cast<float>(s), static_cast<float>(sx));
     return;
   }
   const int blk = blockIdx.x - p.grad_blocks;
-  const int b = blk / p.chunks, chunk = blk % p.chunks;
+  const int b = blk / p.chunks2, chunk = blk % p.chunks2;
   const int cg = p.C / p.G;
   const double n = static_cast<double>(p.S) * cg;
-  // group sums over n
+  // group sums over -n
   for (int g0 = 0; g0 < p.G; g0 += kThreads) {
     const int width = p.G - g0 < kThreads ? p.G - g0 : kThreads;
     chunk_sums(p, b, sums, g0, width,
                [](float2 v, double) { return make_double2(v.x, v.y); });
     if (threadIdx.x < width)
-      sh[g0 + threadIdx.x] = make_float2(static_cast<float>(sums[threadIdx.x].x / n),
-                                         static_cast<float>(sums[threadIdx.x].y / n));
+      sh[g0 + threadIdx.x] = make_float2(static_cast<float>(-sums[threadIdx.x].x / n),
+                                         static_cast<float>(-sums[threadIdx.x].y / n));
   }
   __syncthreads();
-  const int64_t r0 = static_cast<int64_t>(chunk) * p.rows_per_chunk;
-  const int rows = p.S - r0 < p.rows_per_chunk ? static_cast<int>(p.S - r0) : p.rows_per_chunk;
+  const int64_t r0 = static_cast<int64_t>(chunk) * p.rows2;
+  const int rows = p.S - r0 < p.rows2 ? static_cast<int>(p.S - r0) : p.rows2;
   const Split sp = split_of(p.C);
   const int lane = threadIdx.x / sp.oct, oct = threadIdx.x % sp.oct;
   if (lane >= sp.lanes) return;
   const int64_t row0 = static_cast<int64_t>(b) * p.S + r0;
   for (int o = oct; o < p.C / 8; o += sp.oct) {
     const int c0 = o * 8;
-    Chan ch[8];
-    float m1[8], m2[8];
+    Octet ch;
+    ch.load(p, b, c0, cg);
+    F2 m1[4], m2[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      ch[j] = chan_of(p, b, c0 + j, cg);
-      const float2 s = sh[(c0 + j) / cg];
-      m1[j] = s.x;
-      m2[j] = s.y;
+    for (int j = 0; j < 4; ++j) {
+      const float2 s = sh[(c0 + 2 * j) / cg], t = sh[(c0 + 2 * j + 1) / cg];
+      m1[j] = f2(s.x, t.x);
+      m2[j] = f2(s.y, t.y);
     }
-    for (int r = lane; r < rows; r += sp.lanes * 4) {
-      uint4 vx[4], vd[4];
+    for (int r = lane; r < rows; r += sp.lanes * kAhead) {
+      uint4 vx[kAhead], vd[kAhead];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < kAhead; ++q)
         if (r + q * sp.lanes < rows) {
           const int64_t row = row0 + r + q * sp.lanes;
           vx[q] = load8(p.x + row * p.ldx + c0);
           vd[q] = load8(p.dy + row * p.lddy + c0);
         }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < kAhead; ++q) {
         if (r + q * sp.lanes >= rows) break;
-        float x[8], d[8];
-        unpack8(vx[q], x);
-        unpack8(vd[q], d);
+        const uint32_t x[4] = {vx[q].x, vx[q].y, vx[q].z, vx[q].w};
+        const uint32_t d[4] = {vd[q].x, vd[q].y, vd[q].z, vd[q].w};
+        uint32_t y[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float xh = (x[j] - ch[j].mean) * ch[j].rstd;
-          const float h =
-              d[j] * act_grad<ACT>(fmaf(xh, ch[j].gamma, ch[j].beta)) * ch[j].gamma;
-          x[j] = ch[j].rstd * (h - m1[j] - xh * m2[j]);
+        for (int j = 0; j < 4; ++j) {
+          F2 xh, dv;
+          ch.at<ACT>(x[j], d[j], j, xh, dv);
+          const float2 z = f2_get(f2_mul(
+              ch.rstd[j], f2_add(f2_fma(dv, ch.gamma[j], m1[j]), f2_mul(xh, m2[j]))));
+          y[j] = bf16x2(z.x, z.y);
         }
         const int64_t row = row0 + r + q * sp.lanes;
         if (store_ok(p.status, row < static_cast<int64_t>(p.B) * p.S && c0 + 8 <= p.lddx))
-          *reinterpret_cast<uint4 *>(p.dx + row * p.lddx + c0) = pack8(x);
+          *reinterpret_cast<uint4 *>(p.dx + row * p.lddx + c0) = make_uint4(y[0], y[1], y[2], y[3]);
       }
     }
   }
@@ -543,11 +611,8 @@ int64_t chunk_rows(int64_t B, int64_t S, int64_t C) {
 }
 
 // Shared memory of the first kernels: every thread's eight channels (or all
-// channels, where they are more), and a float per channel.
-int lane_smem(int C) {
-  return split_of(C).lanes * C * static_cast<int>(sizeof(float2)) +
-         C * static_cast<int>(sizeof(float));
-}
+// channels, where they are more), and two floats per channel.
+int lane_smem(int C) { return (split_of(C).lanes + 1) * C * static_cast<int>(sizeof(float2)); }
 
 // Launch behind the kernel ahead in the stream (programmatic dependent launch:
 // every kernel here waits for it before it reads anything).
@@ -578,20 +643,28 @@ cudaError_t launch(dim3 grid, size_t smem, size_t max_smem, const GroupNormArgs 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-constexpr size_t kMaxLaneSmem = kGroupNormMaxC * (sizeof(float2) + sizeof(float));
+constexpr size_t kMaxLaneSmem = kGroupNormMaxC * 2 * sizeof(float2);
 constexpr size_t kMaxGroupSmem = kGroupNormMaxG * sizeof(float2);
 
 void fill_chunks(GroupNormArgs &p) {
   p.rows_per_chunk = static_cast<int32_t>(chunk_rows(p.B, p.S, p.C));
   p.chunks = static_cast<int32_t>((p.S + p.rows_per_chunk - 1) / p.rows_per_chunk);
+  // Rows of a block of the second kernel: four blocks per SM, whose joins and
+  // loads hide one another.
+  const int64_t want = (4 * 148 + p.B - 1) / p.B;
+  const int64_t least = static_cast<int64_t>(split_of(p.C).lanes) * kAhead;
+  const int64_t rows = (p.S + want - 1) / want;
+  p.rows2 = static_cast<int32_t>((rows + least - 1) / least * least);
+  p.chunks2 = static_cast<int32_t>((p.S + p.rows2 - 1) / p.rows2);
 }
 
 template <int ACT>
 cudaError_t run_forward(const GroupNormArgs &p, cudaStream_t stream) {
-  const dim3 grid(p.chunks, p.B);
-  const cudaError_t e = launch<gn_stats_kernel>(grid, lane_smem(p.C), kMaxLaneSmem, p, stream);
+  const cudaError_t e =
+      launch<gn_stats_kernel>(dim3(p.chunks, p.B), lane_smem(p.C), kMaxLaneSmem, p, stream);
   if (e != cudaSuccess) return e;
-  return launch<gn_apply_kernel<ACT>>(grid, p.G * sizeof(float2), kMaxGroupSmem, p, stream);
+  return launch<gn_apply_kernel<ACT>>(dim3(p.chunks2, p.B), p.G * sizeof(float2), kMaxGroupSmem, p,
+                                      stream);
 }
 
 template <int ACT>
@@ -600,7 +673,7 @@ cudaError_t run_backward(GroupNormArgs p, bool gf32, cudaStream_t stream) {
                                                         kMaxLaneSmem, p, stream);
   if (e != cudaSuccess) return e;
   p.grad_blocks = (p.dgamma || p.dbeta) ? (p.C + 31) / 32 : 0;
-  const int grid = p.grad_blocks + (p.dx ? p.chunks * p.B : 0);
+  const int grid = p.grad_blocks + (p.dx ? p.chunks2 * p.B : 0);
   if (grid == 0) return cudaSuccess;
   const size_t smem = p.G * sizeof(float2);
   return gf32 ? launch<gn_bwd_dx_kernel<ACT, true>>(dim3(grid), smem, kMaxGroupSmem, p, stream)
