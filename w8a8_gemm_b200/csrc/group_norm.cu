@@ -33,18 +33,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 8;  // rows of one step of the statistics
 constexpr int kAhead = 4;  // rows whose loads a thread has under way elsewhere
 
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    f[2 * j] = bf16_lo(w[j]);
-    f[2 * j + 1] = bf16_hi(w[j]);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]),
-                    bf16x2(f[6], f[7]));
-}
 __device__ __forceinline__ uint4 load8(const uint16_t *p) {
   return *reinterpret_cast<const uint4 *>(p);
 }

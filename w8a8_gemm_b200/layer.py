@@ -1,16 +1,36 @@
-"""Layer-level use of the library: one DualScale + SegLinear quantized linear.
+"""Layer-level use of the library: one DualScale + SegLinear quantized linear,
+its adapters and gradients, and what stands before an attention.
 
 Offline (once): quantize the weight segment-wise and calibrate s+ / s- on a
 calibration slice -- both on the GPU through the C ABI.  Online (per call):
 quantize the activation into the stacked planes, then run the fused GEMM.
+The quantized weight is frozen; adapters beside it are trained with the
+explicit forward and backward calls below.
 """
 from __future__ import annotations
 
-from typing import Optional
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
 from . import binding as B
+
+
+class Adapters:
+    """The low-rank adapters of one layer: A bf16 [L][R][K], B bf16 [L][N][R],
+    scale fp32 [L] (CUDA).  Adapter a adds scale[a] B[a] A[a] x to the layer's
+    output of every row it is named for."""
+
+    def __init__(self, A: torch.Tensor, B_: torch.Tensor, scale: torch.Tensor):
+        if A.dim() != 3 or B_.dim() != 3 or A.shape[0] != B_.shape[0] or \
+                A.shape[1] != B_.shape[2] or scale.shape != A.shape[:1]:
+            raise ValueError("A must be [L, R, K], B [L, N, R] and scale [L]")
+        self.A, self.B, self.scale = A, B_, scale
+
+    def plan(self, ids: torch.Tensor) -> torch.Tensor:
+        """The plan of a batch with adapter ids[m] (int32 [M]; -1: none) on row m;
+        it serves every layer with as many adapters."""
+        return B.sq_lora_plan(ids, self.A.shape[0])
 
 
 class DualScaleSegLinear:
@@ -125,3 +145,112 @@ class DualScaleSegLinear:
 
     def __call__(self, x: torch.Tensor, y: Optional[torch.Tensor] = None) -> torch.Tensor:
         return self.gemm(self.quantize(x), y)
+
+    def adapted(self, x: torch.Tensor, adapters: Adapters, plan: torch.Tensor,
+                y: Optional[torch.Tensor] = None):
+        """(y, t): the layer's output with its rows' adapters added, in place on
+        the GEMM's output, and t [M, R] for adapted_backward."""
+        y = self(x, y)
+        return B.sq_lora_forward(x, adapters.A, adapters.B, adapters.scale, plan, y, y=y)
+
+    def input_grad(self, dy: torch.Tensor, dx: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """dL/dx of the frozen layer from dy bf16 [M, N], straight through the
+        activation quantizer."""
+        if self.wq4 is not None:
+            B.sq_unpack_weight_w4(self.wq4, self.wq)
+        return B.sq_dualscale_seglinear_input_grad(dy, self.wq, self.s_w, self.d, self.seg, dx=dx,
+                                                   workspace=workspace)
+
+    def adapted_backward(self, dy: torch.Tensor, x: torch.Tensor, t: torch.Tensor,
+                         adapters: Adapters, plan: torch.Tensor, grad_dtype=torch.bfloat16,
+                         need_dx: bool = True):
+        """(dA, dB, dx) of adapted(); x is its input and t its second result.  dx
+        (None without need_dx) joins the frozen layer's part and the adapters'."""
+        dx = self.input_grad(dy) if need_dx else None
+        return B.sq_lora_backward(dy, x, t, adapters.A, adapters.B, adapters.scale, plan, dx,
+                                  dx=dx, grad_dtype=grad_dtype, need_dx=need_dx)
+
+
+class AttentionGrads(NamedTuple):
+    x: torch.Tensor                 # bf16 [B, S, C]
+    gamma: Optional[torch.Tensor]   # [C]
+    beta: Optional[torch.Tensor]
+    A: Optional[torch.Tensor]       # as the adapters
+    B: Optional[torch.Tensor]
+
+
+class AttentionInput:
+    """From features to q|k|v: an optional channels-last group norm with its
+    activation, the quantized projection with its rows' adapters, and rotary
+    positions on the q and k columns, in place.
+
+    qkv       DualScaleSegLinear with bf16 output, columns q | k | v
+    head_dim  columns of a head
+    rotated_heads  heads that turn: q's and k's, the first columns of the output
+    inv_freq  fp32 CUDA [rot / 2], with `factor` from binding.sq_rope_frequencies
+    layout, axis_pairs  as in binding.sq_rope_forward
+    groups    groups of the norm (0: no norm); gamma, beta, eps, act as in
+              binding.sq_group_norm_forward
+    """
+
+    def __init__(self, qkv: DualScaleSegLinear, head_dim: int, rotated_heads: int,
+                 inv_freq: torch.Tensor, factor: float = 1.0,
+                 layout: int = B.SQ_ROPE_INTERLEAVED, axis_pairs: Optional[Sequence[int]] = None,
+                 groups: int = 0, gamma: Optional[torch.Tensor] = None,
+                 beta: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                 act: int = B.SQ_ACT_NONE):
+        if qkv.out_dtype != torch.bfloat16:
+            raise ValueError("the projection must write bf16")
+        if head_dim < 1 or rotated_heads < 1 or rotated_heads * head_dim > qkv.N:
+            raise ValueError("the rotated heads must lie within the projection's output")
+        if groups == 0 and (gamma is not None or beta is not None or act != B.SQ_ACT_NONE):
+            raise ValueError("gamma, beta and act belong to a norm (groups > 0)")
+        self.qkv, self.head_dim, self.turned = qkv, head_dim, rotated_heads * head_dim
+        self.inv_freq, self.factor = inv_freq, factor
+        self.layout, self.axis_pairs = layout, axis_pairs
+        self.groups, self.gamma, self.beta, self.eps, self.act = groups, gamma, beta, eps, act
+
+    def _rope(self, call, x, positions, out):
+        return call(x, positions, self.inv_freq, self.head_dim, out, layout=self.layout,
+                    axis_pairs=self.axis_pairs, factor=self.factor)
+
+    def forward(self, x: torch.Tensor, positions: torch.Tensor,
+                adapters: Optional[Adapters] = None, plan: Optional[torch.Tensor] = None):
+        """x bf16 [B, S, C] -> (q|k|v bf16 [B * S, N], saved); positions int32
+        [B * S] or [B * S, axes]; adapters and plan (of the B * S rows) together."""
+        if (adapters is None) != (plan is None):
+            raise ValueError("adapters and plan come together")
+        mean = rstd = t = None
+        h = x
+        if self.groups:
+            h, mean, rstd = B.sq_group_norm_forward(x, self.groups, self.gamma, self.beta,
+                                                    eps=self.eps, act=self.act)
+        h = h.reshape(-1, x.shape[2])
+        if adapters is None:
+            y = self.qkv(h)
+        else:
+            y, t = self.qkv.adapted(h, adapters, plan)
+        qk = y[:, :self.turned]
+        self._rope(B.sq_rope_forward, qk, positions, qk)
+        return y, (x, h, mean, rstd, t, positions, adapters, plan)
+
+    __call__ = forward
+
+    def backward(self, dy: torch.Tensor, saved, grad_dtype=torch.bfloat16) -> AttentionGrads:
+        """The gradients of forward() from dy bf16 [B * S, N], whose q and k columns
+        are turned back in place."""
+        x, h, mean, rstd, t, positions, adapters, plan = saved
+        qk = dy[:, :self.turned]
+        self._rope(B.sq_rope_backward, qk, positions, qk)
+        dA = dB = dgamma = dbeta = None
+        if adapters is None:
+            dx = self.qkv.input_grad(dy)
+        else:
+            dA, dB, dx = self.qkv.adapted_backward(dy, h, t, adapters, plan, grad_dtype)
+        dx = dx.view(x.shape)
+        if self.groups:
+            dx, dgamma, dbeta = B.sq_group_norm_backward(dx, x, self.groups, self.gamma, self.beta,
+                                                         mean, rstd, act=self.act, dx=dx,
+                                                         grad_dtype=grad_dtype)
+        return AttentionGrads(dx, dgamma, dbeta, dA, dB)
