@@ -2,16 +2,16 @@
 // its input, straight through the activation quantizer:
 //   dx[m][k] = sum_n dy[m][n] W~[n][k],  W~[n][k] = s_w[i(k)][n] W^[n][k] / d[g(n)][k].
 //
-// Two kernels.  The first writes W~ transposed, rounded to bf16, into the
-// caller's workspace (3 N K bytes of traffic, a few percent of the product):
-// steps and divisors vary along both dimensions, so they belong to the weight,
-// and with both operands contiguous along the contracted dimension the product
-// needs no transposition.  The rounding to bf16 is one more rounding of the
-// size of dy's own and averages over the N terms.
+// Two kernels.  The first writes W~, rounded to bf16, into the caller's
+// workspace (3 N K bytes of traffic, a few percent of the product): steps and
+// divisors vary along both dimensions, so they belong to the weight.  The
+// rounding to bf16 is one more rounding of the size of dy's own and averages
+// over the N terms.
 //
 // The second is a bf16 product on the tensor cores: persistent blocks of 128 x
-// BN output tiles, TMA into a ring of shared-memory stages (64 columns of the
-// contraction, 128-byte swizzle), tcgen05.mma kind::f16 issued by one thread,
+// BN output tiles, TMA into a ring of shared-memory stages (64 terms of the
+// contraction, 128-byte swizzle; W~ as it lies, contiguous along the output:
+// an MN-major operand), tcgen05.mma kind::f16 issued by one thread,
 // fp32 sums in tensor memory, two accumulator buffers so that a tile's
 // epilogue runs under the next tile's products.
 #include <cuda.h>
@@ -26,48 +26,57 @@
 namespace sq {
 namespace {
 
-// -------------------------------------------------------------- W~ transposed
-// 64 x 64 tiles through shared memory.  wt [K][ldw], ldw >= N.
-constexpr int kTr = 64;
-__global__ void __launch_bounds__(256) dequant_transpose_kernel(
+// ------------------------------------------------------------------------- W~
+// w [N][K].  A thread has 8 neighbouring channels of kRows rows of the weight,
+// all loads under way at once; a block 256 channels of 64 rows.
+constexpr int kDeqThreads = 256, kDeqLanes = kDeqThreads / 32, kDeqRows = 8;
+__global__ void __launch_bounds__(kDeqThreads) dequant_kernel(
     const int8_t *__restrict__ wq, const float *__restrict__ s_w, const float *__restrict__ d,
-    int64_t N, int64_t K, const __grid_constant__ SegParams seg, uint16_t *__restrict__ wt,
-    int64_t ldw, int *status) {
-  __shared__ uint16_t tile[kTr][kTr + 2];  // [k][n]
-  const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kTr;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kTr;
-  // thread: 16 codes of one weight row
-  const int nr = threadIdx.x >> 2, kc = (threadIdx.x & 3) * 16;
-  const int64_t n = n0 + nr, k = k0 + kc;
-  if (n < N && k < K) {  // K % 16 == 0
-    const uint4 v = *reinterpret_cast<const uint4 *>(wq + n * K + k);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    const int g = seg.G > 1 ? seg_index(seg.off, seg.n_seg, n) : 0;
-    // input segments are at least 32 wide and aligned to 32: one for 16 codes
-    const int i = seg.S > 1 ? seg_index(seg.off, seg.n_seg, k) : 0;
-    const float s = s_w[i * N + n] * (seg.w4 ? 0.0625f : 1.0f);  // W4 operands hold 16 q
+    int64_t N, int64_t K, const __grid_constant__ SegParams seg, uint16_t *__restrict__ w,
+    int *status) {
+  grid_dependency_wait();
+  grid_dependency_launch();
+  const int64_t k = (static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31)) * 8;
+  if (k >= K) return;  // K % 16 == 0
+  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kDeqLanes * kDeqRows + (threadIdx.x >> 5);
+  // input segments are at least 32 wide and aligned to 32: one for 8 codes
+  const int i = seg.S > 1 ? seg_index(seg.off, seg.n_seg, k) : 0;
+  uint2 v[kDeqRows];
+  float s[kDeqRows];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const uint32_t byte = (w[j >> 2] >> ((j & 3) * 8)) & 0xFFu;
-      float q;
+  for (int r = 0; r < kDeqRows; ++r) {
+    const int64_t n = n0 + r * kDeqLanes;
+    if (n < N) {
+      v[r] = *reinterpret_cast<const uint2 *>(wq + n * K + k);
+      s[r] = s_w[i * N + n] * (seg.w4 ? 0.0625f : 1.0f);  // W4 operands hold 16 q
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kDeqRows; ++r) {
+    const int64_t n = n0 + r * kDeqLanes;
+    if (n >= N) break;
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t byte = ((j < 4 ? v[r].x : v[r].y) >> ((j & 3) * 8)) & 0xFFu;
       if (seg.fp8) {
         const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte),
                                                      __NV_E4M3);
-        q = __half2float(__half(h));
+        q[j] = __half2float(__half(h));
       } else {
-        q = static_cast<float>(static_cast<int8_t>(byte));
+        q[j] = static_cast<float>(static_cast<int8_t>(byte));
       }
-      q *= s;
-      if (d != nullptr) q = __fdiv_rn(q, d[g * K + k + j]);
-      const __nv_bfloat16 b = __float2bfloat16_rn(q);
-      tile[kc + j][nr] = *reinterpret_cast<const uint16_t *>(&b);
+      q[j] *= s[r];
     }
+    if (d != nullptr) {
+      const float *dg = d + (seg.G > 1 ? seg_index(seg.off, seg.n_seg, n) : 0) * K + k;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = __fdiv_rn(q[j], dg[j]);
+    }
+    if (store_ok(status, k + 8 <= K))
+      *reinterpret_cast<uint4 *>(w + n * K + k) = make_uint4(
+          bf16x2(q[0], q[1]), bf16x2(q[2], q[3]), bf16x2(q[4], q[5]), bf16x2(q[6], q[7]));
   }
-  __syncthreads();
-  const int c = threadIdx.x & 63;
-  for (int r = threadIdx.x >> 6; r < kTr; r += 4)
-    if (k0 + r < K && n0 + c < N && store_ok(status, n0 + c < ldw))
-      wt[(k0 + r) * ldw + n0 + c] = tile[r][c];
 }
 
 // -------------------------------------------------------------------- product
@@ -152,7 +161,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           uint8_t *sa = smem + stage * L::STAGE;
           mbar_arrive_expect_tx(&full[stage], L::STAGE);
           tma_load_2d(sa, &tmA, &full[stage], kb * BK, mt * BM);
-          tma_load_2d(sa + L::A, &tmB, &full[stage], kb * BK, nt * BN);
+#pragma unroll
+          for (int b = 0; b < BN / 64; ++b)
+            tma_load_2d(sa + L::A + b * 8192, &tmB, &full[stage], nt * BN + b * 64, kb * BK);
           armed |= 1u << stage;
           armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) {
@@ -168,7 +179,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16(BM, BN);
+      constexpr uint32_t idesc = idesc_bf16(BM, BN) | kIdescTransB;
       int stage = 0;
       uint32_t phase = 0, iter = 0;
       for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x, ++iter) {
@@ -183,8 +194,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint32_t sa = smem_u32(smem + stage * L::STAGE), sb = sa + L::A;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            mma_bf16_tc(acc, sdesc_kmajor_sw128(sa + kk * 32), sdesc_kmajor_sw128(sb + kk * 32),
-                        idesc, (kb | kk) != 0);
+            mma_bf16_tc(acc, sdesc_kmajor_sw128(sa + kk * 32),
+                        sdesc_mnmajor_sw128(sb + kk * 2048, 8192), idesc, (kb | kk) != 0);
           mma_commit(&empty[stage]);
           if (++stage == STAGES) {
             stage = 0;
@@ -261,13 +272,12 @@ sq_status tensor_map_2d(CUtensorMap *map, const void *ptr, int64_t inner, int64_
 }
 
 template <int BN>
-sq_status run_gemm(const InputGradRequest &r, const uint16_t *wt, int64_t ldw, int sms,
-                   cudaStream_t stream) {
+sq_status run_gemm(const InputGradRequest &r, const uint16_t *w, int sms, cudaStream_t stream) {
   using L = GemmSmem<BN>;
   static_assert(L::BYTES <= 232448, "dynamic shared memory above the per-block limit");
   CUtensorMap tmA, tmB;
   sq_status st = tensor_map_2d(&tmA, r.dy, r.N, r.M, r.lddy, BM);
-  if (st == SQ_OK) st = tensor_map_2d(&tmB, wt, r.N, r.K, ldw, BN);
+  if (st == SQ_OK) st = tensor_map_2d(&tmB, w, r.K, r.N, r.K, BK);
   if (st != SQ_OK) return st;
   GradArgs p;
   p.M = static_cast<int32_t>(r.M);
@@ -309,13 +319,21 @@ size_t input_grad_workspace_bytes(int64_t N, int64_t K) {
 }
 
 sq_status launch_input_grad(const InputGradRequest &r, cudaStream_t stream) {
-  const int64_t ldw = (r.N + 7) / 8 * 8;
-  uint16_t *wt = static_cast<uint16_t *>(r.workspace);
-  dequant_transpose_kernel<<<dim3(static_cast<unsigned>((r.K + kTr - 1) / kTr),
-                                  static_cast<unsigned>((r.N + kTr - 1) / kTr)),
-                             256, 0, stream>>>(r.wq, r.s_w, r.d, r.N, r.K, r.seg, wt, ldw,
-                                               r.status);
-  if (cudaGetLastError() != cudaSuccess) return SQ_ERR_CUDA;
+  uint16_t *w = static_cast<uint16_t *>(r.workspace);
+  constexpr int64_t kRows = kDeqLanes * kDeqRows;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((r.K + 255) / 256),
+                     static_cast<unsigned>((r.N + kRows - 1) / kRows));
+  cfg.blockDim = dim3(kDeqThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, dequant_kernel, r.wq, r.s_w, r.d, r.N, r.K, r.seg, w, r.status) !=
+      cudaSuccess)
+    return SQ_ERR_CUDA;
   const int sms = sm_count();
   // Tile width: a block's time goes with the operand rows of its tiles, 128 + BN
   // each, times the rounds of tiles (1109 x 1536 x 1536: 108 tiles of 128 columns
@@ -325,9 +343,9 @@ sq_status launch_input_grad(const InputGradRequest &r, cudaStream_t stream) {
     return (mt * ((r.K + bn - 1) / bn) + sms - 1) / sms * (BM + bn);
   };
   const int64_t c64 = cost(64), c128 = cost(128), c256 = cost(256);
-  if (c256 <= c128 && c256 <= c64) return run_gemm<256>(r, wt, ldw, sms, stream);
-  if (c128 <= c64) return run_gemm<128>(r, wt, ldw, sms, stream);
-  return run_gemm<64>(r, wt, ldw, sms, stream);
+  if (c256 <= c128 && c256 <= c64) return run_gemm<256>(r, w, sms, stream);
+  if (c128 <= c64) return run_gemm<128>(r, w, sms, stream);
+  return run_gemm<64>(r, w, sms, stream);
 }
 
 }  // namespace sq

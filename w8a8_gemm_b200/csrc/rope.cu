@@ -22,7 +22,7 @@ namespace sq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxUnits = 4;  // units a thread holds in registers at once
+constexpr int kAhead = 4;  // rows whose loads a thread has under way at once
 
 template <typename T>
 struct Vec;
@@ -84,7 +84,7 @@ __device__ __forceinline__ float2 turn(const RopeArgs &p, int64_t row, int i) {
 // place).  VEC false: pairs and columns one by one, for rotated widths that
 // are no multiple of a unit.
 template <typename T, bool HALF, bool VEC>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs p) {
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs p) {
   extern __shared__ float2 cs[];  // [rows of the block][rot / 2]
   using V = Vec<T>;
   constexpr int N = V::N;
@@ -102,71 +102,91 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs p) {
   };
 
   if constexpr (VEC) {
+    // A thread keeps its place in the row (head, unit) over several rows; where
+    // a row has fewer units than the block threads, `lanes` rows go side by side.
     const int turned = HALF ? pairs / N : p.rot / N;             // units of a head that turn
     const int per_head = turned + (in_place ? 0 : (p.D - p.rot) / N);
     const int per_row = p.H * per_head;
-    const int total = rows * per_row;
-    bool ready = false;
-    for (int u0 = threadIdx.x; u0 - static_cast<int>(threadIdx.x) < total;
-         u0 += kThreads * kMaxUnits) {
-      uint4 a[kMaxUnits], b[kMaxUnits];
-      int64_t at[kMaxUnits];   // element offset of the first vector within its row
-      int unit[kMaxUnits], r[kMaxUnits];
+    const int lanes = per_row < kThreads ? kThreads / per_row : 1;
+    const int lane = per_row < kThreads ? threadIdx.x / per_row : 0;
+    int u = per_row < kThreads ? threadIdx.x - lane * per_row : threadIdx.x;
+    int r = lane;
+    bool work = lane < lanes && u < per_row && r < rows;
+    int unit = 0;
+    int64_t at = 0;  // element offset of the unit's first vector within a row
+    uint4 a[kAhead], b[kAhead];
+    auto place = [&]() {
+      const int h = u / per_head;
+      unit = u - h * per_head;
+      at = static_cast<int64_t>(h) * p.D +
+           (unit < turned ? unit * N : p.rot + (unit - turned) * N);
+    };
+    auto load = [&]() {
 #pragma unroll
-      for (int k = 0; k < kMaxUnits; ++k) {
-        const int u = u0 + k * kThreads;
-        r[k] = -1;
-        if (u >= total) continue;
-        r[k] = u / per_row;
-        const int v = u - r[k] * per_row;
-        const int h = v / per_head;
-        unit[k] = v - h * per_head;
-        at[k] = static_cast<int64_t>(h) * p.D +
-                (unit[k] < turned ? unit[k] * N : p.rot + (unit[k] - turned) * N);
-        const T *src = x + (row0 + r[k]) * p.ldx + at[k];
-        a[k] = *reinterpret_cast<const uint4 *>(src);
-        if (HALF && unit[k] < turned) b[k] = *reinterpret_cast<const uint4 *>(src + pairs);
+      for (int q = 0; q < kAhead; ++q) {
+        if (r + q * lanes >= rows) break;
+        const T *src = x + (row0 + r + q * lanes) * p.ldx + at;
+        a[q] = *reinterpret_cast<const uint4 *>(src);
+        if (HALF && unit < turned) b[q] = *reinterpret_cast<const uint4 *>(src + pairs);
       }
-      if (!ready) {
-        angles();
-        __syncthreads();
-        ready = true;
-      }
+    };
+    if (work) {
+      place();
+      load();
+    }
+    angles();
+    __syncthreads();
+    while (work) {
 #pragma unroll
-      for (int k = 0; k < kMaxUnits; ++k) {
-        if (r[k] < 0) continue;
-        T *dst = out + (row0 + r[k]) * p.ldo + at[k];
-        const bool ok = store_ok(p.status, row0 + r[k] < p.M && at[k] + N <= p.ldo);
-        if (unit[k] >= turned) {
-          if (ok) *reinterpret_cast<uint4 *>(dst) = a[k];
+      for (int q = 0; q < kAhead; ++q) {
+        if (r + q * lanes >= rows) break;
+        const int64_t row = row0 + r + q * lanes;
+        T *dst = out + row * p.ldo + at;
+        const bool ok = store_ok(p.status, row < p.M && at + N <= p.ldo);
+        if (unit >= turned) {
+          if (ok) *reinterpret_cast<uint4 *>(dst) = a[q];
           continue;
         }
+        const float4 *w = reinterpret_cast<const float4 *>(
+            cs + (r + q * lanes) * pairs + unit * (HALF ? N : N / 2));  // two pairs each
         if constexpr (HALF) {
-          float u[N], v[N], fu[N], fv[N];
-          V::unpack(a[k], u);
-          V::unpack(b[k], v);
-          const float2 *w = cs + r[k] * pairs + unit[k] * N;
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            fu[j] = u[j] * w[j].x - v[j] * w[j].y;
-            fv[j] = u[j] * w[j].y + v[j] * w[j].x;
-          }
-          if (ok) {
-            *reinterpret_cast<uint4 *>(dst) = V::pack(fu);
-            *reinterpret_cast<uint4 *>(dst + pairs) = V::pack(fv);
-          }
-        } else {
-          float u[N], f[N];
-          V::unpack(a[k], u);
-          const float2 *w = cs + r[k] * pairs + unit[k] * (N / 2);
+          float x0[N], x1[N], f0[N], f1[N];
+          V::unpack(a[q], x0);
+          V::unpack(b[q], x1);
 #pragma unroll
           for (int j = 0; j < N; j += 2) {
-            f[j] = u[j] * w[j / 2].x - u[j + 1] * w[j / 2].y;
-            f[j + 1] = u[j] * w[j / 2].y + u[j + 1] * w[j / 2].x;
+            const float4 t = w[j / 2];
+            f0[j] = x0[j] * t.x - x1[j] * t.y;
+            f1[j] = x0[j] * t.y + x1[j] * t.x;
+            f0[j + 1] = x0[j + 1] * t.z - x1[j + 1] * t.w;
+            f1[j + 1] = x0[j + 1] * t.w + x1[j + 1] * t.z;
+          }
+          if (ok) {
+            *reinterpret_cast<uint4 *>(dst) = V::pack(f0);
+            *reinterpret_cast<uint4 *>(dst + pairs) = V::pack(f1);
+          }
+        } else {
+          float x0[N], f[N];
+          V::unpack(a[q], x0);
+#pragma unroll
+          for (int j = 0; j < N; j += 4) {
+            const float4 t = w[j / 4];
+            f[j] = x0[j] * t.x - x0[j + 1] * t.y;
+            f[j + 1] = x0[j] * t.y + x0[j + 1] * t.x;
+            f[j + 2] = x0[j + 2] * t.z - x0[j + 3] * t.w;
+            f[j + 3] = x0[j + 2] * t.w + x0[j + 3] * t.z;
           }
           if (ok) *reinterpret_cast<uint4 *>(dst) = V::pack(f);
         }
       }
+      r += kAhead * lanes;
+      if (r >= rows) {
+        r = lane;
+        u += kThreads;
+        work = per_row >= kThreads && u < per_row;
+        if (work) place();
+      }
+      if (work) load();
     }
   } else {
     angles();
@@ -197,12 +217,13 @@ template <typename T>
 cudaError_t run(RopeArgs p, bool half, cudaStream_t stream) {
   constexpr int N = Vec<T>::N;
   const bool vec = p.rot % (half ? 2 * N : N) == 0;
-  // Rows of a block: enough for every thread to have an angle to form and two
-  // units to turn, with at most 32 KB of cosines and sines, but no more than
+  // Rows of a block: enough for every thread to have an angle to form and its
+  // loads under way, with at most 32 KB of cosines and sines, but no more than
   // leave every SM four blocks.
   const int64_t units = static_cast<int64_t>(p.H) * p.D / (vec && half ? 2 * N : N);
   int64_t rows = kThreads / (p.rot / 2);
-  if (rows * units < 2 * kThreads) rows = 2 * kThreads / units;
+  const int64_t ahead = units < kThreads ? kAhead * (kThreads / units) : kAhead;
+  if (rows < ahead) rows = ahead;
   const int64_t most = 32768 / (static_cast<int64_t>(p.rot / 2) * 8);
   if (rows > most) rows = most;
   if (rows > p.M / (4 * 148)) rows = p.M / (4 * 148);
