@@ -8,12 +8,16 @@
 // rounding to bf16 is one more rounding of the size of dy's own and averages
 // over the N terms.
 //
-// The second is a bf16 product on the tensor cores: persistent blocks of 128 x
-// BN output tiles, TMA into a ring of shared-memory stages (64 terms of the
-// contraction, 128-byte swizzle; W~ as it lies, contiguous along the output:
-// an MN-major operand), tcgen05.mma kind::f16 issued by one thread,
-// fp32 sums in tensor memory, two accumulator buffers so that a tile's
-// epilogue runs under the next tile's products.
+// The second is a bf16 product on the tensor cores: persistent pairs of blocks,
+// each pair 256 x BN output tiles of one tcgen05.mma kind::f16, cta_group::2.
+// A block fetches 128 rows of dy and BN / 2 columns of W~ a step (64 terms of
+// the contraction) by TMA into a ring of stages, 128-byte swizzled; W~ lies
+// contiguous along the output, an MN-major operand.  The sums are fp32 in tensor
+// memory, in two buffers, so that a tile's epilogue runs under the next tile's
+// products.  What bounds it is the way of the operands from L2 to an SM, about
+// 61 bytes a clock: one block by itself with 128 x 256 tiles fetches 48 KB for
+// 512 clocks of products, a pair 32 KB a block.
+#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -23,13 +27,16 @@
 #include "bf16.cuh"
 #include "sq_internal.h"
 
+namespace cg = cooperative_groups;
+
 namespace sq {
 namespace {
 
 // ------------------------------------------------------------------------- W~
-// w [N][K].  A thread has 8 neighbouring channels of kRows rows of the weight,
-// all loads under way at once; a block 256 channels of 64 rows.
-constexpr int kDeqThreads = 256, kDeqLanes = kDeqThreads / 32, kDeqRows = 8;
+// w [N][K].  A thread has 8 neighbouring channels of kDeqRows rows of the weight,
+// all loads under way at once; a block 256 channels of 16 rows (64 rows left too few
+// blocks to hide the divisions: 1536 x 1536 with divisors took 11.5 us).
+constexpr int kDeqThreads = 256, kDeqLanes = kDeqThreads / 32, kDeqRows = 2;
 __global__ void __launch_bounds__(kDeqThreads) dequant_kernel(
     const int8_t *__restrict__ wq, const float *__restrict__ s_w, const float *__restrict__ d,
     int64_t N, int64_t K, const __grid_constant__ SegParams seg, uint16_t *__restrict__ w,
@@ -80,15 +87,15 @@ __global__ void __launch_bounds__(kDeqThreads) dequant_kernel(
 }
 
 // -------------------------------------------------------------------- product
-constexpr int BM = 128, BK = 64;
+constexpr int BM = 128, BK = 64;  // rows of a block, terms of a step
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
 
 template <int BN>
 struct GemmSmem {
-  static constexpr int A = BM * BK * 2, B = BN * BK * 2;
+  static constexpr int A = BM * BK * 2, B = BN / 2 * BK * 2;
   static constexpr int STAGE = A + B;
-  static constexpr int STAGES = BN == 256 ? 4 : 6;
+  static constexpr int STAGES = BN == 256 ? 6 : 8;
   static constexpr int BARS = STAGES * STAGE;
   static constexpr int BYTES = BARS + (2 * STAGES + 5) * 8 + 16 + 1024;
 };
@@ -106,6 +113,9 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatil
   return bounded_wait(bar, parity, abort_flag, status, SQ_ERR_DEVICE_TIMEOUT);
 }
 
+// Barriers: `full` (both blocks' copies) and `acc_empty` (both blocks' epilogues)
+// count in the even block, which issues the products; `empty` and `acc_full`
+// are committed to in both.
 template <int BN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     input_grad_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -114,6 +124,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   constexpr int STAGES = L::STAGES;
   constexpr int COLS = 2 * BN;  // two accumulator buffers
   extern __shared__ uint8_t smem_raw[];
+  // the same offset in both blocks: the window starts at the same address
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::BARS);
@@ -124,6 +135,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  cg::cluster_group cluster = cg::this_cluster();
+  const uint32_t rank = cluster.block_rank();  // block of the pair
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -132,7 +146,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], kEpiWarps);
+      mbar_init(&acc_empty[b], 2 * kEpiWarps);
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
@@ -141,11 +155,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     prefetch_tmap(&tmB);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, COLS);
-    tmem_relinquish();
+    tmem_alloc_pair(tmem_slot, COLS);
+    tmem_relinquish_pair();
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster.sync();  // both blocks' barriers and columns stand
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   grid_dependency_wait();  // the prologue above touches no global memory
@@ -154,16 +169,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_parity = 0;
-      for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x) {
-        const int mt = tile / p.num_n_tiles, nt = tile % p.num_n_tiles;
+      bool gave_up = false;
+      for (int tile = first; tile < p.num_tiles; tile += step) {
+        const int row = (tile / p.num_n_tiles * 2 + rank) * BM;
+        const int col = tile % p.num_n_tiles * BN + rank * (BN / 2);
         for (int kb = 0; kb < p.num_kb; ++kb) {
-          if (!wait_bar(&empty[stage], phase ^ 1, abort_flag, p.status)) goto producer_done;
+          if (!wait_bar(&empty[stage], phase ^ 1, abort_flag, p.status)) {
+            gave_up = true;
+            goto producer_done;
+          }
           uint8_t *sa = smem + stage * L::STAGE;
-          mbar_arrive_expect_tx(&full[stage], L::STAGE);
-          tma_load_2d(sa, &tmA, &full[stage], kb * BK, mt * BM);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * L::STAGE);
+          const uint32_t bar = cluster_addr(&full[stage], 0);
+          tma_load_2d_pair(sa, &tmA, bar, kb * BK, row);
 #pragma unroll
-          for (int b = 0; b < BN / 64; ++b)
-            tma_load_2d(sa + L::A + b * 8192, &tmB, &full[stage], nt * BN + b * 64, kb * BK);
+          for (int b = 0; b < BN / 128; ++b)
+            tma_load_2d_pair(sa + L::A + b * 8192, &tmB, bar, col + b * 64, kb * BK);
           armed |= 1u << stage;
           armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) {
@@ -173,19 +194,33 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
     producer_done:
-      // never leave with a copy in flight into this block's shared memory
-      for (int s = 0; s < STAGES; ++s)
-        if (armed & (1u << s)) mbar_wait(&full[s], (armed_parity >> s) & 1u, kBoundedWaitNs);
+      // Never leave with a copy, or a product's arrival, under way into this
+      // block's shared memory.  After a wait that ran out, the even block's
+      // barriers tell of the copies of both; the odd block gives its own, which
+      // have had that wait's seconds, a little more.
+      for (int s = 0; s < STAGES; ++s) {
+        const uint32_t parity = (armed_parity >> s) & 1u;
+        if (!(armed & (1u << s))) continue;
+        if (!gave_up && wait_bar(&empty[s], parity, abort_flag, p.status)) continue;
+        gave_up = true;
+        if (rank == 0) mbar_wait(&full[s], parity, kBoundedWaitNs);
+      }
+      if (gave_up && rank == 1) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < kBoundedWaitNs / 1000) {
+        }
+      }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16(BM, BN) | kIdescTransB;
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16(2 * BM, BN) | kIdescTransB;
       int stage = 0;
       uint32_t phase = 0, iter = 0;
-      for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x, ++iter) {
+      for (int tile = first; tile < p.num_tiles; tile += step, ++iter) {
         const uint32_t buf = iter & 1;
         if (!wait_bar(&acc_empty[buf], ((iter >> 1) & 1) ^ 1, abort_flag, p.status))
           goto mma_exit;
+        fence_cluster();  // the other block's reads of this buffer come before
         tc_fence_after();
         const uint32_t acc = tmem_base + buf * BN;
         for (int kb = 0; kb < p.num_kb; ++kb) {
@@ -194,30 +229,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint32_t sa = smem_u32(smem + stage * L::STAGE), sb = sa + L::A;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            mma_bf16_tc(acc, sdesc_kmajor_sw128(sa + kk * 32),
-                        sdesc_mnmajor_sw128(sb + kk * 2048, 8192), idesc, (kb | kk) != 0);
-          mma_commit(&empty[stage]);
+            mma_bf16_pair(acc, sdesc_kmajor_sw128(sa + kk * 32),
+                          sdesc_mnmajor_sw128(sb + kk * 2048, 8192), idesc, (kb | kk) != 0);
+          mma_commit_pair(&empty[stage]);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
           }
         }
-        mma_commit(&acc_full[buf]);
+        mma_commit_pair(&acc_full[buf]);
       }
     mma_exit:
-      mma_commit(mma_done);
+      mma_commit_pair_here(mma_done);
       mbar_wait(mma_done, 0, kBoundedWaitNs);
     }
   } else {
     const int quarter = warp & 3;         // TMEM lanes this warp may read
     const int half = (warp - 2) >> 2;     // which half of the columns
     uint32_t iter = 0;
-    for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x, ++iter) {
+    for (int tile = first; tile < p.num_tiles; tile += step, ++iter) {
       const uint32_t buf = iter & 1;
       if (!wait_bar(&acc_full[buf], (iter >> 1) & 1, abort_flag, p.status)) break;
       tc_fence_after();
-      const int mt = tile / p.num_n_tiles, nt = tile % p.num_n_tiles;
-      const int row = mt * BM + quarter * 32 + lane;
+      const int row = (tile / p.num_n_tiles * 2 + rank) * BM + quarter * 32 + lane;
+      const int nt = tile % p.num_n_tiles;
       const uint32_t src = tmem_base + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
       for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
@@ -242,16 +277,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
     }
   }
 
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster.sync();  // no products and no arrivals under way in either block
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem_base, COLS);
+    tmem_dealloc_pair(tmem_base, COLS);
   }
 }
 
@@ -283,7 +319,7 @@ sq_status run_gemm(const InputGradRequest &r, const uint16_t *w, int sms, cudaSt
   p.M = static_cast<int32_t>(r.M);
   p.K = static_cast<int32_t>(r.K);
   p.num_n_tiles = static_cast<int32_t>((r.K + BN - 1) / BN);
-  p.num_tiles = static_cast<int32_t>((r.M + BM - 1) / BM) * p.num_n_tiles;
+  p.num_tiles = static_cast<int32_t>((r.M + 2 * BM - 1) / (2 * BM)) * p.num_n_tiles;
   p.num_kb = static_cast<int32_t>((r.N + BK - 1) / BK);
   p.dx = r.dx;
   p.lddx = r.lddx;
@@ -298,15 +334,18 @@ sq_status run_gemm(const InputGradRequest &r, const uint16_t *w, int sms, cudaSt
     attr_set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.num_tiles < sms ? p.num_tiles : sms);
+  cfg.gridDim = dim3(2 * (p.num_tiles < sms / 2 ? p.num_tiles : sms / 2));
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = L::BYTES;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, input_grad_kernel<BN>, tmA, tmB, p) != cudaSuccess)
     return SQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? SQ_OK : SQ_ERR_CUDA;
@@ -335,17 +374,14 @@ sq_status launch_input_grad(const InputGradRequest &r, cudaStream_t stream) {
       cudaSuccess)
     return SQ_ERR_CUDA;
   const int sms = sm_count();
-  // Tile width: a block's time goes with the operand rows of its tiles, 128 + BN
-  // each, times the rounds of tiles (1109 x 1536 x 1536: 108 tiles of 128 columns
-  // in one round beat 216 of 64 in two, 12 us against 20).
-  const int64_t mt = (r.M + BM - 1) / BM;
+  // Tile width: a block's time goes with the operand rows that it fetches, 128 +
+  // BN / 2 a step, times the rounds of tiles.
+  const int64_t mt = (r.M + 2 * BM - 1) / (2 * BM);
   auto cost = [&](int64_t bn) {
-    return (mt * ((r.K + bn - 1) / bn) + sms - 1) / sms * (BM + bn);
+    return (mt * ((r.K + bn - 1) / bn) + sms / 2 - 1) / (sms / 2) * (BM + bn / 2);
   };
-  const int64_t c64 = cost(64), c128 = cost(128), c256 = cost(256);
-  if (c256 <= c128 && c256 <= c64) return run_gemm<256>(r, w, sms, stream);
-  if (c128 <= c64) return run_gemm<128>(r, w, sms, stream);
-  return run_gemm<64>(r, w, sms, stream);
+  return cost(256) <= cost(128) ? run_gemm<256>(r, w, sms, stream)
+                                : run_gemm<128>(r, w, sms, stream);
 }
 
 }  // namespace sq
