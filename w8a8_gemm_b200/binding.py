@@ -94,14 +94,20 @@ class Segments:
         return self.n_seg if self.mode == SQ_SEG_INPUT else 1
 
     def _c(self):
-        if self.offsets is None:
-            arr = None
-            ptr = ctypes.POINTER(ctypes.c_int32)()
-        else:
-            arr = (ctypes.c_int32 * len(self.offsets))(*[int(v) for v in self.offsets])
-            ptr = ctypes.cast(arr, ctypes.POINTER(ctypes.c_int32))
-        s = _Segments(self.mode, self.n_seg, ptr, self.n_groups, self.flags)
-        return s, arr  # keep the array alive for the call
+        return _c_segments(self.mode, None if self.offsets is None else tuple(self.offsets),
+                           self.n_groups, self.flags)
+
+
+@functools.lru_cache(maxsize=256)
+def _c_segments(mode, offsets, n_groups, flags):
+    """The C form of a segment table (the calls only read it) and its array, which
+    lives as long as it."""
+    if offsets is None:
+        arr, n_seg, ptr = None, 1, ctypes.POINTER(ctypes.c_int32)()
+    else:
+        arr = (ctypes.c_int32 * len(offsets))(*[int(v) for v in offsets])
+        n_seg, ptr = len(offsets) - 1, ctypes.cast(arr, ctypes.POINTER(ctypes.c_int32))
+    return _Segments(mode, n_seg, ptr, n_groups, flags), arr
 
 
 _lib = None
@@ -529,6 +535,7 @@ def sq_dualscale_seglinear_host_noalloc(x_host: torch.Tensor, d: Optional[torch.
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 _OUT = {_BF16: SQ_OUT_BF16, _F32: SQ_OUT_F32}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _explain(name: str, t, dtype, shape, dev: int, contiguous: bool):
@@ -577,14 +584,16 @@ def _rows_of(name: str, t, dtype):
     """(rows, columns, device) of the tensor that gives a call its sizes."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _explain(name, t, dtype, (), -1, False)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions")
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"{name} is on cuda:{dev}, not on the current device")
-    return t.shape[0], t.shape[1], dev
+    try:
+        rows, cols = t.shape
+    except ValueError:
+        raise ValueError(f"{name} must have two dimensions") from None
+    return rows, cols, dev
 
 
 def _out_dtype(dtype, name: str) -> int:
@@ -754,16 +763,15 @@ def _int_array(values: tuple):
 
 
 def _rope(call: str, x, positions, inv_freq, head_dim, out, layout, axis_pairs, factor):
-    if not isinstance(x, torch.Tensor):
+    kind = getattr(x, "dtype", None)
+    if kind is None:
         raise ValueError("x must be a tensor")
-    kind = x.dtype
     dtype = _out_dtype(kind, "x")
     M, cols, dev = _rows_of("x", x, kind)
     if head_dim < 1 or cols % head_dim != 0:
         raise ValueError(f"{cols} columns are no whole number of heads of {head_dim}")
     axes = 1 if axis_pairs is None else len(axis_pairs)
-    if axes == 1 and positions.dim() == 1:
-        positions = positions[:, None]
+    flat = axes == 1 and isinstance(positions, torch.Tensor) and positions.dim() == 1
     pairs = inv_freq.numel()
     if out is None:
         out = torch.empty(M, cols, dtype=kind, device=dev)
@@ -772,7 +780,8 @@ def _rope(call: str, x, positions, inv_freq, head_dim, out, layout, axis_pairs, 
     if px == po and M == 1:
         ldo = ldx
     _check(getattr(lib(), call)(px, ldx, po, ldo, dtype,
-                                _whole("positions", positions, _I32, (M, axes), dev),
+                                _whole("positions", positions, _I32, (M,) if flat else (M, axes),
+                                       dev),
                                 _whole("inv_freq", inv_freq, _F32, (pairs,), dev),
                                 None if axis_pairs is None else _int_array(tuple(axis_pairs)),
                                 axes, factor, M, cols // head_dim, head_dim, 2 * pairs, layout,
@@ -830,7 +839,7 @@ def _gn_sizes(x):
     if x.dim() != 3:
         raise ValueError("x must be [B, S, C]")
     dev = x.get_device()
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"x is on cuda:{dev}, not on the current device")
     return (*x.shape, dev)
 
