@@ -272,7 +272,10 @@ struct ContractArgs {
   int *status;
 };
 
-constexpr int kContractThreads = 128;
+// Warps: 0 TMA, 1 products, 4 .. 7 copies of scattered rows (one warp by itself
+// takes 128 clocks a copy instruction: 1501 rows of 1536 took 19 us); all of them
+// store.
+constexpr int kContractThreads = 256, kCopyWarps = 4;
 
 template <int RT>
 struct ContractSmem {
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(kContractThreads)
   const bool run = tile.w != 0;  // neighbouring rows
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], run ? 1 : 2);
+      mbar_init(&full[s], run ? 1 : 1 + kCopyWarps);
       mbar_init(&empty[s], 1);
     }
     mbar_init(done, 1);
@@ -347,58 +350,33 @@ __global__ void __launch_bounds__(kContractThreads)
       // ---------------------------------------------------------- producer
       // Rows past the tile's last are the next ones of a box, or left out:
       // what stands there only meets sums that are not stored.
-      const int first = rec[4];
-      int32_t rows[kTileRows / 4];  // scattered: this lane copies rows 4 i + lane / 8
+      if (lane == 0) {
+        const int first = rec[4];
+        const uint32_t bytes = (run ? S::kIn : 0) + S::kW;
+        uint32_t armed = 0, armed_parity = 0;
+        for (int step = 0; step < steps; ++step) {
+          const int st = step % STAGES;
+          const uint32_t phase = (step / STAGES) & 1;
+          uint8_t *in = smem + st * S::kStage;
+          const int c0 = c_lo + step * 64;
+          if (!bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT))
+            break;
+          mbar_arrive_expect_tx(&full[st], bytes);
+          if (run) tma_load_2d(in, &tm_in, &full[st], c0, first);
+          if constexpr (!TRANS) {
+            tma_load_3d(in + S::kIn, &tm_w, &full[st], c0, 0, bin);
+          } else {
 #pragma unroll
-      for (int i = 0; i < kTileRows / 4; ++i) rows[i] = run ? 0 : rec[4 + i * 4 + (lane >> 3)];
-      const uint32_t bytes = (run ? S::kIn : 0) + S::kW;
-      uint32_t armed = 0, armed_parity = 0;
-      LateArrival late;
-      for (int step = 0; step < steps; ++step) {
-        const int st = step % STAGES;
-        const uint32_t phase = (step / STAGES) & 1;
-        bool ok = true;
-        uint8_t *in = smem + st * S::kStage;
-        const int c0 = c_lo + step * 64;
-        late.before_wait(lane, &empty[st], phase ^ 1);
-        if (lane == 0) {
-          ok = bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
-          if (ok) {
-            mbar_arrive_expect_tx(&full[st], bytes);
-            if (run) tma_load_2d(in, &tm_in, &full[st], c0, first);
-            if constexpr (!TRANS) {
-              tma_load_3d(in + S::kIn, &tm_w, &full[st], c0, 0, bin);
-            } else {
-#pragma unroll
-              for (int h = 0; h < RT / 64; ++h)
-                tma_load_3d(in + S::kIn + h * 8192, &tm_w, &full[st], h * 64, c0, bin);
-            }
-            armed |= 1u << st;
-            armed_parity = (armed_parity & ~(1u << st)) | (phase << st);
+            for (int h = 0; h < RT / 64; ++h)
+              tma_load_3d(in + S::kIn + h * 8192, &tm_w, &full[st], h * 64, c0, bin);
           }
+          armed |= 1u << st;
+          armed_parity = (armed_parity & ~(1u << st)) | (phase << st);
         }
-        if (!__shfl_sync(~0u, ok, 0)) break;
-        if (!run) {
-          const int c = lane & 7, col = c0 + c * 8;
-          const bool in_cols = col < p.C;
-          const uint32_t to = smem_u32(in);
-#pragma unroll
-          for (int i = 0; i < kTileRows / 4; ++i) {
-            if (i * 4 >= count) break;
-            const int r = i * 4 + (lane >> 3);
-            if (r < count)
-              cp_async16(to + swz128(r, c), p.in + rows[i] * p.ld + (in_cols ? col : 0), in_cols);
-          }
-          cp_async_commit();
-          late.push(lane, &full[st]);
-        }
-      }
-      late.catch_up(lane);
-      // never leave with a copy in flight into this block's shared memory
-      cp_async_wait<0>();
-      if (lane == 0)
+        // never leave with a copy in flight into this block's shared memory
         for (int s = 0; s < STAGES; ++s)
           if (armed & (1u << s)) mbar_wait(&full[s], (armed_parity >> s) & 1u, kBoundedWaitNs);
+      }
       __syncwarp();
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
@@ -422,6 +400,36 @@ __global__ void __launch_bounds__(kContractThreads)
         mma_commit(done);
       }
       __syncwarp();
+    } else if (warp >= 4 && !run) {
+      // ------------------------------------------------- scattered rows: copies
+      // This warp's 32 rows, four a copy instruction.
+      const int first = (warp - 4) * 32, c = lane & 7;
+      int32_t rows[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rows[i] = rec[4 + first + i * 4 + (lane >> 3)];
+      LateArrival late;
+      for (int step = 0; step < steps; ++step) {
+        const int st = step % STAGES;
+        const uint32_t phase = (step / STAGES) & 1;
+        late.before_wait(lane, &empty[st], phase ^ 1);
+        bool ok = true;
+        if (lane == 0)
+          ok = bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
+        if (!__shfl_sync(~0u, ok, 0)) break;
+        const int col = c_lo + step * 64 + c * 8;
+        const bool in_cols = col < p.C;
+        const uint32_t to = smem_u32(smem + st * S::kStage);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = first + i * 4 + (lane >> 3);
+          if (r < count)
+            cp_async16(to + swz128(r, c), p.in + rows[i] * p.ld + (in_cols ? col : 0), in_cols);
+        }
+        cp_async_commit();
+        late.push(lane, &full[st]);
+      }
+      late.catch_up(lane);
+      cp_async_wait<0>();
     }
     const bool ok = bounded_wait(done, 0, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
     tc_fence_after();
@@ -431,13 +439,15 @@ __global__ void __launch_bounds__(kContractThreads)
     // partial sums -> shared memory -> sum over the slices
     float *part = reinterpret_cast<float *>(smem);
     constexpr int PS = S::kPartRow;
+    const int quarter = warp & 3;  // TMEM lanes this warp may read
 #pragma unroll
-    for (int c = 0; c < RT; c += 32) {
+    for (int c0 = 0; c0 < RT / 2; c0 += 32) {
+      const int c = (warp >> 2) * (RT / 2) + c0;
       uint32_t r[32];
       __syncwarp();
-      tmem_ld_32x32b_x32(tmem + c + (static_cast<uint32_t>(warp * 32) << 16), r);
+      tmem_ld_32x32b_x32(tmem + c + (static_cast<uint32_t>(quarter * 32) << 16), r);
       tmem_ld_wait();
-      float *to = part + threadIdx.x * PS + c;
+      float *to = part + (quarter * 32 + lane) * PS + c;
 #pragma unroll
       for (int j = 0; j < 32; j += 4)
         *reinterpret_cast<uint4 *>(to + j) =
