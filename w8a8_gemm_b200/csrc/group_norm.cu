@@ -31,7 +31,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 8;  // rows of one step of the statistics
-constexpr int kAhead = 4;  // rows whose loads a thread has under way elsewhere
+constexpr int kAhead = 4;  // rows whose loads a thread has under way in the backward pass
 
 __device__ __forceinline__ uint4 load8(const uint16_t *p) {
   return *reinterpret_cast<const uint4 *>(p);
@@ -237,10 +237,20 @@ __global__ void __launch_bounds__(kThreads) gn_stats_kernel(const GroupNormArgs 
     st.clear();
     const uint16_t *src = x + o * 8;
     int r = lane;
-    for (; r + (kBatch - 1) * sp.lanes < rows; r += sp.lanes * kBatch) {
-      uint4 v[kBatch];
+    uint4 v[kBatch], next[kBatch];  // a batch's loads run under the one before
+    const int step = sp.lanes * kBatch, span = (kBatch - 1) * sp.lanes;
+    if (r + span < rows) {
 #pragma unroll
-      for (int q = 0; q < kBatch; ++q) v[q] = load8(src + (r + q * sp.lanes) * p.ldx);
+      for (int q = 0; q < kBatch; ++q) next[q] = load8(src + (r + q * sp.lanes) * p.ldx);
+    }
+    for (; r + span < rows; r += step) {
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) v[q] = next[q];
+      if (r + step + span < rows) {
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+          next[q] = load8(src + (r + step + q * sp.lanes) * p.ldx);
+      }
       st.batch(v);
     }
     for (; r < rows; r += sp.lanes) st.row(load8(src + r * p.ldx));
@@ -312,12 +322,27 @@ __device__ __forceinline__ void join_stats(const GroupNormArgs &p, int b, float2
   __syncthreads();
 }
 
+// A thread's first rows are under way before the statistics are there: x was
+// complete before the statistics' kernel began to read it.
 template <int ACT>
-__global__ void __launch_bounds__(kThreads, 4) gn_apply_kernel(const GroupNormArgs p) {
+__global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(const GroupNormArgs p) {
   extern __shared__ float2 sh[];  // [G] {mean, rstd}
   __shared__ double2 sums[kThreads];
-  grid_dependency_wait();
   const int b = blockIdx.y;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows2;
+  const int rows = p.S - r0 < p.rows2 ? static_cast<int>(p.S - r0) : p.rows2;
+  const Split sp = split_of(p.C);
+  const int lane = threadIdx.x / sp.oct, oct = threadIdx.x % sp.oct;
+  const int64_t row0 = static_cast<int64_t>(b) * p.S + r0;
+  uint4 v[kBatch];
+  auto load = [&](int r, int c0) {
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q)
+      if (r + q * sp.lanes < rows) v[q] = load8(p.x + (row0 + r + q * sp.lanes) * p.ldx + c0);
+  };
+  bool loaded = lane < sp.lanes;
+  if (loaded) load(lane, oct * 8);
+  grid_dependency_wait();
   join_stats(p, b, sh, sums);
   if (blockIdx.x == 0)
     for (int g = threadIdx.x; g < p.G; g += kThreads)
@@ -325,45 +350,37 @@ __global__ void __launch_bounds__(kThreads, 4) gn_apply_kernel(const GroupNormAr
         p.mean[b * p.G + g] = sh[g].x;
         p.rstd[b * p.G + g] = sh[g].y;
       }
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows2;
-  const int rows = p.S - r0 < p.rows2 ? static_cast<int>(p.S - r0) : p.rows2;
-  const Split sp = split_of(p.C);
-  const int lane = threadIdx.x / sp.oct, oct = threadIdx.x % sp.oct;
   if (lane >= sp.lanes) return;
   const int cg = p.C / p.G;
-  const int64_t row0 = static_cast<int64_t>(b) * p.S + r0;
   for (int o = oct; o < p.C / 8; o += sp.oct) {
     const int c0 = o * 8;
-    F2 minus_mean[4], scale[4], shift[4];
+    // x scale + shift: the one rounding of mean scale is 2^-15 of the step of x's
+    // own bf16 grid near its mean
+    F2 scale[4], shift[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float m[2], k[2], t[2];
+      float k[2], t[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int c = c0 + 2 * j + e;
-        const float2 v = sh[c / cg];
-        m[e] = -v.x;
-        k[e] = v.y * (p.gamma ? bf16_lo(p.gamma[c]) : 1.0f);
-        t[e] = p.beta ? bf16_lo(p.beta[c]) : 0.0f;
+        const float2 st = sh[c / cg];
+        k[e] = st.y * (p.gamma ? bf16_lo(p.gamma[c]) : 1.0f);
+        t[e] = fmaf(-st.x, k[e], p.beta ? bf16_lo(p.beta[c]) : 0.0f);
       }
-      minus_mean[j] = f2(m[0], m[1]);
       scale[j] = f2(k[0], k[1]);
       shift[j] = f2(t[0], t[1]);
     }
-    for (int r = lane; r < rows; r += sp.lanes * kAhead) {
-      uint4 v[kAhead];
+    for (int r = lane; r < rows; r += sp.lanes * kBatch) {
+      if (!loaded) load(r, c0);
+      loaded = false;
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q)
-        if (r + q * sp.lanes < rows) v[q] = load8(p.x + (row0 + r + q * sp.lanes) * p.ldx + c0);
-#pragma unroll
-      for (int q = 0; q < kAhead; ++q) {
+      for (int q = 0; q < kBatch; ++q) {
         if (r + q * sp.lanes >= rows) break;
         const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
         uint32_t y[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 z =
-              f2_get(f2_fma(f2_add(f2_of_bf16(w[j]), minus_mean[j]), scale[j], shift[j]));
+          const float2 z = f2_get(f2_fma(f2_of_bf16(w[j]), scale[j], shift[j]));
           y[j] = bf16x2(act<ACT>(z.x), act<ACT>(z.y));
         }
         const int64_t row = row0 + r + q * sp.lanes;
@@ -500,8 +517,8 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs
   extern __shared__ float2 sh[];
   __shared__ double2 sums[kThreads];
   const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
-  grid_dependency_wait();
   if (static_cast<int>(blockIdx.x) < p.grad_blocks) {
+    grid_dependency_wait();
     const int c = blockIdx.x * 32 + ln;
     double s = 0.0, sx = 0.0;
     if (c < p.C) {
@@ -526,6 +543,30 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs
   const int blk = blockIdx.x - p.grad_blocks;
   const int b = blk / p.chunks2, chunk = blk % p.chunks2;
   const int cg = p.C / p.G;
+  const int64_t r0 = static_cast<int64_t>(chunk) * p.rows2;
+  const int rows = p.S - r0 < p.rows2 ? static_cast<int>(p.S - r0) : p.rows2;
+  const Split sp = split_of(p.C);
+  const int lane = threadIdx.x / sp.oct, oct = threadIdx.x % sp.oct;
+  const int64_t row0 = static_cast<int64_t>(b) * p.S + r0;
+  // The first rows and values of the channels come before the sums: they were
+  // complete before the sums' kernel began to read them.
+  uint4 vx[kAhead], vd[kAhead];
+  Octet ch;
+  auto load = [&](int r, int c0) {
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+      if (r + q * sp.lanes < rows) {
+        const int64_t row = row0 + r + q * sp.lanes;
+        vx[q] = load8(p.x + row * p.ldx + c0);
+        vd[q] = load8(p.dy + row * p.lddy + c0);
+      }
+  };
+  bool loaded = lane < sp.lanes;
+  if (loaded) {
+    load(lane, oct * 8);
+    ch.load(p, b, oct * 8, cg);
+  }
+  grid_dependency_wait();
   const double n = static_cast<double>(p.S) * cg;
   // group sums over -n
   for (int g0 = 0; g0 < p.G; g0 += kThreads) {
@@ -537,16 +578,10 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs
                                          static_cast<float>(-sums[threadIdx.x].y / n));
   }
   __syncthreads();
-  const int64_t r0 = static_cast<int64_t>(chunk) * p.rows2;
-  const int rows = p.S - r0 < p.rows2 ? static_cast<int>(p.S - r0) : p.rows2;
-  const Split sp = split_of(p.C);
-  const int lane = threadIdx.x / sp.oct, oct = threadIdx.x % sp.oct;
   if (lane >= sp.lanes) return;
-  const int64_t row0 = static_cast<int64_t>(b) * p.S + r0;
   for (int o = oct; o < p.C / 8; o += sp.oct) {
     const int c0 = o * 8;
-    Octet ch;
-    ch.load(p, b, c0, cg);
+    if (o != oct) ch.load(p, b, c0, cg);
     F2 m1[4], m2[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -555,14 +590,8 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs
       m2[j] = f2(s.y, t.y);
     }
     for (int r = lane; r < rows; r += sp.lanes * kAhead) {
-      uint4 vx[kAhead], vd[kAhead];
-#pragma unroll
-      for (int q = 0; q < kAhead; ++q)
-        if (r + q * sp.lanes < rows) {
-          const int64_t row = row0 + r + q * sp.lanes;
-          vx[q] = load8(p.x + row * p.ldx + c0);
-          vd[q] = load8(p.dy + row * p.lddy + c0);
-        }
+      if (!loaded) load(r, c0);
+      loaded = false;
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         if (r + q * sp.lanes >= rows) break;
@@ -573,8 +602,8 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs
         for (int j = 0; j < 4; ++j) {
           F2 xh, dv;
           ch.at<ACT>(x[j], d[j], j, xh, dv);
-          const float2 z = f2_get(f2_mul(
-              ch.rstd[j], f2_add(f2_fma(dv, ch.gamma[j], m1[j]), f2_mul(xh, m2[j]))));
+          const float2 z =
+              f2_get(f2_mul(ch.rstd[j], f2_fma(xh, m2[j], f2_fma(dv, ch.gamma[j], m1[j]))));
           y[j] = bf16x2(z.x, z.y);
         }
         const int64_t row = row0 + r + q * sp.lanes;
@@ -634,13 +663,13 @@ cudaError_t launch(dim3 grid, size_t smem, size_t max_smem, const GroupNormArgs 
 constexpr size_t kMaxLaneSmem = kGroupNormMaxC * 2 * sizeof(float2);
 constexpr size_t kMaxGroupSmem = kGroupNormMaxG * sizeof(float2);
 
-void fill_chunks(GroupNormArgs &p) {
+void fill_chunks(GroupNormArgs &p, int blocks2) {
   p.rows_per_chunk = static_cast<int32_t>(chunk_rows(p.B, p.S, p.C));
   p.chunks = static_cast<int32_t>((p.S + p.rows_per_chunk - 1) / p.rows_per_chunk);
-  // Rows of a block of the second kernel: four blocks per SM, whose joins and
-  // loads hide one another.
-  const int64_t want = (4 * 148 + p.B - 1) / p.B;
-  const int64_t least = static_cast<int64_t>(split_of(p.C).lanes) * kAhead;
+  // Rows of a block of the second kernel: the blocks that an SM holds at once
+  // (three forward, two backward), in one round.
+  const int64_t want = (blocks2 * 148 + p.B - 1) / p.B;
+  const int64_t least = split_of(p.C).lanes;
   const int64_t rows = (p.S + want - 1) / want;
   p.rows2 = static_cast<int32_t>((rows + least - 1) / least * least);
   p.chunks2 = static_cast<int32_t>((p.S + p.rows2 - 1) / p.rows2);
@@ -679,7 +708,7 @@ size_t group_norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G) {
 
 cudaError_t launch_group_norm_forward(GroupNormArgs p, void *workspace, int act,
                                       cudaStream_t stream) {
-  fill_chunks(p);
+  fill_chunks(p, 3);
   p.part = static_cast<float2 *>(workspace);
   if (act == SQ_ACT_SILU) return run_forward<SQ_ACT_SILU>(p, stream);
   if (act == SQ_ACT_GELU) return run_forward<SQ_ACT_GELU>(p, stream);
@@ -688,7 +717,7 @@ cudaError_t launch_group_norm_forward(GroupNormArgs p, void *workspace, int act,
 
 cudaError_t launch_group_norm_backward(GroupNormArgs p, void *workspace, int act, bool gf32,
                                        cudaStream_t stream) {
-  fill_chunks(p);
+  fill_chunks(p, 2);
   p.part = static_cast<float2 *>(workspace);
   p.chan_part = p.part + static_cast<int64_t>(p.B) * p.chunks * p.G;
   if (act == SQ_ACT_SILU) return run_backward<SQ_ACT_SILU>(p, gf32, stream);
