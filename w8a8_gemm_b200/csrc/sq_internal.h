@@ -155,7 +155,7 @@ struct GroupNormArgs {
   int32_t B, C, G;
   float eps;
   // set by the launcher
-  int32_t rows_per_chunk, chunks, rows2, chunks2, grad_blocks;
+  int32_t rows_per_chunk, chunks, rows2, chunks2, slice, slices, grad_blocks;
   float2 *part, *chan_part;
   int *status;
 };
