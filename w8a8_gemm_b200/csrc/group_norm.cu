@@ -50,10 +50,22 @@ __host__ __device__ inline Split split_of(int C) {
   return o >= kThreads ? Split{kThreads, 1} : Split{o, kThreads / o};
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// f(q) for the first `n` of K rows: without a test for each where there are K, so
+// that the rows' instructions mix.
+template <int K, typename F>
+__device__ __forceinline__ void first_rows(int n, F &&f) {
+  if (n >= K) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  return v;
+    for (int q = 0; q < K; ++q) f(q);
+  } else {
+#pragma unroll
+    for (int q = 0; q < K - 1; ++q)
+      if (q < n) f(q);
+  }
+}
+// Rows lane, lane + lanes, ... below `rows`.
+__device__ __forceinline__ int rows_of(int lane, int lanes, int rows) {
+  return lane < lanes && lane < rows ? (rows - 1 - lane) / lanes + 1 : 0;
 }
 
 // 2^u and 1/u by the special-function unit, within 2^-22 or so; past the largest
@@ -132,47 +144,63 @@ struct Running {
   }
 };
 
+// Sums over the channels of each group of f(c), a power of two of neighbouring
+// threads per group: out(g, sum) by one of them, or all with ALL.
+__host__ __device__ inline int threads_per_group(int cg) {
+  int t = 1;
+  while (t < 32 && t * 8 < cg) t *= 2;
+  return t;
+}
+__device__ __forceinline__ float2 sum_over(float2 s, int t) {
+  for (int o = 1; o < t; o <<= 1) {
+    s.x += __shfl_xor_sync(~0u, s.x, o);
+    s.y += __shfl_xor_sync(~0u, s.y, o);
+  }
+  return s;
+}
+
 // Joins the threads' statistics sh[lanes][width] (lane l saw the rows l, l + lanes,
-// ... of `rows`) into `out`(g, mean, squares) for each of `groups` groups of cg
-// channels: first the mean, then the squares about it.  A warp a group.
-template <int THREADS, typename Out>
-__device__ __forceinline__ void join_lanes(const float2 *sh, int lanes, int width, int rows,
-                                           int groups, int cg, Out &&out) {
+// ... of `rows`), {mean, squares} of each channel, over the lanes into chan[width]
+// and these over each group into out(g, mean, squares): first the mean, then the
+// squares about it.
+template <typename Out>
+__device__ __forceinline__ void join_lanes(const float2 *sh, float2 *chan, int lanes, int width,
+                                           int rows, int groups, int cg, Out &&out) {
   const int each = rows / lanes, more = rows % lanes;  // rows of a lane
   const int used = rows < lanes ? rows : lanes;        // lanes with any
-  const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
-  const int dl = 32 / cg, dc = 32 % cg, l0 = ln / cg, k0 = ln % cg;
+  const float all = static_cast<float>(rows), inv = 1.0f / all;
   __syncthreads();
-  for (int g = warp; g < groups; g += THREADS / 32) {
-    const float2 *src = sh + g * cg;
+  for (int c = threadIdx.x; c < width; c += kThreads) {
     float s = 0.0f;
-    int l = l0, c = k0;
-    while (l < used) {
-      s = fmaf(static_cast<float>(each + (l < more)), src[l * width + c].x, s);
-      l += dl;
-      c += dc;
-      if (c >= cg) {
-        c -= cg;
-        ++l;
-      }
-    }
-    const float mean = warp_sum(s) / (static_cast<float>(cg) * static_cast<float>(rows));
+    for (int l = 0; l < used; ++l)
+      s = fmaf(static_cast<float>(each + (l < more)), sh[l * width + c].x, s);
+    const float mean = s * inv;
     float m2 = 0.0f;
-    l = l0;
-    c = k0;
-    while (l < used) {
-      const float2 v = src[l * width + c];
+    for (int l = 0; l < used; ++l) {
+      const float2 v = sh[l * width + c];
       const float d = v.x - mean;
       m2 += fmaf(static_cast<float>(each + (l < more)) * d, d, v.y);
-      l += dl;
-      c += dc;
-      if (c >= cg) {
-        c -= cg;
-        ++l;
-      }
     }
-    m2 = warp_sum(m2);
-    if (ln == 0) out(g, mean, m2);
+    chan[c] = make_float2(mean, m2);
+  }
+  __syncthreads();
+  const int t = threads_per_group(cg), part = threadIdx.x % t;
+  for (int g0 = 0; g0 < groups; g0 += kThreads / t) {
+    const int g = g0 + threadIdx.x / t;
+    const float2 *src = chan + g * cg;
+    float2 s = make_float2(0.0f, 0.0f);
+    if (g < groups)
+      for (int c = part; c < cg; c += t) s.x += src[c].x;
+    const float mean = sum_over(s, t).x / static_cast<float>(cg);
+    s.x = 0.0f;
+    if (g < groups)
+      for (int c = part; c < cg; c += t) {
+        const float2 v = src[c];
+        const float d = v.x - mean;
+        s.y += fmaf(all * d, d, v.y);
+      }
+    const float m2 = sum_over(s, t).y;
+    if (g < groups && part == 0) out(g, mean, m2);
   }
 }
 
@@ -214,8 +242,9 @@ __device__ __forceinline__ void channel_sums(float2 *sh, float2 *chan, int lanes
 
 // ------------------------------------------------------------------- forward
 // Chunk statistics: part[b][chunk][g] = {mean, sum of squares about it}.
-__global__ void __launch_bounds__(kThreads) gn_stats_kernel(const GroupNormArgs p) {
-  extern __shared__ float2 sh[];  // [lanes][C] {mean, squares} of each thread's rows
+__global__ void __launch_bounds__(kThreads, 2) gn_stats_kernel(const GroupNormArgs p) {
+  // [lanes][C] {mean, squares} of each thread's rows, then of all rows
+  extern __shared__ float2 sh[];
   grid_dependency_wait();
   grid_dependency_launch();
   const int b = blockIdx.y;
@@ -227,16 +256,16 @@ __global__ void __launch_bounds__(kThreads) gn_stats_kernel(const GroupNormArgs 
   for (int o = oct; o < p.C / 8 && lane < sp.lanes; o += sp.oct) {
     Running st;
     st.clear();
-    const uint16_t *src = x + o * 8;
+    const int64_t step = sp.lanes * p.ldx;
+    const uint16_t *src = x + lane * p.ldx + o * 8;
     uint4 v[kBatch];
-    auto load = [&](int r) {
-#pragma unroll
-      for (int q = 0; q < kBatch; ++q)
-        if (r + q * sp.lanes < rows) v[q] = load8(src + (r + q * sp.lanes) * p.ldx);
+    auto load = [&](int n) {
+      first_rows<kBatch>(n, [&](int q) { v[q] = load8(src + q * step); });
+      src += kBatch * step;
     };
-    int r = lane;
-    load(r);
-    while (r < rows) {
+    int left = rows_of(lane, sp.lanes, rows);
+    load(left);
+    while (left > 0) {
       // sums of x - c and (x - c)^2 over up to kShifted rows, c the first of them
       const F2 minus = splat(-1.0f);
       const F2 c[4] = {f2_mul(f2_of_bf16(v[0].x), minus), f2_mul(f2_of_bf16(v[0].y), minus),
@@ -244,25 +273,23 @@ __global__ void __launch_bounds__(kThreads) gn_stats_kernel(const GroupNormArgs 
       F2 s[4], s2[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[j] = s2[j] = splat(0.0f);
-      int n = 0;
-      for (; n < kShifted && r < rows; r += sp.lanes * kBatch) {
+      const int n = left < kShifted ? left : kShifted;
+      for (int i = 0; i < n; i += kBatch, left -= kBatch) {
+        uint4 w[kBatch];
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          if (r + q * sp.lanes >= rows) break;
-          ++n;
-          const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+        for (int q = 0; q < kBatch; ++q) w[q] = v[q];
+        load(left - kBatch);
+        first_rows<kBatch>(left, [&](int q) {
+          const uint32_t u[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const F2 d = f2_add(f2_of_bf16(w[j]), c[j]);
+            const F2 d = f2_add(f2_of_bf16(u[j]), c[j]);
             s[j] = f2_add(s[j], d);
             s2[j] = f2_fma(d, d, s2[j]);
           }
-          // the next batch's row in the place that has just become free
-          const int next = r + (q + kBatch) * sp.lanes;
-          if (next < rows) v[q] = load8(src + next * p.ldx);
-        }
+        });
       }
-      const float inv = 1.0f / static_cast<float>(n);
+      const float inv = __fdividef(1.0f, static_cast<float>(n));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const F2 m = f2_mul(s[j], splat(inv));
@@ -274,11 +301,11 @@ __global__ void __launch_bounds__(kThreads) gn_stats_kernel(const GroupNormArgs 
     st.store(sh + lane * p.C + o * 8);
   }
   const int64_t slot = (static_cast<int64_t>(b) * p.chunks + blockIdx.x) * p.G;
-  join_lanes<kThreads>(sh, sp.lanes, p.C, rows, p.G, p.C / p.G, [&](int g, float mean, float m2) {
-                         if (store_ok(p.status,
-                                      slot + g < static_cast<int64_t>(p.B) * p.chunks * p.G))
-                           p.part[slot + g] = make_float2(mean, m2);
-                       });
+  join_lanes(sh, sh + sp.lanes * p.C, sp.lanes, p.C, rows, p.G, p.C / p.G,
+             [&](int g, float mean, float m2) {
+               if (store_ok(p.status, slot + g < static_cast<int64_t>(p.B) * p.chunks * p.G))
+                 p.part[slot + g] = make_float2(mean, m2);
+             });
 }
 
 // Sums over a sample's chunks of {f(v, n), g(v, n)} of each group's partials, n
@@ -354,11 +381,12 @@ __global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(const GroupNormAr
   const Split sp = split_of(width);
   const int lane = threadIdx.x / sp.oct, oct = threadIdx.x % sp.oct;
   const int64_t row0 = static_cast<int64_t>(b) * p.S + r0;
+  const int mine = rows_of(lane, sp.lanes, rows);
+  const int64_t stepx = sp.lanes * p.ldx, stepy = sp.lanes * p.ldy;
+  const uint16_t *x = p.x + (row0 + lane) * p.ldx;
   uint4 v[kBatch];
-  auto load = [&](int r, int c0) {
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q)
-      if (r + q * sp.lanes < rows) v[q] = load8(p.x + (row0 + r + q * sp.lanes) * p.ldx + c0);
+  auto load = [&](const uint16_t *src, int n) {
+    first_rows<kBatch>(n, [&](int q) { v[q] = load8(src + q * stepx); });
   };
   // the channels' gamma and beta, as they lie in two bf16 of a word
   uint32_t gm[4], bt[4];
@@ -372,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(const GroupNormAr
   };
   bool loaded = lane < sp.lanes;
   if (loaded) {
-    load(lane, ch0 + oct * 8);
+    load(x + ch0 + oct * 8, mine);
     load_params(ch0 + oct * 8);
   }
   grid_dependency_wait();
@@ -403,12 +431,12 @@ __global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(const GroupNormAr
       scale[j] = f2(k[0], k[1]);
       shift[j] = f2(t[0], t[1]);
     }
-    for (int r = lane; r < rows; r += sp.lanes * kBatch) {
-      if (!loaded) load(r, c0);
+    const uint16_t *src = x + c0;
+    uint16_t *dst = p.y + (row0 + lane) * p.ldy + c0;
+    for (int left = mine; left > 0; left -= kBatch) {
+      if (!loaded) load(src, left);
       loaded = false;
-#pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        if (r + q * sp.lanes >= rows) break;
+      first_rows<kBatch>(left, [&](int q) {
         const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
         uint32_t y[4];
 #pragma unroll
@@ -416,10 +444,11 @@ __global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(const GroupNormAr
           const float2 z = f2_get(act<ACT>(f2_fma(f2_of_bf16(w[j]), scale[j], shift[j])));
           y[j] = bf16x2(z.x, z.y);
         }
-        const int64_t row = row0 + r + q * sp.lanes;
-        if (store_ok(p.status, row < static_cast<int64_t>(p.B) * p.S && c0 + 8 <= p.ldy))
-          *reinterpret_cast<uint4 *>(p.y + row * p.ldy + c0) = make_uint4(y[0], y[1], y[2], y[3]);
-      }
+        if (store_ok(p.status, row0 + rows <= static_cast<int64_t>(p.B) * p.S && c0 + 8 <= p.ldy))
+          *reinterpret_cast<uint4 *>(dst + q * stepy) = make_uint4(y[0], y[1], y[2], y[3]);
+      });
+      src += kBatch * stepx;
+      dst += kBatch * stepy;
     }
   }
 }
@@ -470,7 +499,7 @@ __device__ __forceinline__ void store_param_grads(const GroupNormArgs &p, int c,
 // Chunk sums: chan_part[b][chunk][c] = {sum dv, sum dv xh} and
 // part[b][chunk][g] = {sum h, sum h xh}.
 template <int ACT>
-__global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const GroupNormArgs p) {
+__global__ void __launch_bounds__(kThreads, 2) gn_bwd_sums_kernel(const GroupNormArgs p) {
   extern __shared__ float2 sh[];  // [lanes][C], then the channels' sums
   grid_dependency_wait();
   grid_dependency_launch();
@@ -490,19 +519,18 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const GroupNormAr
     F2 sd[4], sx[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) sd[j] = sx[j] = f2(0.0f, 0.0f);
-    for (int r = lane; r < rows; r += sp.lanes * kAhead) {
+    const int64_t stepx = sp.lanes * p.ldx, stepd = sp.lanes * p.lddy;
+    const uint16_t *xs = p.x + (row0 + lane) * p.ldx + c0;
+    const uint16_t *ds = p.dy + (row0 + lane) * p.lddy + c0;
+    for (int left = rows_of(lane, sp.lanes, rows); left > 0; left -= kAhead) {
       uint4 vx[kAhead], vd[kAhead];
-#pragma unroll
-      for (int q = 0; q < kAhead; ++q) {
-        const int64_t row = row0 + r + q * sp.lanes;
-        if (r + q * sp.lanes < rows) {
-          vx[q] = load8(p.x + row * p.ldx + c0);
-          vd[q] = load8(p.dy + row * p.lddy + c0);
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < kAhead; ++q) {
-        if (r + q * sp.lanes >= rows) break;
+      first_rows<kAhead>(left, [&](int q) {
+        vx[q] = load8(xs + q * stepx);
+        vd[q] = load8(ds + q * stepd);
+      });
+      xs += kAhead * stepx;
+      ds += kAhead * stepd;
+      first_rows<kAhead>(left, [&](int q) {
         const uint32_t x[4] = {vx[q].x, vx[q].y, vx[q].z, vx[q].w};
         const uint32_t d[4] = {vd[q].x, vd[q].y, vd[q].z, vd[q].w};
 #pragma unroll
@@ -512,7 +540,7 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const GroupNormAr
           sd[j] = f2_add(sd[j], dv);
           sx[j] = f2_fma(dv, xh, sx[j]);
         }
-      }
+      });
     }
     float4 *to = reinterpret_cast<float4 *>(sh + lane * p.C + c0);
 #pragma unroll
@@ -526,25 +554,26 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(const GroupNormAr
   for (int c = threadIdx.x; c < p.C; c += kThreads)
     if (store_ok(p.status, slot < static_cast<int64_t>(p.B) * p.chunks))
       p.chan_part[slot * p.C + c] = chan[c];
-  const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
-  for (int g = warp; g < p.G; g += kWarps) {
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int c = g * cg + ln; c < (g + 1) * cg; c += 32) {
-      const float gm = p.gamma ? bf16_lo(p.gamma[c]) : 1.0f;
-      s1 = fmaf(gm, chan[c].x, s1);
-      s2 = fmaf(gm, chan[c].y, s2);
-    }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if (ln == 0 && store_ok(p.status, slot < static_cast<int64_t>(p.B) * p.chunks))
-      p.part[slot * p.G + g] = make_float2(s1, s2);
+  const int n = threads_per_group(cg), part = threadIdx.x % n;
+  for (int g0 = 0; g0 < p.G; g0 += kThreads / n) {
+    const int g = g0 + threadIdx.x / n;
+    float2 s = make_float2(0.0f, 0.0f);
+    if (g < p.G)
+      for (int c = g * cg + part; c < (g + 1) * cg; c += n) {
+        const float gm = p.gamma ? bf16_lo(p.gamma[c]) : 1.0f;
+        s.x = fmaf(gm, chan[c].x, s.x);
+        s.y = fmaf(gm, chan[c].y, s.y);
+      }
+    s = sum_over(s, n);
+    if (g < p.G && part == 0 && store_ok(p.status, slot < static_cast<int64_t>(p.B) * p.chunks))
+      p.part[slot * p.G + g] = s;
   }
 }
 
 // The first `grad_blocks` blocks add up 32 channels each of dgamma and dbeta;
 // the others write dx.
 template <int ACT, bool GF32>
-__global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs p) {
+__global__ void __launch_bounds__(kThreads, 2) gn_bwd_dx_kernel(const GroupNormArgs p) {
   extern __shared__ float2 sh[];
   __shared__ double2 sums[kThreads];
   const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
@@ -586,18 +615,19 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs
   // complete before the sums' kernel began to read them.
   uint4 vx[kAhead], vd[kAhead];
   Octet ch;
-  auto load = [&](int r, int c0) {
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q)
-      if (r + q * sp.lanes < rows) {
-        const int64_t row = row0 + r + q * sp.lanes;
-        vx[q] = load8(p.x + row * p.ldx + c0);
-        vd[q] = load8(p.dy + row * p.lddy + c0);
-      }
+  const int mine = rows_of(lane, sp.lanes, rows);
+  const int64_t stepx = sp.lanes * p.ldx, stepd = sp.lanes * p.lddy, stepo = sp.lanes * p.lddx;
+  auto load = [&](const uint16_t *xs, const uint16_t *ds, int n) {
+    first_rows<kAhead>(n, [&](int q) {
+      vx[q] = load8(xs + q * stepx);
+      vd[q] = load8(ds + q * stepd);
+    });
   };
+  const uint16_t *x0 = p.x + (row0 + lane) * p.ldx + ch0;
+  const uint16_t *d0 = p.dy + (row0 + lane) * p.lddy + ch0;
   bool loaded = lane < sp.lanes;
   if (loaded) {
-    load(lane, ch0 + oct * 8);
+    load(x0 + oct * 8, d0 + oct * 8, mine);
     ch.load(p, b, ch0 + oct * 8, cg);
   }
   grid_dependency_wait();
@@ -623,12 +653,12 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs
       m1[j] = f2(s.x, t.x);
       m2[j] = f2(s.y, t.y);
     }
-    for (int r = lane; r < rows; r += sp.lanes * kAhead) {
-      if (!loaded) load(r, c0);
+    const uint16_t *xs = x0 + o * 8, *ds = d0 + o * 8;
+    uint16_t *dst = p.dx + (row0 + lane) * p.lddx + c0;
+    for (int left = mine; left > 0; left -= kAhead) {
+      if (!loaded) load(xs, ds, left);
       loaded = false;
-#pragma unroll
-      for (int q = 0; q < kAhead; ++q) {
-        if (r + q * sp.lanes >= rows) break;
+      first_rows<kAhead>(left, [&](int q) {
         const uint32_t x[4] = {vx[q].x, vx[q].y, vx[q].z, vx[q].w};
         const uint32_t d[4] = {vd[q].x, vd[q].y, vd[q].z, vd[q].w};
         uint32_t y[4];
@@ -640,10 +670,12 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(const GroupNormArgs
               f2_get(f2_mul(ch.rstd[j], f2_fma(xh, m2[j], f2_fma(dv, ch.gamma[j], m1[j]))));
           y[j] = bf16x2(z.x, z.y);
         }
-        const int64_t row = row0 + r + q * sp.lanes;
-        if (store_ok(p.status, row < static_cast<int64_t>(p.B) * p.S && c0 + 8 <= p.lddx))
-          *reinterpret_cast<uint4 *>(p.dx + row * p.lddx + c0) = make_uint4(y[0], y[1], y[2], y[3]);
-      }
+        if (store_ok(p.status, row0 + rows <= static_cast<int64_t>(p.B) * p.S && c0 + 8 <= p.lddx))
+          *reinterpret_cast<uint4 *>(dst + q * stepo) = make_uint4(y[0], y[1], y[2], y[3]);
+      });
+      xs += kAhead * stepx;
+      ds += kAhead * stepd;
+      dst += kAhead * stepo;
     }
   }
 }
