@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -199,6 +200,27 @@ def lib() -> ctypes.CDLL:
             f.restype = ctypes.c_int
         _lib = L
     return _lib
+
+
+_native = None
+
+
+def _calls():
+    """The compiled calls of the operators around the quantized linear
+    (csrc/torch_calls.cpp) on this library, or False where they are not built."""
+    global _native
+    if _native is None:
+        L = lib()
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_sqtorch.so")
+        if not os.path.exists(path):
+            _native = False
+        else:
+            spec = importlib.util.spec_from_file_location("_sqtorch", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.init(L._handle)
+            _native = module
+    return _native
 
 
 def status_string(code: int) -> str:
@@ -530,12 +552,22 @@ def sq_dualscale_seglinear_host_noalloc(x_host: torch.Tensor, d: Optional[torch.
 
 # ------------------------------------------- operators around the quantized linear
 # These calls are short on the GPU (a few microseconds for a decoding step), so
-# their checks are written to be short on the host: one comparison per tensor,
-# and an explanation looked for only when it fails.
+# they go through compiled checks (_calls) where those are built.  What follows
+# them in each function is the same call through ctypes: it runs where they are
+# not built, and finds the reason where they say that an argument does not fit.
+# One comparison per tensor, and an explanation looked for only when it fails.
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 _OUT = {_BF16: SQ_OUT_BF16, _F32: SQ_OUT_F32}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _done(r, where: str):
+    """The outputs of a compiled call, which returns an int where the library
+    refused it."""
+    if r.__class__ is int:
+        _check(r, where)
+    return r
 
 
 def _explain(name: str, t, dtype, shape, dev: int, contiguous: bool):
@@ -672,6 +704,11 @@ def sq_lora_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: to
     bf16 or fp32 [M, N] (None: zeros, bf16 unless y says otherwise); y may be base
     (in place); t fp32 [M, R] is kept for the backward pass (rows without an
     adapter are not written)."""
+    native = _native or _calls()
+    if native:
+        r = native.lora_forward(x, A, B, scale, plan, base, y, t, workspace)
+        if r is not None:
+            return _done(r, "sq_lora_forward")
     M, K, dev = _rows_of("x", x, _BF16)
     L, R, Ka, N = _lora_sizes(A, B)
     if Ka != K:
@@ -705,6 +742,12 @@ def sq_lora_backward(dy: torch.Tensor, x: torch.Tensor, t: torch.Tensor, A: torc
     """Gradients of sq_lora_forward -> (dA, dB, dx): dA [L, R, K] and dB [L, N, R]
     of grad_dtype (bf16 or fp32; None without need_weights), dx = dx_base + the
     adapters' part (dx_base None: zeros; dx may be dx_base; None without need_dx)."""
+    native = _native or _calls()
+    if native and grad_dtype in _OUT:
+        r = native.lora_backward(dy, x, t, A, B, scale, plan, dx_base, dx, dA, dB,
+                                 grad_dtype is _F32, workspace, need_dx, need_weights)
+        if r is not None:
+            return _done(r, "sq_lora_backward")
     M, N, dev = _rows_of("dy", dy, _BF16)
     L, R, K, Nb = _lora_sizes(A, B)
     if Nb != N:
@@ -763,6 +806,12 @@ def _int_array(values: tuple):
 
 
 def _rope(call: str, x, positions, inv_freq, head_dim, out, layout, axis_pairs, factor):
+    native = _native or _calls()
+    if native:
+        r = native.rope(call == "sq_rope_backward", x, positions, inv_freq, head_dim, out, layout,
+                        axis_pairs, factor)
+        if r is not None:
+            return _done(r, call)[0]
     kind = getattr(x, "dtype", None)
     if kind is None:
         raise ValueError("x must be a tensor")
@@ -851,6 +900,11 @@ def sq_group_norm_forward(x: torch.Tensor, groups: int, gamma: Optional[torch.Te
     """y = act(group norm of x) over channels-last samples x bf16 [B, S, C] ->
     (y, mean, rstd); mean and rstd fp32 [B, groups] are kept for the backward
     pass.  gamma, beta bf16 [C] or None; y may be x (in place)."""
+    native = _native or _calls()
+    if native:
+        r = native.group_norm_forward(x, groups, gamma, beta, eps, act, y, workspace)
+        if r is not None:
+            return _done(r, "sq_group_norm_forward")
     B, S, C, dev = _gn_sizes(x)
     if y is None:
         y = torch.empty(B, S, C, dtype=_BF16, device=dev)
@@ -873,6 +927,12 @@ def sq_group_norm_backward(dy: torch.Tensor, x: torch.Tensor, groups: int,
                            workspace: Optional[torch.Tensor] = None, need_dx: bool = True):
     """Gradients of sq_group_norm_forward -> (dx, dgamma, dbeta); dgamma and dbeta
     [C] of grad_dtype (None where gamma or beta is None); dx may be dy."""
+    native = _native or _calls()
+    if native and grad_dtype in _OUT:
+        r = native.group_norm_backward(dy, x, groups, gamma, beta, mean, rstd, act, dx,
+                                       grad_dtype is _F32, workspace, need_dx)
+        if r is not None:
+            return _done(r, "sq_group_norm_backward")
     B, S, C, dev = _gn_sizes(x)
     shape = (B, S, C)
     out = _out_dtype(grad_dtype, "grad_dtype")
@@ -912,6 +972,13 @@ def sq_dualscale_seglinear_input_grad(dy: torch.Tensor, wq: torch.Tensor, s_w: t
     to its input (dy bf16 [M, N] -> dx bf16 [M, K]), straight through the
     activation quantizer.  workspace: uint8, sq_input_grad_workspace_bytes(N, K);
     layers on one stream may share one."""
+    native = _native or _calls()
+    if native:
+        cs, keep = seg._c()
+        r = native.input_grad(dy, wq, s_w, d, ctypes.addressof(cs), seg.n_groups, seg.S, dx,
+                              workspace)
+        if r is not None:
+            return _done(r, "sq_dualscale_seglinear_input_grad")[0]
     M, N, dev = _rows_of("dy", dy, _BF16)
     if not isinstance(wq, torch.Tensor) or wq.dim() != 2:
         raise ValueError("wq must be [N, K]")

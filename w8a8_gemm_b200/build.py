@@ -10,18 +10,24 @@ and weight quantizers depend on IEEE round-to-nearest fp32 operations.  The CUDA
 runtime is linked statically, so the library needs only the NVIDIA driver at
 run time; driver entry points (tensor-map encoding) are resolved through the
 runtime, so there is no link-time dependency on libcuda.
+
+Beside it, _sqtorch.so: the short way from torch tensors to the library's
+operators (csrc/torch_calls.cpp), compiled with the host compiler against the
+torch that imports it.  Without it the same calls go through ctypes.
 """
 import glob
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libsegquant.so")
 LIB_DEBUG = os.path.join(HERE, "libsegquant_debug.so")
+CALLS = os.path.join(HERE, "_sqtorch.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -51,7 +57,30 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def build_calls(force: bool = False) -> str:
+    src = os.path.join(CSRC, "torch_calls.cpp")
+    header = os.path.join(INCLUDE, "segquant.h")
+    if (not force and os.path.exists(CALLS)
+            and os.path.getmtime(CALLS) >= max(os.path.getmtime(src), os.path.getmtime(header))):
+        return CALLS
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    dirs = [INCLUDE, os.path.join(home, "include"), os.path.join(cuda, "include"),
+            sysconfig.get_paths()["include"]]
+    tmp = CALLS + f".tmp{os.getpid()}"
+    subprocess.run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+                    "-fvisibility=hidden",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                    *[f"-I{d}" for d in dirs], src, "-o", tmp, "-L" + os.path.join(home, "lib"),
+                    "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-ldl"],
+                   check=True)
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
+    build_calls(force)
     lib = LIB_DEBUG if debug else LIB
     if not force and up_to_date(lib):
         return lib
