@@ -542,7 +542,7 @@ SQ_API sq_status sq_lora_plan(const int32_t *adapter, int64_t M, int32_t n_adapt
  * sq_lora_forward -- adapters of rank R beside a projection, for every row m
  * with adapter a:   t[m] = A[a] x[m],   y[m] = base[m] + scale[a] B[a] t[m].
  * Rows without an adapter: y[m] = base[m] (left alone when y is base) and t[m]
- * is not written.  t is fp32; where y is bf16, t enters the second product
+ * is not written.  t is fp32; where y is bf16, scale t enters the second product
  * rounded to bf16; where y is fp32, with 24 bits.  Sums are fp32.
  *   x      bf16 [M][ldx];  A bf16 [L][R][K], B bf16 [L][N][R], scale fp32 [L]
  *   plan   of sq_lora_plan for this M and L
@@ -557,7 +557,7 @@ SQ_API sq_status sq_lora_plan(const int32_t *adapter, int64_t M, int32_t n_adapt
  *   R 8..128, K and N >= 8, all multiples of 8; K, N <= 2^20; leading dimensions
  *   at least the row's length and multiples of 8; x, A, B, base, y, t, plan
  *   16-byte aligned, scale 4-byte; M <= 2^24, M * ld <= 2^44.
- * M == 0 is a valid no-op.  Two kernels.
+ * M == 0 is a valid no-op.  Two kernels, one for a few rows.
  * sq_lora_workspace_bytes: for the forward and for the backward call (there with
  * grad_dtype); 0 for sizes out of range.
  */

@@ -244,3 +244,40 @@ def test_plan_of_another_batch_is_reported_and_nothing_written():
     assert all((g == 9.0).all() for g in (dA, dB, dx))
     assert (y == 9.0).all() and (t == 9.0).all()
     assert B.sq_get_device_status() == B.SQ_OK
+
+
+FEW = [  # M, K, N, R, L, spread: around the sizes up to which one kernel does both products
+    (1, 8, 8, 8, 1, "one"), (2, 64, 4096, 64, 2, "one"), (15, 520, 264, 128, 1, "one"),
+    (16, 1536, 1536, 16, 1, "one"), (17, 1536, 1536, 16, 1, "one"), (17, 264, 1000, 40, 2, "one"),
+    (32, 2056, 72, 104, 9, "scattered"), (32, 1536, 2048, 128, 2, "one"), (33, 256, 64, 8, 3, "scattered"),
+    (31, 72, 2056, 128, 40, "scattered"), (24, 128, 128, 16, 3, "none"), (9, 6144, 1536, 24, 1024, "runs"),
+]
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("M,K,N,R,L,spread", FEW)
+def test_few_rows(M, K, N, R, L, spread, out):
+    """Strided and in place, zeros for base, rows without an adapter left alone,
+    and the same bits again."""
+    p = _problem(M, K, N, R, L, seed=3 * M + R, spread=spread, out=out)
+    plan = B.sq_lora_plan(p["ids"], L)
+    some = (p["ids"] >= 0) & (p["ids"] < L)
+    wide = torch.full((M, N + 16), 3.25, dtype=out, device="cuda")
+    y = wide[:, 8:8 + N]
+    y.copy_(p["base"])
+    x = torch.full((M, K + 8), float("nan"), dtype=BF, device="cuda")
+    x[:, :K] = p["x"]
+    t = torch.full((M, R), -7.5, device="cuda")
+    B.sq_lora_forward(x[:, :K], p["A"], p["B"], p["scale"], plan, y, y=y, t=t)
+    v, e, T, eT = ref.lora_forward(p["x"], p["A"], p["B"], p["scale"], p["ids"], p["base"], out)
+    ref.check(y.contiguous(), v, e, "y")
+    ref.check(t[some], T[some], eT[some], "t")
+    assert (t[~some] == -7.5).all() and torch.equal(y[~some], p["base"][~some])
+    assert (wide[:, :8] == 3.25).all() and (wide[:, 8 + N:] == 3.25).all()
+    z, _ = B.sq_lora_forward(p["x"], p["A"], p["B"], p["scale"], plan, None,
+                             y=torch.full((M, N), 9.0, dtype=out, device="cuda"))
+    v, e, _, _ = ref.lora_forward(p["x"], p["A"], p["B"], p["scale"], p["ids"], None, out)
+    ref.check(z, v, e, "y without base")
+    again, _ = B.sq_lora_forward(p["x"], p["A"], p["B"], p["scale"], plan, p["base"])
+    assert torch.equal(again, y)
+    assert B.sq_get_device_status() == B.SQ_OK
