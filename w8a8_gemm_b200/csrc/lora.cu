@@ -718,7 +718,8 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const FewArgs p) 
 // the SM an element meets one 16-byte shared load and store and an addition:
 // with the products on the warp-level path, whose operands pass through the
 // same load pipe, that pipe was the bound (8858 x 6144, rank 64: 59 us).
-// Scattered rows of base are copied by two warps.  Rows without an adapter are
+// Scattered rows of base are copied by four warps (1501 ragged rows, 1536 -> 2304
+// in fp32: 22.8 us with the contraction, 25.7 with two warps).  Rows without an adapter are
 // copied from base (left alone when out is base).
 struct ExpandArgs {
   const int32_t *plan;
@@ -735,7 +736,7 @@ struct ExpandMaps {
 };
 
 constexpr int kExpandWarps = 8;                            // adding and storing
-constexpr int kExpandThreads = 64 + 32 * kExpandWarps + 64;  // producer, MMA, two copying
+constexpr int kExpandThreads = 64 + 32 * (kExpandWarps + kCopyWarps);  // and producer, MMA
 
 template <int RT, bool F32>
 struct ExpandSmem {
@@ -807,7 +808,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 3);                  // producer, two copying warps
+      mbar_init(&full[s], 1 + kCopyWarps);     // producer, copying warps
       mbar_init(&empty[s], kExpandWarps + 1);  // storing warps, MMA issuer
     }
     for (int b = 0; b < 2; ++b) {
@@ -921,9 +922,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         if (bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, kTimeout)) {
           meta[st] = kUnitEnd;
           armed &= ~(1u << st);  // its last copy has been read
-          mbar_arrive(&full[st]);
-          mbar_arrive(&full[st]);
-          mbar_arrive(&full[st]);
+          for (int i = 0; i < 1 + kCopyWarps; ++i) mbar_arrive(&full[st]);
         }
       }
       // never leave with a copy in flight into this block's shared memory
@@ -997,8 +996,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       const int n = u.here(), slab = u.slab;
       // this warp's rows: how many, and whether one box holds them
       const int mine = count - quarter * 32 < 32 ? count - quarter * 32 : 32;
-      const bool box = h.w != 0 && mine == 32;
       const int first = __shfl_sync(~0u, row, 0);
+      // rows ascend within a tile
+      const bool box = mine == 32 && __shfl_sync(~0u, row, 31) - first == 31;
       u.next_tile();
       if (u.left > 0) read(u.tile);
       const bool none = bin >= p.L;
@@ -1098,8 +1098,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------- copying warps
-    // scattered base: 64 rows each, lane: rows 2 i + lane / 16, chunk lane % 16
-    const int r0 = (warp - 2 - kExpandWarps) * 64 + (lane >> 4);
+    // scattered base: 32 rows each, lane: rows 2 i + lane / 16, chunk lane % 16
+    const int r0 = (warp - 2 - kExpandWarps) * 32 + (lane >> 4);
     const int q = lane & 15;
     int step = 0;
     bool ok = true;
@@ -1109,9 +1109,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       const int4 h = *reinterpret_cast<const int4 *>(rec);
       if (h.x >= p.L && in_place) continue;
       const bool copies = has_base && h.w == 0;
-      int32_t rows[32];
+      int32_t rows[16];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) rows[i] = copies ? rec[4 + r0 + 2 * i] : 0;
+      for (int i = 0; i < 16; ++i) rows[i] = copies ? rec[4 + r0 + 2 * i] : 0;
       const int n = u.here();
       for (int i = 0; i < n; ++i, ++step) {
         const int st = step % STAGES;
@@ -1130,7 +1130,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         const uint8_t *src = static_cast<const uint8_t *>(p.base) + static_cast<int64_t>(col) * E;
         if (col < p.C) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
+          for (int k = 0; k < 16; ++k) {
             if (r0 - (lane >> 4) + 2 * k >= h.y) break;
             if (r0 + 2 * k < h.y)
               cp_async16(to + swz128(r0 + 2 * k, q & 7), src + rows[k] * p.ld_base * E, true);
@@ -1708,12 +1708,12 @@ template <int RT, int TERMS>
 cudaError_t run_outer(const OuterMaps &maps, const OuterArgs &a, cudaStream_t stream) {
   using S = OuterSmem<RT, TERMS>;
   const int slabs = a.slabs0 + (a.side[1].C + kOuterSlab - 1) / kOuterSlab;
-  // Blocks of a slab: as many (up to the portable cluster size, and one for each
-  // two full row tiles) as let all slabs run at once.  A cluster lies within one
+  // Blocks of a slab: as many (up to the portable cluster size, with 64 rows each
+  // at least) as let all slabs run at once.  A cluster lies within one
   // of the GPU's partitions, which leaves some places empty: 60 slabs by 4 take
-  // 58 us, by 7 (three blocks per SM) two rounds and 80 us.
+  // 42 us, by 7 (three blocks per SM) two rounds and 80 us.
   int shares = 1;
-  for (int n = 2; n <= 8 && a.M >= 2 * kTileRows * n; ++n)
+  for (int n = 2; n <= 8 && a.M >= kTileRows / 2 * n; ++n)
     if (static_cast<int64_t>(slabs) * n * 16 <= static_cast<int64_t>(S::kPerSm) * sm_count() * 15)
       shares = n;
   return launch<lora_outer_kernel<RT, TERMS>>(dim3(slabs * shares), kOuterThreads, S::kBytes,
