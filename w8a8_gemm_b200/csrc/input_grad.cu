@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "bf16.cuh"
@@ -34,9 +35,10 @@ namespace {
 
 // ------------------------------------------------------------------------- W~
 // w [N][K].  A thread has 8 neighbouring channels of kDeqRows rows of the weight,
-// all loads under way at once; a block 256 channels of 16 rows (64 rows left too few
-// blocks to hide the divisions: 1536 x 1536 with divisors took 11.5 us).
-constexpr int kDeqThreads = 256, kDeqLanes = kDeqThreads / 32, kDeqRows = 2;
+// all loads under way at once; a block 256 channels of 32 rows.  A channel's divisor
+// is inverted once (one rounding more; with a division for every code 1536 x
+// 1536 took 7.6 us for 6.7), unless its inverse is past the largest number.
+constexpr int kDeqThreads = 256, kDeqLanes = kDeqThreads / 32, kDeqRows = 4;
 __global__ void __launch_bounds__(kDeqThreads) dequant_kernel(
     const int8_t *__restrict__ wq, const float *__restrict__ s_w, const float *__restrict__ d,
     int64_t N, int64_t K, const __grid_constant__ SegParams seg, uint16_t *__restrict__ w,
@@ -50,6 +52,22 @@ __global__ void __launch_bounds__(kDeqThreads) dequant_kernel(
   const int i = seg.S > 1 ? seg_index(seg.off, seg.n_seg, k) : 0;
   uint2 v[kDeqRows];
   float s[kDeqRows];
+  float inv[8], dv[8];  // of activation group `group`
+  bool inverts = true;
+  int group = -1;
+  auto divisors = [&](int64_t n) {
+    const int g = seg.G > 1 ? seg_index(seg.off, seg.n_seg, n) : 0;
+    if (g == group) return;
+    group = g;
+    inverts = true;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dv[j] = d[g * K + k + j];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      inv[j] = __frcp_rn(dv[j]);
+      inverts = inverts && fabsf(inv[j]) < INFINITY;
+    }
+  };
 #pragma unroll
   for (int r = 0; r < kDeqRows; ++r) {
     const int64_t n = n0 + r * kDeqLanes;
@@ -76,9 +94,9 @@ __global__ void __launch_bounds__(kDeqThreads) dequant_kernel(
       q[j] *= s[r];
     }
     if (d != nullptr) {
-      const float *dg = d + (seg.G > 1 ? seg_index(seg.off, seg.n_seg, n) : 0) * K + k;
+      divisors(n);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = __fdiv_rn(q[j], dg[j]);
+      for (int j = 0; j < 8; ++j) q[j] = inverts ? q[j] * inv[j] : __fdiv_rn(q[j], dv[j]);
     }
     if (store_ok(status, k + 8 <= K))
       *reinterpret_cast<uint4 *>(w + n * K + k) = make_uint4(
@@ -163,13 +181,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   cluster.sync();  // both blocks' barriers and columns stand
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  grid_dependency_wait();  // the prologue above touches no global memory
+  // dy was complete before the kernel ahead of this one began; only W~, which that
+  // one writes, has to be waited for
+  if (warp != 0) grid_dependency_wait();
 
   if (warp == 0) {
     if (lane == 0) {
-      int stage = 0;
+      int stage = 0, early = 0;
       uint32_t phase = 0, armed = 0, armed_parity = 0;
       bool gave_up = false;
+      // the first tile's rows of dy, as many stages as there are
+      if (first < p.num_tiles) {
+        early = p.num_kb < STAGES ? p.num_kb : STAGES;
+        for (int kb = 0; kb < early; ++kb) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[kb], 2 * L::STAGE);
+          tma_load_2d_pair(smem + kb * L::STAGE, &tmA, cluster_addr(&full[kb], 0), kb * BK,
+                           (first / p.num_n_tiles * 2 + rank) * BM);
+        }
+      }
+      grid_dependency_wait();
       for (int tile = first; tile < p.num_tiles; tile += step) {
         const int row = (tile / p.num_n_tiles * 2 + rank) * BM;
         const int col = tile % p.num_n_tiles * BN + rank * (BN / 2);
@@ -179,9 +209,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             goto producer_done;
           }
           uint8_t *sa = smem + stage * L::STAGE;
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * L::STAGE);
           const uint32_t bar = cluster_addr(&full[stage], 0);
-          tma_load_2d_pair(sa, &tmA, bar, kb * BK, row);
+          if (tile != first || kb >= early) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * L::STAGE);
+            tma_load_2d_pair(sa, &tmA, bar, kb * BK, row);
+          }
 #pragma unroll
           for (int b = 0; b < BN / 128; ++b)
             tma_load_2d_pair(sa + L::A + b * 8192, &tmB, bar, col + b * 64, kb * BK);
