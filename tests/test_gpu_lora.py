@@ -281,3 +281,74 @@ def test_few_rows(M, K, N, R, L, spread, out):
     again, _ = B.sq_lora_forward(p["x"], p["A"], p["B"], p["scale"], plan, p["base"])
     assert torch.equal(again, y)
     assert B.sq_get_device_status() == B.SQ_OK
+
+
+def test_infinite_values_of_a_used_row_stay_infinite():
+    """Places past a tile's last row add nothing, not even 0 times infinity."""
+    M, K, N, R, L = 300, 128, 128, 16, 3
+    p = _problem(M, K, N, R, L, seed=4, spread="scattered")
+    first = int((p["ids"] == 1).nonzero()[0, 0])
+    p["x"][first, 5] = float("inf")
+    p["dy"][first, 7] = float("inf")
+    plan = B.sq_lora_plan(p["ids"], L)
+    t = torch.rand(M, R, device="cuda") + 0.5
+    dA, dB, _ = B.sq_lora_backward(p["dy"], p["x"], t, p["A"], p["B"], p["scale"], plan, None,
+                                   need_dx=False)
+    # dy's infinity makes dt of that row infinite (NaN where B is 0): dA[1] whole
+    assert torch.isinf(dB[1, 7]).all() and torch.isfinite(dB[1, :7]).all()
+    assert torch.isfinite(dB[1, 8:]).all()
+    assert torch.isfinite(dA[[0, 2]]).all() and torch.isfinite(dB[[0, 2]]).all()
+    p["dy"][first, 7] = 1.0
+    dA, dB, _ = B.sq_lora_backward(p["dy"], p["x"], t, p["A"], p["B"], p["scale"], plan, None,
+                                   need_dx=False)
+    assert torch.isinf(dA[1, :, 5]).all() and torch.isfinite(dB).all()
+    assert torch.isfinite(dA[1, :, :5]).all() and torch.isfinite(dA[1, :, 6:]).all()
+
+
+def test_the_stride_of_a_single_row_says_nothing():
+    K, N, R, L = 64, 4096, 128, 2
+    p = _problem(1, K, N, R, L, seed=8, spread="one")
+    plan = B.sq_lora_plan(p["ids"], L)
+    far = {k: torch.as_strided(p[k], p[k].shape, (2 ** 42, 1)) for k in ("x", "base", "dy")}
+    y, t = B.sq_lora_forward(p["x"], p["A"], p["B"], p["scale"], plan, p["base"])
+    z, _ = B.sq_lora_forward(far["x"], p["A"], p["B"], p["scale"], plan, far["base"])
+    assert torch.equal(y, z)
+    want = B.sq_lora_backward(p["dy"], p["x"], t, p["A"], p["B"], p["scale"], plan, p["dx_base"])
+    got = B.sq_lora_backward(far["dy"], far["x"], t, p["A"], p["B"], p["scale"], plan,
+                             torch.as_strided(p["dx_base"], (1, K), (2 ** 42, 1)))
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    wq, s_w = torch.ones(N, K, dtype=torch.int8, device="cuda"), torch.ones(1, N, device="cuda")
+    assert torch.equal(B.sq_dualscale_seglinear_input_grad(p["dy"], wq, s_w, None, B.Segments()),
+                       B.sq_dualscale_seglinear_input_grad(far["dy"], wq, s_w, None, B.Segments()))
+
+
+def test_plans_made_by_two_threads_at_once():
+    """Plans of one and of 1024 adapters, whose kernels need different amounts of
+    shared memory, from two host threads."""
+    import threading
+    ids = torch.arange(500, device="cuda", dtype=torch.int32) % 7
+    want = {L: B.sq_lora_plan(ids, L) for L in (1, 1024)}
+    wrong = []
+
+    def run(L):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(200):
+                try:
+                    got = B.sq_lora_plan(ids, L)
+                except B.SegQuantError as e:
+                    wrong.append((L, str(e)))
+                    return
+            torch.cuda.current_stream().synchronize()
+            tiles = int(got[3])
+            n = (4 + L + 2 + 3) // 4 * 4 + 132 * tiles
+            head = 4 + L + 2
+            if not (torch.equal(got[:head], want[L][:head])
+                    and torch.equal(got[(4 + L + 2 + 3) // 4 * 4:n], want[L][(4 + L + 2 + 3) // 4 * 4:n])):
+                wrong.append((L, "differs"))
+
+    threads = [threading.Thread(target=run, args=(L,)) for L in (1, 1024)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong, wrong

@@ -327,6 +327,7 @@ sq_status tensor_map_2d(CUtensorMap *map, const void *ptr, int64_t inner, int64_
                         int64_t ld, int box_rows) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (enc == nullptr) return SQ_ERR_CUDA;
+  if (outer <= 1) ld = (inner + 7) / 8 * 8;  // one row: its stride may be anything
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
   const cuuint32_t box[2] = {BK, static_cast<cuuint32_t>(box_rows)};

@@ -1360,9 +1360,12 @@ __global__ void __launch_bounds__(kOuterThreads, OuterSmem<RT, TERMS>::kPerSm)
                                   (i * 2 + (lane >> 4)) & 31);
           if (c < 8 || wide) {
 #pragma unroll
-            for (int i = 0; i < kOuterRows / 2; ++i)
+            for (int i = 0; i < kOuterRows / 2; ++i) {
+              // zeros past the tile's last row, which meet zeros of v
+              const bool in = in_cols && q * kOuterRows + i * 2 + (lane >> 4) < h.y;
               cp_async16(to + swz128(i * 2 + (lane >> 4), c & 7),
-                         sd.src + rows[i] * sd.ld + (in_cols ? col : 0), in_cols);
+                         sd.src + rows[i] * sd.ld + (in ? col : 0), in);
+            }
           }
           cp_async_commit();
           late.push(lane, &full[st]);
@@ -1645,6 +1648,7 @@ cudaError_t tile_map(CUtensorMap *map, bool f32, const void *ptr, int64_t d0, in
   EncodeTiledFn enc = tensor_map_encoder();
   if (enc == nullptr) return cudaErrorNotSupported;
   const int elem = f32 ? 4 : 2;
+  if (d1 <= 1) ld = (d0 + 7) / 8 * 8;  // one row: its stride may be anything
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1),
                               static_cast<cuuint64_t>(d2)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * elem,
@@ -1822,9 +1826,9 @@ size_t lora_workspace_bytes(int64_t M, int32_t R, int32_t L, bool f32) {
 
 cudaError_t launch_lora_plan(const int32_t *adapter, int64_t M, int32_t L, int32_t *plan,
                              int *status, cudaStream_t stream) {
+  // the limit for any L: calls of two threads must not lower each other's
   const int bytes = (kPlanWarps * (L + 1) + 2 * (L + 2)) * 4;
-  cudaError_t e = cudaFuncSetAttribute(lora_plan_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e = allow_smem<lora_plan_kernel>((kPlanWarps * 1025 + 2 * 1026) * 4);
   if (e != cudaSuccess) return e;
   lora_plan_kernel<<<1, kPlanWarps * 32, bytes, stream>>>(adapter, static_cast<int32_t>(M), L,
                                                           plan, status);
