@@ -583,7 +583,8 @@ SQ_API sq_status sq_lora_forward(const void *x, int64_t ldx, const void *A, cons
  *   dy       bf16 [M][lddy];  x, A, B, scale, plan as in the forward call
  *   t        fp32 [M][R] of the forward call
  *   dx_base  bf16 [M][ldbase] or NULL for zeros; dx bf16 [M][lddx] output, or
- *            NULL (with dx_base NULL) to skip it; dx_base may be dx
+ *            NULL (with dx_base NULL) to skip it; dx_base may be dx; dx must not
+ *            overlap dy or x
  *   dA, dB   [L][R][K] and [L][N][R] outputs of grad_dtype, or both NULL
  *   workspace  device memory of sq_lora_workspace_bytes(M, R, L, grad_dtype)
  *            bytes, 16-byte aligned; needs no initial value (NULL when M == 0)

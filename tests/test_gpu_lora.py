@@ -352,3 +352,40 @@ def test_plans_made_by_two_threads_at_once():
     for th in threads:
         th.join()
     assert not wrong, wrong
+
+
+@pytest.mark.parametrize("M,K,N,R,L,spread", [(333, 1536, 1536, 8, 3, "runs"),
+                                              (6000, 1536, 2048, 64, 2, "mixed")])
+def test_backward_kernels_side_by_side_keep_the_streams_order(M, K, N, R, L, spread):
+    """dA, dB and dx are whole for whatever comes next on the stream: consumers
+    right behind the call, and the buffers used again by the next one, eager and
+    replayed, give the bits of calls that are waited for."""
+    p = _problem(M, K, N, R, L, seed=21, spread=spread)
+    plan = B.sq_lora_plan(p["ids"], L)
+    _, t = B.sq_lora_forward(p["x"], p["A"], p["B"], p["scale"], plan, p["base"])
+    ws = torch.empty(B.sq_lora_workspace_bytes(M, R, L), dtype=torch.uint8, device="cuda")
+    dA, dB = torch.empty_like(p["A"]), torch.empty_like(p["B"])
+    dx = torch.empty_like(p["x"])
+    dys = [p["dy"], (2 * p["dy"].float()).to(BF), (-p["dy"].float()).to(BF)]
+
+    def step(dy):
+        B.sq_lora_backward(dy, p["x"], t, p["A"], p["B"], p["scale"], plan, None, dx=dx, dA=dA,
+                           dB=dB, workspace=ws)
+        return [v.clone() for v in (dA, dB, dx)]
+
+    want = []
+    for dy in dys:
+        want.append(step(dy))
+        torch.cuda.synchronize()
+    for _ in range(20):
+        got = [step(dy) for dy in dys]
+        for a, b in zip(want, got):
+            assert all(torch.equal(u, v) for u, v in zip(a, b))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [step(dy) for dy in dys]
+    for _ in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))

@@ -264,3 +264,16 @@ def test_reference_gradients_against_differences():
     dx = ref.input_grad(dy, w)[0]
     for v, diff in _differences(lambda x: x @ w.t(), (x,), 0, dy):
         assert math.isclose(float((dx * v).sum()), diff, rel_tol=1e-6, abs_tol=1e-7)
+
+
+def test_lora_outputs_over_inputs_are_refused(L):
+    """The kernels of a call run side by side: an output in an input's place."""
+    need = L.sq_lora_workspace_bytes(4, 8, 2, 0)
+    fwd = dict(x=FAKE, ldx=64, A=FAKE, B=FAKE, scale=FAKE, plan=FAKE, base=None, ldbase=0,
+               y=FAKE, ldy=64, out=0, t=FAKE, workspace=FAKE, bytes=need, M=4, N=64, K=64, R=8, L=2)
+    assert _call(L.sq_lora_forward, fwd) == INVALID
+    bwd = dict(dy=FAKE, lddy=64, x=2 * FAKE, ldx=64, t=FAKE, A=FAKE, B=FAKE, scale=FAKE, plan=FAKE,
+               base=None, ldbase=0, dx=FAKE, lddx=64, dA=FAKE, dB=FAKE, grads=0, workspace=FAKE,
+               bytes=need, M=4, N=64, K=64, R=8, L=2)
+    assert _call(L.sq_lora_backward, bwd) == INVALID
+    assert _call(L.sq_lora_backward, bwd, dx=2 * FAKE) == INVALID

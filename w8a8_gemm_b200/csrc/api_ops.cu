@@ -183,7 +183,7 @@ sq_status sq_lora_forward(const void *x, int64_t ldx, const void *A, const void 
   if (base != nullptr) SQ_TRY(check_rows(base, M, N, ldbase));
   if (M == 0) return SQ_OK;
   const bool f32 = out_dtype == SQ_OUT_F32;
-  if (t == nullptr || (base == y && ldbase != ldy)) return SQ_ERR_INVALID_ARG;
+  if (t == nullptr || y == x || (base == y && ldbase != ldy)) return SQ_ERR_INVALID_ARG;
   if (workspace == nullptr || workspace_bytes < lora_workspace_bytes(M, R, n_adapters, f32))
     return SQ_ERR_INVALID_ARG;
   if (!aligned(t, 16) || !aligned(workspace, 16)) return SQ_ERR_ALIGNMENT;
@@ -229,6 +229,7 @@ sq_status sq_lora_backward(const void *dy, int64_t lddy, const void *x, int64_t 
                 workspace_bytes < lora_workspace_bytes(M, R, n_adapters, f32)))
     return SQ_ERR_INVALID_ARG;
   if (dx != nullptr && dx_base == dx && ldbase != lddx) return SQ_ERR_INVALID_ARG;
+  if (dx != nullptr && M > 0 && (dx == dy || dx == x)) return SQ_ERR_INVALID_ARG;
   if (!aligned(t, 16) || !aligned(workspace, 16) || !aligned(dA, 16) || !aligned(dB, 16))
     return SQ_ERR_ALIGNMENT;
   if (dA == nullptr && (dx == nullptr || M == 0)) return SQ_OK;

@@ -840,7 +840,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   Units u;
   u.init(p.plan, fits ? p.plan[3] : 0, p.L, (p.C + SLAB - 1) / SLAB);
   const bool has_base = p.base != nullptr, in_place = p.base == p.out;
-  if (warp != 0) grid_dependency_wait();
+  if (warp != 0) {
+    grid_dependency_wait();
+    grid_dependency_launch();
+  }
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -1177,6 +1180,7 @@ struct OuterSide {
 struct OuterArgs {
   OuterSide side[2];
   int32_t slabs0;  // slabs of side 0
+  int32_t beside;  // the kernel ahead is the expansion, not the contraction
   const int32_t *plan;
   int64_t M;
   int32_t R, L;
@@ -1271,7 +1275,10 @@ __global__ void __launch_bounds__(kOuterThreads, OuterSmem<RT, TERMS>::kPerSm)
   };
   const int t_lo = first_tile(rank), t_hi = first_tile(rank + 1);
   auto bin_of = [&](int tile) { return recs[static_cast<int64_t>(tile) * kRecWords]; };
-  grid_dependency_wait();
+  // Behind the expansion: that one lets this kernel begin when the contraction
+  // is complete, and nothing here touches what it writes, so the two run side by
+  // side; the wait at the end keeps the stream's order for what comes next.
+  if (!p.beside) grid_dependency_wait();
 
   const int cols = sd.C - c0 < kOuterSlab ? sd.C - c0 : kOuterSlab;
   float keep[RT];  // storing warps: the sums of a first adapter that is shared
@@ -1592,6 +1599,7 @@ __global__ void __launch_bounds__(kOuterThreads, OuterSmem<RT, TERMS>::kPerSm)
     tc_fence_after();
     tmem_dealloc(tmem, 2 * RT);
   }
+  if (p.beside) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------ host side
@@ -1756,12 +1764,20 @@ cudaError_t run_backward(const LoraRequest &q, cudaStream_t stream) {
   cudaError_t e = by_rank(q.R, [&](auto rt) {
     return run_contract<decltype(rt)::value, true, TERMS>(q.B, c, stream);
   });
+  if (e == cudaSuccess && q.dx != nullptr) {
+    const ExpandArgs x = {q.plan, q.base, q.ld_base, q.dx, q.lddx, q.M,
+                          max_tiles, K, q.R, q.L, q.status};
+    e = by_rank(q.R, [&](auto rt) {
+      return run_expand<decltype(rt)::value, true, false>(q.A, vdt, x, stream);
+    });
+  }
   if (e == cudaSuccess && q.dA != nullptr) {
     OuterMaps maps;
     OuterArgs o = {};
     o.side[0] = {q.dy, q.lddy, q.scale, q.dB, N, 0};
     o.side[1] = {q.x, q.ldx, nullptr, q.dA, K, 1};
     o.slabs0 = (N + kOuterSlab - 1) / kOuterSlab;
+    o.beside = q.dx != nullptr;
     o.plan = q.plan;
     o.M = q.M;
     o.R = q.R;
@@ -1775,13 +1791,6 @@ cudaError_t run_backward(const LoraRequest &q, cudaStream_t stream) {
       e = by_rank(q.R, [&](auto rt) {
         return run_outer<decltype(rt)::value, TERMS>(maps, o, stream);
       });
-  }
-  if (e == cudaSuccess && q.dx != nullptr) {
-    const ExpandArgs x = {q.plan, q.base, q.ld_base, q.dx, q.lddx, q.M,
-                          max_tiles, K, q.R, q.L, q.status};
-    e = by_rank(q.R, [&](auto rt) {
-      return run_expand<decltype(rt)::value, true, false>(q.A, vdt, x, stream);
-    });
   }
   return e;
 }
