@@ -842,7 +842,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   const bool has_base = p.base != nullptr, in_place = p.base == p.out;
   if (warp != 0) {
     grid_dependency_wait();
-    grid_dependency_launch();
+    if constexpr (TRANS) grid_dependency_launch();  // the outer products run beside
   }
 
   if (warp == 0) {
@@ -1685,9 +1685,9 @@ cudaError_t run_contract(const uint16_t *w, const ContractArgs &a, cudaStream_t 
               : bf16_map(&tm_w, w, a.C, a.R, a.L, a.C, RT);
   if (e != cudaSuccess) return e;
   // Slices of the contracted dimension: as many as let all tiles run at once
-  // (two blocks per SM), none shorter than 256 columns.
+  // (two blocks per SM), none shorter than 128 columns.
   int slices = 1;
-  while (slices < 8 && a.C >= 256 * slices * 2 && a.max_tiles * slices * 2 <= 2 * sm_count())
+  while (slices < 8 && a.C >= 128 * slices * 2 && a.max_tiles * slices * 2 <= 2 * sm_count())
     slices *= 2;
   return launch<lora_contract_kernel<RT, TRANS, TERMS>>(
       dim3(static_cast<unsigned>(a.max_tiles), slices), kContractThreads,
