@@ -63,6 +63,19 @@ __device__ __forceinline__ void first_rows(int n, F &&f) {
       if (q < n) f(q);
   }
 }
+// f(e, group of channel c0 + e) for eight channels, with one division.
+template <typename F>
+__device__ __forceinline__ void eight_groups(int c0, int cg, F &&f) {
+  int g = c0 / cg, left = (g + 1) * cg - c0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    f(e, g);
+    if (--left == 0) {
+      left = cg;
+      ++g;
+    }
+  }
+}
 // Rows lane, lane + lanes, ... below `rows`.
 __device__ __forceinline__ int rows_of(int lane, int lanes, int rows) {
   return lane < lanes && lane < rows ? (rows - 1 - lane) / lanes + 1 : 0;
@@ -418,18 +431,16 @@ __global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(const GroupNormAr
     // x scale + shift: the one rounding of mean scale is 2^-15 of the step of x's
     // own bf16 grid near its mean
     F2 scale[4], shift[4];
+    float k[8], t[8];
+    eight_groups(c0, cg, [&](int e, int g) {
+      const float2 st = sh[g - first];
+      k[e] = st.y * (e & 1 ? bf16_hi(gm[e / 2]) : bf16_lo(gm[e / 2]));
+      t[e] = fmaf(-st.x, k[e], e & 1 ? bf16_hi(bt[e / 2]) : bf16_lo(bt[e / 2]));
+    });
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float k[2], t[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int c = c0 + 2 * j + e;
-        const float2 st = sh[c / cg - first];
-        k[e] = st.y * (e ? bf16_hi(gm[j]) : bf16_lo(gm[j]));
-        t[e] = fmaf(-st.x, k[e], e ? bf16_hi(bt[j]) : bf16_lo(bt[j]));
-      }
-      scale[j] = f2(k[0], k[1]);
-      shift[j] = f2(t[0], t[1]);
+      scale[j] = f2(k[2 * j], k[2 * j + 1]);
+      shift[j] = f2(t[2 * j], t[2 * j + 1]);
     }
     const uint16_t *src = x + c0;
     uint16_t *dst = p.y + (row0 + lane) * p.ldy + c0;
@@ -458,21 +469,19 @@ __global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(const GroupNormAr
 struct Octet {
   F2 minus_mean[4], rstd[4], gamma[4], beta[4];
   __device__ __forceinline__ void load(const GroupNormArgs &p, int b, int c0, int cg) {
+    float m[8], r[8], gm[8], bt[8];
+    eight_groups(c0, cg, [&](int e, int g) {
+      m[e] = -p.mean[b * p.G + g];
+      r[e] = p.rstd[b * p.G + g];
+      gm[e] = p.gamma ? bf16_lo(p.gamma[c0 + e]) : 1.0f;
+      bt[e] = p.beta ? bf16_lo(p.beta[c0 + e]) : 0.0f;
+    });
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float m[2], r[2], g[2], t[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int c = c0 + 2 * j + e, at = b * p.G + c / cg;
-        m[e] = -p.mean[at];
-        r[e] = p.rstd[at];
-        g[e] = p.gamma ? bf16_lo(p.gamma[c]) : 1.0f;
-        t[e] = p.beta ? bf16_lo(p.beta[c]) : 0.0f;
-      }
-      minus_mean[j] = f2(m[0], m[1]);
-      rstd[j] = f2(r[0], r[1]);
-      gamma[j] = f2(g[0], g[1]);
-      beta[j] = f2(t[0], t[1]);
+      minus_mean[j] = f2(m[2 * j], m[2 * j + 1]);
+      rstd[j] = f2(r[2 * j], r[2 * j + 1]);
+      gamma[j] = f2(gm[2 * j], gm[2 * j + 1]);
+      beta[j] = f2(bt[2 * j], bt[2 * j + 1]);
     }
   }
   // xh and dv of the channels 2 j, 2 j + 1
@@ -647,11 +656,15 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_dx_kernel(const GroupNormA
     const int c0 = ch0 + o * 8;
     if (o != oct) ch.load(p, b, c0, cg);
     F2 m1[4], m2[4];
+    float s1[8], s2[8];
+    eight_groups(c0, cg, [&](int e, int g) {
+      s1[e] = sh[g - first].x;
+      s2[e] = sh[g - first].y;
+    });
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 s = sh[(c0 + 2 * j) / cg - first], t = sh[(c0 + 2 * j + 1) / cg - first];
-      m1[j] = f2(s.x, t.x);
-      m2[j] = f2(s.y, t.y);
+      m1[j] = f2(s1[2 * j], s1[2 * j + 1]);
+      m2[j] = f2(s2[2 * j], s2[2 * j + 1]);
     }
     const uint16_t *xs = x0 + o * 8, *ds = d0 + o * 8;
     uint16_t *dst = p.dx + (row0 + lane) * p.lddx + c0;
