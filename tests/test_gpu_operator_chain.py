@@ -231,3 +231,58 @@ def test_side_stream_and_two_replayed_graphs():
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(want, res))
     assert B.sq_get_device_status() == B.SQ_OK
+
+
+def test_empty_batch_and_a_slice_of_wider_features():
+    c = dict(CASES[1])
+    front, ad, x, pos, ids, dy = _make(c.pop("B"), **c)
+    for a in (None, ad):
+        out, saved = front(x[:0], pos[:0], a, None if a is None else a.plan(ids[:0]))
+        g = front.backward(dy[:0].clone(), saved)
+        assert out.shape == (0, front.qkv.N) and g.x.shape == x[:0].shape
+        assert not g.gamma.any() and not g.beta.any()
+        assert (g.A is None) if a is None else not (g.A.any() or g.B.any())
+    C = x.shape[2]
+    wide = torch.full((*x.shape[:2], C + 80), float("nan"), dtype=BF, device="cuda")
+    part = wide[:, :, 40:40 + C]
+    part.copy_(x)
+    plan = ad.plan(ids)
+    want, got = front(x, pos, ad, plan), front(part, pos, ad, plan)
+    assert torch.equal(want[0], got[0])
+    a, b = front.backward(dy.clone(), want[1]), front.backward(dy.clone(), got[1])
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+    assert B.sq_get_device_status() == B.SQ_OK
+
+
+def test_host_threads_on_streams_of_their_own():
+    """Four threads make the same calls at once, each on its stream."""
+    import threading
+    c = dict(CASES[1])
+    front, ad, x, pos, ids, dy = _make(c.pop("B"), **c)
+    plan, rows, layer = ad.plan(ids), x.view(-1, x.shape[2]), front.qkv
+    torch.cuda.synchronize()
+    results = {}
+
+    def run(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(30):
+                y, t = B.sq_lora_forward(rows, ad.A, ad.B, ad.scale, plan, None)
+                grads = B.sq_lora_backward(dy, rows, t, ad.A, ad.B, ad.scale, plan, None)
+                h = B.sq_group_norm_forward(x, 32, front.gamma, front.beta, act=front.act)
+                g = B.sq_group_norm_backward(x, x, 32, front.gamma, front.beta, *h[1:])
+                d = B.sq_dualscale_seglinear_input_grad(dy, layer.wq, layer.s_w, None, layer.seg)
+                q = B.sq_rope_forward(dy, pos, front.inv_freq, front.head_dim,
+                                      axis_pairs=front.axis_pairs)
+        stream.synchronize()
+        results[i] = [y, *grads, *h, *g, d, q]
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert len(results) == 4
+    for i in range(1, 4):
+        assert all(torch.equal(a, b) for a, b in zip(results[0], results[i]))
+    assert B.sq_get_device_status() == B.SQ_OK

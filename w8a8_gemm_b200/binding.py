@@ -95,8 +95,8 @@ class Segments:
         return self.n_seg if self.mode == SQ_SEG_INPUT else 1
 
     def _c(self):
-        return _c_segments(self.mode, None if self.offsets is None else tuple(self.offsets),
-                           self.n_groups, self.flags)
+        offsets = None if self.offsets is None else tuple(map(int, self.offsets))
+        return _c_segments(self.mode, offsets, self.n_groups, self.flags)
 
 
 @functools.lru_cache(maxsize=256)
@@ -106,7 +106,7 @@ def _c_segments(mode, offsets, n_groups, flags):
     if offsets is None:
         arr, n_seg, ptr = None, 1, ctypes.POINTER(ctypes.c_int32)()
     else:
-        arr = (ctypes.c_int32 * len(offsets))(*[int(v) for v in offsets])
+        arr = (ctypes.c_int32 * len(offsets))(*offsets)
         n_seg, ptr = len(offsets) - 1, ctypes.cast(arr, ctypes.POINTER(ctypes.c_int32))
     return _Segments(mode, n_seg, ptr, n_groups, flags), arr
 
