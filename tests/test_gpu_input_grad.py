@@ -76,3 +76,30 @@ def test_no_rows_capture_and_a_shared_workspace():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(a, one) and torch.equal(b, two)
+
+
+@pytest.mark.parametrize("M,N,K,mode,n,G,divisor", [
+    (1, 1536, 128, B.SQ_SEG_NONE, 1, 1, True), (256, 1500, 1920, B.SQ_SEG_INPUT, 4, 1, False),
+    (257, 1536, 896, B.SQ_SEG_OUTPUT, 4, 4, True), (200, 6000, 16, B.SQ_SEG_NONE, 1, 1, False),
+    (700, 2000, 656, B.SQ_SEG_NONE, 1, 1, True), (1025, 1600, 768, B.SQ_SEG_INPUT, 6, 1, False),
+    (3, 4095, 1808, B.SQ_SEG_NONE, 1, 1, True)])
+def test_long_contractions_of_few_tiles(M, N, K, mode, n, G, divisor):
+    """Several pairs of blocks share a tile's contraction: values, the rows and
+    columns past the last left alone, the same bits from a replayed graph."""
+    seg, wq, s_w, d, g = _layer(N, K, mode, n, G, divisor, 0, seed=N)
+    ld = (N + 7) // 8 * 8
+    dy = torch.full((M, ld + 8), float("nan"), dtype=BF, device="cuda")[:, :N]
+    dy.copy_(torch.randn(M, N, generator=g, device="cuda"))
+    out = torch.full((M + 2, K + 8), 4.0, dtype=BF, device="cuda")
+    B.sq_dualscale_seglinear_input_grad(dy, wq, s_w, d, seg, dx=out[:M, :K])
+    w = ref.dequantized(_codes(wq, 0), s_w, d, mode, seg.offsets, G)
+    ref.check(out[:M, :K].contiguous(), *ref.input_grad(dy, w), "dx")
+    assert (out[:, K:] == 4.0).all() and (out[M:] == 4.0).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = B.sq_dualscale_seglinear_input_grad(dy, wq, s_w, d, seg)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again, out[:M, :K])
+    assert B.sq_get_device_status() == B.SQ_OK

@@ -14,7 +14,8 @@
 // the contraction) by TMA into a ring of stages, 128-byte swizzled; W~ lies
 // contiguous along the output, an MN-major operand.  The sums are fp32 in tensor
 // memory, in two buffers, so that a tile's epilogue runs under the next tile's
-// products.  What bounds it is the way of the operands from L2 to an SM, about
+// products.  Where there are few tiles, several pairs of a cluster share one's
+// contraction and add their sums in a fixed order.  What bounds it is the way of the operands from L2 to an SM, about
 // 61 bytes a clock: one block by itself with 128 x 256 tiles fetches 48 KB for
 // 512 clocks of products, a pair 32 KB a block.
 #include <cooperative_groups.h>
@@ -121,6 +122,7 @@ struct GemmSmem {
 struct GradArgs {
   int32_t M, K;         // output rows and columns
   int32_t num_n_tiles, num_tiles, num_kb;
+  int32_t splits;       // pairs that share a tile's contraction
   uint16_t *dx;
   int64_t lddx;
   int *status;
@@ -141,6 +143,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   using L = GemmSmem<BN>;
   constexpr int STAGES = L::STAGES;
   constexpr int COLS = 2 * BN;  // two accumulator buffers
+  constexpr int kPartRow = BN + 4;  // floats
+  static_assert(BM * kPartRow * 4 <= L::BARS, "partial sums reuse the stages");
   extern __shared__ uint8_t smem_raw[];
   // the same offset in both blocks: the window starts at the same address
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -154,8 +158,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   cg::cluster_group cluster = cg::this_cluster();
-  const uint32_t rank = cluster.block_rank();  // block of the pair
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  // A cluster has one pair, or the pairs that share a tile's contraction.
+  const uint32_t even = cluster.block_rank() & ~1u, rank = cluster.block_rank() & 1u;
+  const uint32_t both = 3u << even;
+  const int pair = static_cast<int>(even >> 1);
+  const int first = blockIdx.x / (2 * p.splits), step = gridDim.x / (2 * p.splits);
+  const int kb_lo = p.num_kb * pair / p.splits;
+  const int steps = p.num_kb * (pair + 1) / p.splits - kb_lo;  // of 64 terms
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -192,25 +201,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       bool gave_up = false;
       // the first tile's rows of dy, as many stages as there are
       if (first < p.num_tiles) {
-        early = p.num_kb < STAGES ? p.num_kb : STAGES;
-        for (int kb = 0; kb < early; ++kb) {
-          if (rank == 0) mbar_arrive_expect_tx(&full[kb], 2 * L::STAGE);
-          tma_load_2d_pair(smem + kb * L::STAGE, &tmA, cluster_addr(&full[kb], 0), kb * BK,
-                           (first / p.num_n_tiles * 2 + rank) * BM);
+        early = steps < STAGES ? steps : STAGES;
+        for (int i = 0; i < early; ++i) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[i], 2 * L::STAGE);
+          tma_load_2d_pair(smem + i * L::STAGE, &tmA, cluster_addr(&full[i], even),
+                           (kb_lo + i) * BK, (first / p.num_n_tiles * 2 + rank) * BM);
         }
       }
       grid_dependency_wait();
       for (int tile = first; tile < p.num_tiles; tile += step) {
         const int row = (tile / p.num_n_tiles * 2 + rank) * BM;
         const int col = tile % p.num_n_tiles * BN + rank * (BN / 2);
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        for (int i = 0; i < steps; ++i) {
+          const int kb = kb_lo + i;
           if (!wait_bar(&empty[stage], phase ^ 1, abort_flag, p.status)) {
             gave_up = true;
             goto producer_done;
           }
           uint8_t *sa = smem + stage * L::STAGE;
-          const uint32_t bar = cluster_addr(&full[stage], 0);
-          if (tile != first || kb >= early) {
+          const uint32_t bar = cluster_addr(&full[stage], even);
+          if (tile != first || i >= early) {
             if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * L::STAGE);
             tma_load_2d_pair(sa, &tmA, bar, kb * BK, row);
           }
@@ -255,21 +265,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         fence_cluster();  // the other block's reads of this buffer come before
         tc_fence_after();
         const uint32_t acc = tmem_base + buf * BN;
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        for (int i = 0; i < steps; ++i) {
           if (!wait_bar(&full[stage], phase, abort_flag, p.status)) goto mma_exit;
           tc_fence_after();
           const uint32_t sa = smem_u32(smem + stage * L::STAGE), sb = sa + L::A;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
             mma_bf16_pair(acc, sdesc_kmajor_sw128(sa + kk * 32),
-                          sdesc_mnmajor_sw128(sb + kk * 2048, 8192), idesc, (kb | kk) != 0);
-          mma_commit_pair(&empty[stage]);
+                          sdesc_mnmajor_sw128(sb + kk * 2048, 8192), idesc, (i | kk) != 0);
+          mma_commit_pair(&empty[stage], both);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
           }
         }
-        mma_commit_pair(&acc_full[buf]);
+        mma_commit_pair(&acc_full[buf], both);
       }
     mma_exit:
       mma_commit_pair_here(mma_done);
@@ -293,6 +303,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tmem_ld_32x32b_x32(src + c, r);
         tmem_ld_wait();
         const int col = nt * BN + c;
+        if (p.splits > 1) {  // this pair's sums: in the stages, all of which have been used
+          float *to = reinterpret_cast<float *>(smem) + (quarter * 32 + lane) * kPartRow + c;
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<uint4 *>(to + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+          continue;
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {  // K % 16 == 0: 8 columns are all in or all out
           const int c8 = col + q * 8;
@@ -309,13 +326,35 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[buf], even));
     }
   }
 
   __syncwarp();
   tc_fence_before();
-  cluster.sync();  // no products and no arrivals under way in either block
+  cluster.sync();  // no products and no arrivals under way in any block
+  if (p.splits > 1) {
+    // The pairs' sums of the tile, added in their order: a block a share of its rows.
+    const int rows = BM / p.splits, nt = first % p.num_n_tiles;
+    for (int e = threadIdx.x; e < rows * (BN / 8); e += kGemmThreads) {
+      const int m = pair * rows + e / (BN / 8), c = e % (BN / 8) * 8;
+      float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      for (int q = 0; q < p.splits; ++q) {
+        const float4 *src = reinterpret_cast<const float4 *>(
+            cluster.map_shared_rank(reinterpret_cast<float *>(smem), 2 * q + rank) +
+            m * kPartRow + c);
+        const float4 a = src[0], b = src[1];
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+      }
+      const int row = (first / p.num_n_tiles * 2 + rank) * BM + m, c8 = nt * BN + c;
+      if (row < p.M && c8 < p.K && store_ok(p.status, c8 + 8 <= p.lddx))
+        *reinterpret_cast<uint4 *>(p.dx + static_cast<int64_t>(row) * p.lddx + c8) =
+            make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                       bf16x2(v[6], v[7]));
+    }
+    cluster.sync();  // no block leaves while its sums are read
+  }
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -341,7 +380,8 @@ sq_status tensor_map_2d(CUtensorMap *map, const void *ptr, int64_t inner, int64_
 }
 
 template <int BN>
-sq_status run_gemm(const InputGradRequest &r, const uint16_t *w, int sms, cudaStream_t stream) {
+sq_status run_gemm(const InputGradRequest &r, const uint16_t *w, int splits, int sms,
+                   cudaStream_t stream) {
   using L = GemmSmem<BN>;
   static_assert(L::BYTES <= 232448, "dynamic shared memory above the per-block limit");
   CUtensorMap tmA, tmB;
@@ -367,7 +407,8 @@ sq_status run_gemm(const InputGradRequest &r, const uint16_t *w, int sms, cudaSt
     attr_set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * (p.num_tiles < sms / 2 ? p.num_tiles : sms / 2));
+  p.splits = splits;
+  cfg.gridDim = dim3(2 * splits * (p.num_tiles < sms / 2 ? p.num_tiles : sms / 2));
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = L::BYTES;
   cfg.stream = stream;
@@ -375,7 +416,7 @@ sq_status run_gemm(const InputGradRequest &r, const uint16_t *w, int sms, cudaSt
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = 2 * splits;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -413,8 +454,16 @@ sq_status launch_input_grad(const InputGradRequest &r, cudaStream_t stream) {
   auto cost = [&](int64_t bn) {
     return (mt * ((r.K + bn - 1) / bn) + sms / 2 - 1) / (sms / 2) * (BM + bn / 2);
   };
-  return cost(256) <= cost(128) ? run_gemm<256>(r, w, sms, stream)
-                                : run_gemm<128>(r, w, sms, stream);
+  // Few tiles: two or four pairs share each one's contraction, where it is long
+  // enough to pay for the sums' way through distributed shared memory (about 3
+  // us) and a GPU of 148 SMs has room for all the clusters (15 of eight blocks,
+  // 33 of four).  200 rows: 3840 -> 1920 18.0 us by four pairs, 22.1 by two, 27.7 by
+  // one; 1536 -> 1536 13.5, 14.6, 15.4; 384 -> 768 10.5, 10.5, 9.1.
+  const int64_t tiles = mt * ((r.K + 127) / 128), kb = (r.N + BK - 1) / BK;
+  if (tiles <= 15 && kb >= 24) return run_gemm<128>(r, w, 4, sms, stream);
+  if (tiles <= 33 && kb >= 24) return run_gemm<128>(r, w, 2, sms, stream);
+  return cost(256) <= cost(128) ? run_gemm<256>(r, w, 1, sms, stream)
+                                : run_gemm<128>(r, w, 1, sms, stream);
 }
 
 }  // namespace sq

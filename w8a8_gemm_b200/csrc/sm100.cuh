@@ -367,12 +367,13 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
       : "memory");
 }
 
-// The same for a pair's operations, on the barrier at this offset in both blocks.
-__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
+// The same for a pair's operations, on the barrier at this offset in the blocks of
+// the cluster that `blocks` has bits for.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar, uint32_t blocks) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(static_cast<uint16_t>(blocks))
       : "memory");
 }
 
