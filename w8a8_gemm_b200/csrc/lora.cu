@@ -301,6 +301,7 @@ struct ContractSmem {
 template <int RT, bool TRANS, int TERMS>
 __global__ void __launch_bounds__(kContractThreads)
     lora_contract_kernel(const __grid_constant__ CUtensorMap tm_in,
+                         const __grid_constant__ CUtensorMap tm_in32,
                          const __grid_constant__ CUtensorMap tm_w, const ContractArgs p) {
   using S = ContractSmem<RT>;
   constexpr int STAGES = S::kStages;
@@ -410,8 +411,11 @@ __global__ void __launch_bounds__(kContractThreads)
       __syncwarp();
     } else if (warp >= 4 && !run) {
       // ------------------------------------------------- scattered rows: copies
-      // This warp's 32 rows, four a copy instruction.
+      // This warp's 32 rows: a box where they are neighbours (rows ascend within a
+      // tile), else four a copy instruction.
       const int first = (warp - 4) * 32, c = lane & 7;
+      const int row0 = rec[4 + first];
+      const bool box = first + 32 <= count && rec[4 + first + 31] - row0 == 31;
       int32_t rows[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) rows[i] = rec[4 + first + i * 4 + (lane >> 3)];
@@ -424,6 +428,14 @@ __global__ void __launch_bounds__(kContractThreads)
         if (lane == 0)
           ok = bounded_wait(&empty[st], phase ^ 1, abort_flag, p.status, SQ_ERR_DEVICE_TIMEOUT);
         if (!__shfl_sync(~0u, ok, 0)) break;
+        if (box) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&full[st], 4096);
+            tma_load_2d(smem + st * S::kStage + first * 128, &tm_in32, &full[st],
+                        c_lo + step * 64, row0);
+          }
+          continue;
+        }
         const int col = c_lo + step * 64 + c * 8;
         const bool in_cols = col < p.C;
         const uint32_t to = smem_u32(smem + st * S::kStage);
@@ -718,8 +730,10 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const FewArgs p) 
 // the SM an element meets one 16-byte shared load and store and an addition:
 // with the products on the warp-level path, whose operands pass through the
 // same load pipe, that pipe was the bound (8858 x 6144, rank 64: 59 us).
-// Scattered rows of base are copied by four warps (1501 ragged rows, 1536 -> 2304
-// in fp32: 22.8 us with the contraction, 25.7 with two warps).  Rows without an adapter are
+// Where a tile's rows are not neighbours, four warps take 32 rows of base each, as
+// boxes or by copies, and begin before the contraction has ended (1501 ragged
+// rows, 1536 -> 2304 in fp32: 18.9 us with the contraction; 21.0 when they wait
+// for it, 25.7 with two warps).  Rows without an adapter are
 // copied from base (left alone when out is base).
 struct ExpandArgs {
   const int32_t *plan;
@@ -732,7 +746,7 @@ struct ExpandArgs {
   int *status;
 };
 struct ExpandMaps {
-  CUtensorMap base, out, w, v;
+  CUtensorMap base, base32, out, w, v;  // rows of a box: 128, 32, 32
 };
 
 constexpr int kExpandWarps = 8;                            // adding and storing
@@ -840,7 +854,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   Units u;
   u.init(p.plan, fits ? p.plan[3] : 0, p.L, (p.C + SLAB - 1) / SLAB);
   const bool has_base = p.base != nullptr, in_place = p.base == p.out;
-  if (warp != 0) {
+  if (warp != 0 && warp < 2 + kExpandWarps) {
     grid_dependency_wait();
     if constexpr (TRANS) grid_dependency_launch();  // the outer products run beside
   }
@@ -1112,6 +1126,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       const int4 h = *reinterpret_cast<const int4 *>(rec);
       if (h.x >= p.L && in_place) continue;
       const bool copies = has_base && h.w == 0;
+      const int w0 = (warp - 2 - kExpandWarps) * 32, row0 = rec[4 + w0];
+      // neighbours (rows ascend within a tile): two boxes
+      const bool box = copies && w0 + 32 <= h.y && rec[4 + w0 + 31] - row0 == 31;
       int32_t rows[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) rows[i] = copies ? rec[4 + r0 + 2 * i] : 0;
@@ -1123,9 +1140,17 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         if (lane == 0) ok = bounded_wait(&empty[st], parity, abort_flag, p.status, kTimeout);
         ok = __shfl_sync(~0u, ok, 0);
         if (!ok) break;
-        if (!copies) {
+        if (!copies || box) {
           late.catch_up(lane);
-          if (lane == 0) mbar_arrive(&full[st]);
+          if (lane == 0 && box) {
+            const int c0 = (u.slab + i) * SLAB;
+            uint8_t *to = smem + st * S::kStage + w0 * 128;
+            mbar_arrive_expect_tx(&full[st], 8192);
+            tma_load_2d(to, &maps.base32, &full[st], c0, row0);
+            tma_load_2d(to + 16384, &maps.base32, &full[st], c0 + BOX, row0);
+          } else if (lane == 0) {
+            mbar_arrive(&full[st]);
+          }
           continue;
         }
         const int col = (u.slab + i) * SLAB + q * (16 / E);
@@ -1678,8 +1703,9 @@ cudaError_t bf16_map(CUtensorMap *map, const void *ptr, int64_t d0, int64_t d1, 
 
 template <int RT, bool TRANS, int TERMS>
 cudaError_t run_contract(const uint16_t *w, const ContractArgs &a, cudaStream_t stream) {
-  CUtensorMap tm_in, tm_w;
+  CUtensorMap tm_in, tm_in32, tm_w;
   cudaError_t e = bf16_map(&tm_in, a.in, a.C, a.M, 0, a.ld, kTileRows);
+  if (e == cudaSuccess) e = bf16_map(&tm_in32, a.in, a.C, a.M, 0, a.ld, 32);
   if (e == cudaSuccess)
     e = TRANS ? bf16_map(&tm_w, w, a.R, a.C, a.L, a.R, 64)
               : bf16_map(&tm_w, w, a.C, a.R, a.L, a.C, RT);
@@ -1691,7 +1717,7 @@ cudaError_t run_contract(const uint16_t *w, const ContractArgs &a, cudaStream_t 
     slices *= 2;
   return launch<lora_contract_kernel<RT, TRANS, TERMS>>(
       dim3(static_cast<unsigned>(a.max_tiles), slices), kContractThreads,
-      ContractSmem<RT>::kBytes, slices, 1, stream, tm_in, tm_w, a);
+      ContractSmem<RT>::kBytes, slices, 1, stream, tm_in, tm_in32, tm_w, a);
 }
 
 template <int RT, bool TRANS, bool F32>
@@ -1702,6 +1728,8 @@ cudaError_t run_expand(const uint16_t *w, const uint16_t *v, const ExpandArgs &a
   const void *base = a.base ? a.base : a.out;  // not read without a base
   cudaError_t e = tile_map(&maps.base, F32, base, a.C, a.M, 0, a.base ? a.ld_base : a.ld_out,
                            kTileRows);
+  if (e == cudaSuccess)
+    e = tile_map(&maps.base32, F32, base, a.C, a.M, 0, a.base ? a.ld_base : a.ld_out, 32);
   if (e == cudaSuccess) e = tile_map(&maps.out, F32, a.out, a.C, a.M, 0, a.ld_out, 32);
   if (e == cudaSuccess)
     e = TRANS ? bf16_map(&maps.w, w, a.C, a.R, a.L, a.C, RT)
