@@ -389,3 +389,29 @@ def test_backward_kernels_side_by_side_keep_the_streams_order(M, K, N, R, L, spr
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("K,N,R", [(200, 328, 24), (1536, 520, 128)])
+def test_requests_of_lengths_around_the_boxes(K, N, R, out):
+    """Tiles put together from several requests: 32 and 64 neighbouring rows come
+    as boxes wherever they begin, others row by row."""
+    lengths = [31, 32, 33, 64, 1, 95, 63, 96, 65, 128, 7, 160, 32, 64, 130, 5, 224, 33]
+    L = 3
+    ids = torch.cat([torch.full((n,), i * 5 % (L + 1) - 1) for i, n in enumerate(lengths)])
+    M = len(ids)
+    p = _problem(M, K, N, R, L, seed=31, spread="one", out=out)
+    p["ids"] = ids.to(torch.int32).cuda()
+    plan = B.sq_lora_plan(p["ids"], L)
+    y, t = B.sq_lora_forward(p["x"], p["A"], p["B"], p["scale"], plan, p["base"])
+    v, e, T, eT = ref.lora_forward(p["x"], p["A"], p["B"], p["scale"], p["ids"], p["base"], out)
+    some = p["ids"] >= 0
+    ref.check(y, v, e, "y")
+    ref.check(t[some], T[some], eT[some], "t")
+    want = ref.lora_backward(p["dy"], p["x"], t, p["A"], p["B"], p["scale"], p["ids"], p["dx_base"],
+                             out)
+    got = B.sq_lora_backward(p["dy"], p["x"], t, p["A"], p["B"], p["scale"], plan, p["dx_base"],
+                             grad_dtype=out)
+    for name, value in zip(("dA", "dB", "dx"), got):
+        ref.check(value, *want[name], name)
+    assert B.sq_get_device_status() == B.SQ_OK

@@ -260,7 +260,8 @@ __device__ __forceinline__ void split_terms(float4 v, uint2 (&out)[TERMS]) {
 // dt[m][j] = scale[a] sum_c in[m][c] W(j, c), W(j, c) = w[a][c][j] (TRANS true:
 // B, an operand whose rows run along the contraction).  One block per row tile and slice of the contracted
 // dimension: TMA brings the tile's rows as a box, 64 columns a stage, where they
-// are neighbours (else a warp copies them), and the weight's box beside them;
+// are neighbours (else four warps take 32 each, as a box or by copies), and the
+// weight's box beside them;
 // one thread issues tcgen05.mma (M = 128, N = RT, sums in tensor memory), so that
 // reading the rows costs the SM next to no instructions.  The blocks of a cluster hold the slices of one tile and add
 // their partial sums through distributed shared memory in a fixed order.  The
@@ -1187,7 +1188,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 // scale) and dA[a][j][k] (src x, v dt, f = 1, stored transposed).  A cluster
 // takes a slab of 128 columns c; its blocks take equal shares of the row tiles
 // of all adapters in order, 64 rows a stage: src's rows as a TMA box where 64
-// neighbours are the adapter's (else a warp copies them) and v's box; both are
+// neighbours are the adapter's (else boxes of 32, or copies by a warp) and v's box; both are
 // operands whose rows run along the contraction, M = 128 columns of src by N =
 // RT, sums in tensor memory, one buffer in use and one being stored.  v is zero
 // in the rows past a tile's last, where src repeats a row of the tile.
@@ -1212,7 +1213,7 @@ struct OuterArgs {
   int *status;
 };
 struct OuterMaps {
-  CUtensorMap src[2], v[2];
+  CUtensorMap src[2], src32[2], v[2];  // rows of a box: 64, 32, 64
 };
 
 constexpr int kOuterThreads = 192;  // producer, MMA issuer, four storing warps
@@ -1263,6 +1264,7 @@ __global__ void __launch_bounds__(kOuterThreads, OuterSmem<RT, TERMS>::kPerSm)
   const bool second = slab >= p.slabs0;
   const OuterSide sd = second ? p.side[1] : p.side[0];
   const CUtensorMap *tm_src = second ? &maps.src[1] : &maps.src[0];
+  const CUtensorMap *tm_src32 = second ? &maps.src32[1] : &maps.src32[0];
   const CUtensorMap *tm_v = second ? &maps.v[1] : &maps.v[0];
   const int c0 = (slab - (second ? p.slabs0 : 0)) * kOuterSlab;
 
@@ -1354,22 +1356,40 @@ __global__ void __launch_bounds__(kOuterThreads, OuterSmem<RT, TERMS>::kPerSm)
     for (int tile = t_lo; tile < t_hi && ok; ++tile) {
       read(tile + 2, after);
       const int4 h = now.h;
-      const int first_row = __shfl_sync(~0u, now.rows[0], 0);
       const int halves = (h.y + kOuterRows - 1) / kOuterRows;
       const bool head = h.x != bin_before;
       const bool tail = tile + 1 == t_hi || next.h.x != h.x;
       for (int q = 0; q < halves && ok; ++q) {
-        const bool box = h.w != 0 && (q + 1) * kOuterRows <= h.y;
+        // The stage's two groups of 32 rows, a row a lane: neighbours (rows ascend
+        // within a tile) come as boxes of 64 or 32 rows, others by copies.
+        const int group[2] = {q == 0 ? now.rows[0] : now.rows[2],
+                              q == 0 ? now.rows[1] : now.rows[3]};
+        int at[2];
+        bool boxes[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          at[j] = __shfl_sync(~0u, group[j], 0);
+          boxes[j] = h.y - q * kOuterRows >= 32 * (j + 1) &&
+                     __shfl_sync(~0u, group[j], 31) - at[j] == 31;
+        }
+        const bool box = boxes[0] && boxes[1] && at[1] - at[0] == 32;
+        const int n_boxes = boxes[0] + boxes[1];
         const int st = take((head && q == 0 ? kStageFirst : 0) |
                                 (tail && q == halves - 1 ? kStageLast : 0),
-                            S::kV + (box ? (wide ? 2 : 1) * 8192 : 0));
+                            S::kV + n_boxes * (wide ? 2 : 1) * 4096);
         if (!ok) break;
         uint8_t *src = smem + st * S::kStage;
         if (lane == 0) {
           if (box) {
-            const int row = first_row + q * kOuterRows;
-            tma_load_2d(src, tm_src, &full[st], c0, row);
-            if (wide) tma_load_2d(src + 8192, tm_src, &full[st], c0 + 64, row);
+            tma_load_2d(src, tm_src, &full[st], c0, at[0]);
+            if (wide) tma_load_2d(src + 8192, tm_src, &full[st], c0 + 64, at[0]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (boxes[j]) {
+                tma_load_2d(src + j * 4096, tm_src32, &full[st], c0, at[j]);
+                if (wide) tma_load_2d(src + 8192 + j * 4096, tm_src32, &full[st], c0 + 64, at[j]);
+              }
           }
 #pragma unroll
           for (int s = 0; s < TERMS; ++s)
@@ -1378,25 +1398,28 @@ __global__ void __launch_bounds__(kOuterThreads, OuterSmem<RT, TERMS>::kPerSm)
               tma_load_3d(src + S::kSrc + (s * (RT / 64) + b) * 8192, tm_v, &full[st], b * 64,
                           tile * kTileRows + q * kOuterRows, s);
         }
-        if (box) {
+        if (n_boxes == 2) {
           late.catch_up(lane);
           if (lane == 0) mbar_arrive(&full[st]);
         } else {
           const int c = lane & 15, col = c0 + c * 8;
           const uint32_t to = smem_u32(src) + (c >> 3) * 8192;
           const bool in_cols = col < sd.C;
-          int32_t rows[kOuterRows / 2];  // all exchanged before the first copy
 #pragma unroll
-          for (int i = 0; i < kOuterRows / 2; ++i)
-            rows[i] = __shfl_sync(~0u, q == 0 ? now.rows[i / 16] : now.rows[2 + i / 16],
-                                  (i * 2 + (lane >> 4)) & 31);
-          if (c < 8 || wide) {
+          for (int j = 0; j < 2; ++j) {
+            if (boxes[j]) continue;
+            int32_t rows[16];  // all exchanged before the first copy
 #pragma unroll
-            for (int i = 0; i < kOuterRows / 2; ++i) {
-              // zeros past the tile's last row, which meet zeros of v
-              const bool in = in_cols && q * kOuterRows + i * 2 + (lane >> 4) < h.y;
-              cp_async16(to + swz128(i * 2 + (lane >> 4), c & 7),
-                         sd.src + rows[i] * sd.ld + (in ? col : 0), in);
+            for (int i = 0; i < 16; ++i)
+              rows[i] = __shfl_sync(~0u, group[j], i * 2 + (lane >> 4));
+            if (c < 8 || wide) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                // zeros past the tile's last row, which meet zeros of v
+                const int r = j * 32 + i * 2 + (lane >> 4);
+                const bool in = in_cols && q * kOuterRows + r < h.y;
+                cp_async16(to + swz128(r, c & 7), sd.src + rows[i] * sd.ld + (in ? col : 0), in);
+              }
             }
           }
           cp_async_commit();
@@ -1813,6 +1836,8 @@ cudaError_t run_backward(const LoraRequest &q, cudaStream_t stream) {
     o.status = q.status;
     e = bf16_map(&maps.src[0], q.dy, N, q.M, 0, q.lddy, kOuterRows);
     if (e == cudaSuccess) e = bf16_map(&maps.src[1], q.x, K, q.M, 0, q.ldx, kOuterRows);
+    if (e == cudaSuccess) e = bf16_map(&maps.src32[0], q.dy, N, q.M, 0, q.lddy, 32);
+    if (e == cudaSuccess) e = bf16_map(&maps.src32[1], q.x, K, q.M, 0, q.ldx, 32);
     if (e == cudaSuccess) e = bf16_map(&maps.v[0], vt, q.R, rows, TERMS, q.R, kOuterRows);
     if (e == cudaSuccess) e = bf16_map(&maps.v[1], vdt, q.R, rows, TERMS, q.R, kOuterRows);
     if (e == cudaSuccess)
