@@ -13,7 +13,8 @@
 // partials (a few KB) and reads the rows again, from L2 where they fit.  (One
 // kernel with the rows kept in a cluster's shared memory was measured: clusters
 // of eight with 200 KB a block find room for 120 of 148 SMs, and 2 x 16384 x 320
-// took 34 us in two rounds, 19 in two kernels.)
+// took 34 us in two rounds, 17.3 in two kernels.)  Backward, 4 x 4096 x 640 with
+// SiLU: 26.2 us.
 //
 // The statistics are (count, mean, sum of squares about the mean).  A thread sums
 // x - c and (x - c)^2 over up to 32 rows, c the first of them, in fp32: the sum of

@@ -61,6 +61,7 @@ __device__ __forceinline__ bool plan_fits(const int32_t *plan, int64_t M, int32_
 // One block: a stable counting sort of the rows by adapter.  Warp w owns the
 // rows [w chunk, (w + 1) chunk) and a histogram of its own, so that the order
 // within an adapter, and with it every sum over its rows, is always the same.
+// (Once per batch: 10 us for 8858 rows, 150 for 100,000.)
 constexpr int kPlanWarps = 32;
 __global__ void __launch_bounds__(kPlanWarps * 32) lora_plan_kernel(
     const int32_t *__restrict__ adapter, int32_t M, int32_t L, int32_t *plan, int *status) {
@@ -267,7 +268,8 @@ __device__ __forceinline__ void split_terms(float4 v, uint2 (&out)[TERMS]) {
 // their partial sums through distributed shared memory in a fixed order.  The
 // operand of the second products is stored as bf16 terms by tile, 128 rows each
 // with zeros past the tile's last: scale t (forward, beside t by row in fp32),
-// or dt and t (backward).
+// or dt and t (backward).  Bound by the rows' way from HBM: 8858 x 6144, rank 64,
+// 27 us by itself, of which 24 are at 4.7 TB/s and the rest start and end.
 struct ContractArgs {
   const uint16_t *in;  // as tm_in
   int64_t ld;
@@ -735,7 +737,8 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const FewArgs p) 
 // boxes or by copies, and begin before the contraction has ended (1501 ragged
 // rows, 1536 -> 2304 in fp32: 18.9 us with the contraction; 21.0 when they wait
 // for it, 25.7 with two warps).  Rows without an adapter are
-// copied from base (left alone when out is base).
+// copied from base (left alone when out is base).  8858 x 6144, rank 64, bf16: 38
+// us, 5.7 TB/s.
 struct ExpandArgs {
   const int32_t *plan;
   const void *base;    // nullptr: 0
@@ -1195,6 +1198,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 // An adapter whose tiles lie in one block goes straight to memory.  A block
 // shares at most its first and its last adapter with its neighbours: those
 // partial sums meet in distributed shared memory, added in block order.
+// Bound by the rows' way from HBM: 8858 rows of two adapters, 6144 + 1536 columns,
+// rank 64, 42 us by itself, 34 of them at 4 TB/s (256 bytes a row and stage).
 struct OuterSide {
   const uint16_t *src;  // as the side's map
   int64_t ld;

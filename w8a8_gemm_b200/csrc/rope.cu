@@ -11,7 +11,9 @@
 // them once into shared memory while its loads of the row are in flight.  The
 // angle is formed and reduced to a fraction of a turn in fp64 (a position of a
 // million times a frequency near one has an fp32 product that is off by 0.03
-// rad); sine and cosine of the reduced angle are fp32.
+// rad); sine and cosine of the reduced angle are fp32.  9216 rows of 48 heads of
+// 128, bf16: 38.2 us, 0.91 of the copy rate (51.7 when a thread found its place in
+// the row anew for every unit); 24 rows of 32 heads: 2.5 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
