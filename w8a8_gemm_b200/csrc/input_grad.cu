@@ -15,9 +15,9 @@
 // contiguous along the output, an MN-major operand.  The sums are fp32 in tensor
 // memory, in two buffers, so that a tile's epilogue runs under the next tile's
 // products.  Where there are few tiles, several pairs of a cluster share one's
-// contraction and add their sums in a fixed order.  What bounds it is the way of the operands from L2 to an SM, about
-// 61 bytes a clock: one block by itself with 128 x 256 tiles fetches 48 KB for
-// 512 clocks of products, a pair 32 KB a block.
+// contraction and add their sums in a fixed order.  What bounds it is the way of
+// the operands from L2 to an SM, 40 to 60 bytes a clock: one block by itself with
+// 128 x 256 tiles fetches 48 KB for 512 clocks of products, a pair 32 KB a block.
 // 8858 x 6144 -> 1536: 114 us for the product (1466 TFLOP/s), 121 in all; with one
 // block a tile 122 and 129.  1109 x 1536 -> 1536: 18.9 us.
 #include <cooperative_groups.h>

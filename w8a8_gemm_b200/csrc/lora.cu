@@ -1191,10 +1191,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 // scale) and dA[a][j][k] (src x, v dt, f = 1, stored transposed).  A cluster
 // takes a slab of 128 columns c; its blocks take equal shares of the row tiles
 // of all adapters in order, 64 rows a stage: src's rows as a TMA box where 64
-// neighbours are the adapter's (else boxes of 32, or copies by a warp) and v's box; both are
-// operands whose rows run along the contraction, M = 128 columns of src by N =
-// RT, sums in tensor memory, one buffer in use and one being stored.  v is zero
-// in the rows past a tile's last, where src repeats a row of the tile.
+// neighbours are the adapter's (else boxes of 32, or copies by a warp) and v's
+// box; both are operands whose rows run along the contraction, M = 128 columns of
+// src by N = RT, sums in tensor memory, one buffer in use and one being stored.
+// Past a tile's last row both are zero.
 // An adapter whose tiles lie in one block goes straight to memory.  A block
 // shares at most its first and its last adapter with its neighbours: those
 // partial sums meet in distributed shared memory, added in block order.
