@@ -259,13 +259,14 @@ __device__ __forceinline__ void split_terms(float4 v, uint2 (&out)[TERMS]) {
 // ------------------------------------------------------------------- contract
 // t[m][j] = sum_c in[m][c] W(j, c), W(j, c) = w[a][j][c] (TRANS false: A), or
 // dt[m][j] = scale[a] sum_c in[m][c] W(j, c), W(j, c) = w[a][c][j] (TRANS true:
-// B, an operand whose rows run along the contraction).  One block per row tile and slice of the contracted
-// dimension: TMA brings the tile's rows as a box, 64 columns a stage, where they
-// are neighbours (else four warps take 32 each, as a box or by copies), and the
-// weight's box beside them;
-// one thread issues tcgen05.mma (M = 128, N = RT, sums in tensor memory), so that
-// reading the rows costs the SM next to no instructions.  The blocks of a cluster hold the slices of one tile and add
-// their partial sums through distributed shared memory in a fixed order.  The
+// B, an operand whose rows run along the contraction).  One block per row tile and
+// slice of the contracted dimension: TMA brings the tile's rows as a box, 64
+// columns a stage, where they are neighbours (else four warps take 32 each, as a
+// box or by copies), and the weight's box beside them; one thread issues
+// tcgen05.mma (M = 128, N = RT, sums in tensor memory), so that reading the rows
+// costs the SM next to no instructions.  The blocks of a cluster hold the slices
+// of one tile and add their partial sums through distributed shared memory in a
+// fixed order.  The
 // operand of the second products is stored as bf16 terms by tile, 128 rows each
 // with zeros past the tile's last: scale t (forward, beside t by row in fp32),
 // or dt and t (backward).  Bound by the rows' way from HBM: 8858 x 6144, rank 64,
