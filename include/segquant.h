@@ -689,6 +689,9 @@ typedef enum {
  *   C a multiple of 8, 8..8192; G 1..1024, dividing C; S 1..2^24; B 0..65535;
  *   ld >= C, multiples of 8; x, y 16-byte aligned, gamma and beta 2-byte, mean
  *   and rstd 4-byte; B * S * ld <= 2^44; eps >= 0, finite.
+ * The mean is taken off before anything is multiplied: a group of equal values
+ * gives act(beta) exactly.  A group with an infinity or a NaN has no finite mean,
+ * NaN for rstd and for its outputs; the other groups do not notice.
  * B == 0 is a valid no-op.  Two kernels.
  * sq_group_norm_workspace_bytes: 0 for sizes out of range.
  */
