@@ -119,14 +119,15 @@ __device__ __forceinline__ F2 act(F2 v) {
   if constexpr (ACT == SQ_ACT_NONE) return v;
   return f2_mul(v, gate<ACT>(v));
 }
-// (v g(u))' = g (1 + v u' (1 - g))
+// (v g(u))' = g (1 + v u' (1 - g)).  GELU: g (1 - g) v first, which is 0 where |v| is
+// large, whose cube (v u') may be past the largest number.
 template <int ACT>
 __device__ __forceinline__ F2 act_grad(F2 v) {
   const F2 g = gate<ACT>(v), rest = f2_fma(g, splat(-1.0f), splat(1.0f));
-  F2 w = v;
   if constexpr (ACT == SQ_ACT_GELU)
-    w = f2_mul(v, f2_fma(f2_mul(v, v), splat(3.0f * kGelu3), splat(kGelu)));
-  return f2_mul(g, f2_fma(w, rest, splat(1.0f)));
+    return f2_fma(f2_mul(f2_mul(g, rest), v),
+                  f2_fma(f2_mul(v, v), splat(3.0f * kGelu3), splat(kGelu)), g);
+  return f2_mul(g, f2_fma(v, rest, splat(1.0f)));
 }
 
 // Running statistics of eight channels over the rows a thread has seen.
