@@ -543,7 +543,8 @@ SQ_API sq_status sq_lora_plan(const int32_t *adapter, int64_t M, int32_t n_adapt
  * with adapter a:   t[m] = A[a] x[m],   y[m] = base[m] + scale[a] B[a] t[m].
  * Rows without an adapter: y[m] = base[m] (left alone when y is base) and t[m]
  * is not written.  t is fp32; where y is bf16, scale t enters the second product
- * rounded to bf16; where y is fp32, with 24 bits.  Sums are fp32.
+ * rounded to bf16; where y is fp32, with 24 bits (in steps of 2^-133).  Sums are
+ * fp32.  Infinities and NaN follow the formulas, in the rows that have them.
  *   x      bf16 [M][ldx];  A bf16 [L][R][K], B bf16 [L][N][R], scale fp32 [L]
  *   plan   of sq_lora_plan for this M and L
  *   base   [M][ldbase] of y's type, or NULL for zeros; y [M][ldy] output.  base
@@ -579,7 +580,7 @@ SQ_API sq_status sq_lora_forward(const void *x, int64_t ldx, const void *A, cons
  * an adapter get dx[m] = dx_base[m].  (dL/dbase is dy itself.)  t and dt enter
  * the second products rounded to bf16 where the result is bf16, with 24 bits
  * where it is fp32.  Every sum has a fixed order: the same call gives the same
- * bits.
+ * bits.  Infinities and NaN follow the formulas, as in the forward call.
  *   dy       bf16 [M][lddy];  x, A, B, scale, plan as in the forward call
  *   t        fp32 [M][R] of the forward call
  *   dx_base  bf16 [M][ldbase] or NULL for zeros; dx bf16 [M][lddx] output, or

@@ -245,14 +245,41 @@ __device__ __forceinline__ void store_grad(void *out, int64_t at, float v) {
     static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v);
 }
 
-// v as TERMS bf16 values whose sum has 8 TERMS significant bits, packed in pairs.
+// v as bf16 (nearest even), or as three bf16 values whose sum is v with its 24
+// bits (in steps of 2^-133, the smallest bf16 number), packed in pairs.  Three are
+// cut off towards zero, all of v's sign, and none is zero unless v is (a place
+// that would be holds 2^-40 of v, far below its last bit): an infinite factor then
+// meets terms of one sign, and neither 0 times infinity nor infinity less infinity
+// comes up that the product itself does not have.  For the same reason an infinite
+// or NaN v is one in every place.
+__device__ __forceinline__ void three_terms(float v, uint32_t (&t)[3]) {
+  const uint32_t u = __float_as_uint(v), e = u & 0x7F800000u;
+  if (e == 0x7F800000u) {
+    t[0] = t[1] = t[2] = (u >> 16) | ((u & 0x007FFFFFu) != 0 ? 0x40u : 0u);
+    return;
+  }
+  const uint32_t least =
+      e == 0 ? 0u : (u & 0x80000000u) | (e > (40u << 23) ? e - (40u << 23) : 0x00010000u);
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    const uint32_t w = __float_as_uint(v) & 0xFFFF0000u;
+    v -= __uint_as_float(w);
+    t[s] = ((w & 0x7FFF0000u) != 0 ? w : least) >> 16;
+  }
+}
 template <int TERMS>
 __device__ __forceinline__ void split_terms(float4 v, uint2 (&out)[TERMS]) {
+  static_assert(TERMS == 1 || TERMS == 3, "bf16 or 24 bits");
+  if constexpr (TERMS == 1) {
+    out[0] = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+  } else {
+    uint32_t x[3], y[3], z[3], w[3];
+    three_terms(v.x, x);
+    three_terms(v.y, y);
+    three_terms(v.z, z);
+    three_terms(v.w, w);
 #pragma unroll
-  for (int s = 0; s < TERMS; ++s) {
-    const uint32_t lo = bf16x2(v.x, v.y), hi = bf16x2(v.z, v.w);
-    out[s] = make_uint2(lo, hi);
-    v = make_float4(v.x - bf16_lo(lo), v.y - bf16_hi(lo), v.z - bf16_lo(hi), v.w - bf16_hi(hi));
+    for (int s = 0; s < 3; ++s) out[s] = make_uint2(x[s] | y[s] << 16, z[s] | w[s] << 16);
   }
 }
 
