@@ -29,6 +29,7 @@
 #include <stdint.h>
 
 #include "bf16.cuh"
+#include "input_grad_plan.h"
 #include "sq_internal.h"
 
 namespace cg = cooperative_groups;
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kDeqThreads) dequant_kernel(
 }
 
 // -------------------------------------------------------------------- product
-constexpr int BM = 128, BK = 64;  // rows of a block, terms of a step
+constexpr int BM = kGradTileRows / 2, BK = kGradStep;  // rows of a block, terms of a step
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
 
@@ -124,7 +125,7 @@ struct GemmSmem {
 struct GradArgs {
   int32_t M, K;         // output rows and columns
   int32_t num_n_tiles, num_tiles, num_kb;
-  int32_t splits;       // pairs that share a tile's contraction
+  int32_t splits;       // pairs that share a tile's contraction; above 1 a cluster has one tile
   uint16_t *dx;
   int64_t lddx;
   int *status;
@@ -382,7 +383,7 @@ sq_status tensor_map_2d(CUtensorMap *map, const void *ptr, int64_t inner, int64_
 }
 
 template <int BN>
-sq_status run_gemm(const InputGradRequest &r, const uint16_t *w, int splits, int sms,
+sq_status run_gemm(const InputGradRequest &r, const uint16_t *w, const InputGradPlan &plan,
                    cudaStream_t stream) {
   using L = GemmSmem<BN>;
   static_assert(L::BYTES <= 232448, "dynamic shared memory above the per-block limit");
@@ -394,7 +395,7 @@ sq_status run_gemm(const InputGradRequest &r, const uint16_t *w, int splits, int
   p.M = static_cast<int32_t>(r.M);
   p.K = static_cast<int32_t>(r.K);
   p.num_n_tiles = static_cast<int32_t>((r.K + BN - 1) / BN);
-  p.num_tiles = static_cast<int32_t>((r.M + 2 * BM - 1) / (2 * BM)) * p.num_n_tiles;
+  p.num_tiles = static_cast<int32_t>(plan.tiles);
   p.num_kb = static_cast<int32_t>((r.N + BK - 1) / BK);
   p.dx = r.dx;
   p.lddx = r.lddx;
@@ -409,8 +410,8 @@ sq_status run_gemm(const InputGradRequest &r, const uint16_t *w, int splits, int
     attr_set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  p.splits = splits;
-  cfg.gridDim = dim3(2 * splits * (p.num_tiles < sms / 2 ? p.num_tiles : sms / 2));
+  p.splits = plan.splits;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * plan.splits * plan.clusters));
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = L::BYTES;
   cfg.stream = stream;
@@ -418,7 +419,7 @@ sq_status run_gemm(const InputGradRequest &r, const uint16_t *w, int splits, int
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2 * splits;
+  attr[1].val.clusterDim.x = 2 * plan.splits;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -449,23 +450,8 @@ sq_status launch_input_grad(const InputGradRequest &r, cudaStream_t stream) {
   if (cudaLaunchKernelEx(&cfg, dequant_kernel, r.wq, r.s_w, r.d, r.N, r.K, r.seg, w, r.status) !=
       cudaSuccess)
     return SQ_ERR_CUDA;
-  const int sms = sm_count();
-  // Tile width: a block's time goes with the operand rows that it fetches, 128 +
-  // BN / 2 a step, times the rounds of tiles.
-  const int64_t mt = (r.M + 2 * BM - 1) / (2 * BM);
-  auto cost = [&](int64_t bn) {
-    return (mt * ((r.K + bn - 1) / bn) + sms / 2 - 1) / (sms / 2) * (BM + bn / 2);
-  };
-  // Few tiles: two or four pairs share each one's contraction, where it is long
-  // enough to pay for the sums' way through distributed shared memory (about 3
-  // us) and a GPU of 148 SMs has room for all the clusters (15 of eight blocks,
-  // 33 of four).  200 rows: 3840 -> 1920 18.0 us by four pairs, 22.1 by two, 27.7 by
-  // one; 1536 -> 1536 13.5, 14.6, 15.4; 384 -> 768 10.5, 10.5, 9.1.
-  const int64_t tiles = mt * ((r.K + 127) / 128), kb = (r.N + BK - 1) / BK;
-  if (tiles <= 15 && kb >= 24) return run_gemm<128>(r, w, 4, sms, stream);
-  if (tiles <= 33 && kb >= 24) return run_gemm<128>(r, w, 2, sms, stream);
-  return cost(256) <= cost(128) ? run_gemm<256>(r, w, 1, sms, stream)
-                                : run_gemm<128>(r, w, 1, sms, stream);
+  const InputGradPlan plan = input_grad_plan(r.M, r.N, r.K, sm_count());
+  return plan.bn == 256 ? run_gemm<256>(r, w, plan, stream) : run_gemm<128>(r, w, plan, stream);
 }
 
 }  // namespace sq
