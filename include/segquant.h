@@ -517,6 +517,10 @@ SQ_API sq_status sq_dualscale_seglinear_host_noalloc(const void *x_host, int64_t
  * of this header hold: caller-owned buffers, host-side validation before
  * anything is launched, asynchronous on `stream`; no call keeps state.
  * A workspace belongs to the calls of one stream at a time.
+ * Outputs and the workspace must overlap neither an input nor each other, except
+ * that a call names two as possibly the same buffer: kernels of one call run side
+ * by side.  An overlap is refused (SQ_ERR_INVALID_ARG) where one of the two is a
+ * single run of bytes or both are rows with the same leading dimension.
  * ======================================================================== */
 
 /*

@@ -5,6 +5,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "spans.h"
 #include "sq_internal.h"
 
 namespace sq {
@@ -60,6 +61,15 @@ sq_status check_lora(int64_t M, int64_t N, int64_t K, int32_t R, int32_t L, cons
   return SQ_OK;
 }
 
+// The inputs of an adapter call that are single runs of bytes.
+struct LoraSpans {
+  Span A, B, scale, plan;
+  LoraSpans(int64_t M, int64_t N, int64_t K, int64_t R, int32_t L, const void *a, const void *b,
+            const void *s, const void *p)
+      : A(a, L * R * K * 2), B(b, L * R * N * 2), scale(s, L * int64_t(4)),
+        plan(p, static_cast<int64_t>(lora_plan_words(M, L)) * 4) {}
+};
+
 sq_status rope_common(const void *x, int64_t ldx, void *out, int64_t ldo, sq_out_dtype dtype,
                       const int32_t *positions, const float *inv_freq, const int32_t *axis_pairs,
                       int32_t n_axes, float factor, int64_t M, int32_t H, int32_t D, int32_t rot,
@@ -89,6 +99,11 @@ sq_status rope_common(const void *x, int64_t ldx, void *out, int64_t ldo, sq_out
   if (positions == nullptr || inv_freq == nullptr) return SQ_ERR_INVALID_ARG;
   if (x == out && ldx != ldo) return SQ_ERR_INVALID_ARG;
   if (!aligned(positions, 4) || !aligned(inv_freq, 4)) return SQ_ERR_ALIGNMENT;
+  const int64_t e = dtype == SQ_OUT_F32 ? 4 : 2;
+  const Span from(x, M, cols * e, ldx * e), to(out, M, cols * e, ldo * e);
+  if ((x != out && overlap(to, from)) ||
+      overlaps_any(to, Span(positions, M * n_axes * 4), Span(inv_freq, rot / 2 * 4)))
+    return SQ_ERR_INVALID_ARG;
   SQ_TRY(device_word(&p.status));
   p.x = x;
   p.ldx = ldx;
@@ -166,6 +181,8 @@ sq_status sq_lora_plan(const int32_t *adapter, int64_t M, int32_t n_adapters, in
   if (!lora_sizes_ok(M, n_adapters)) return SQ_ERR_INVALID_ARG;
   if ((M > 0 && adapter == nullptr) || plan == nullptr) return SQ_ERR_INVALID_ARG;
   if (!aligned(adapter, 4) || !aligned(plan, 16)) return SQ_ERR_ALIGNMENT;
+  if (overlap(Span(plan, lora_plan_words(M, n_adapters) * 4), Span(adapter, M * 4)))
+    return SQ_ERR_INVALID_ARG;
   int *status = nullptr;
   SQ_TRY(device_word(&status));
   return from_cuda(launch_lora_plan(adapter, M, n_adapters, plan, status, cs(stream)));
@@ -187,6 +204,15 @@ sq_status sq_lora_forward(const void *x, int64_t ldx, const void *A, const void 
   if (workspace == nullptr || workspace_bytes < lora_workspace_bytes(M, R, n_adapters, f32))
     return SQ_ERR_INVALID_ARG;
   if (!aligned(t, 16) || !aligned(workspace, 16)) return SQ_ERR_ALIGNMENT;
+  const int64_t e = f32 ? 4 : 2;
+  const LoraSpans in(M, N, K, R, n_adapters, A, B, scale, plan);
+  const Span sx(x, M, K * 2, ldx * 2), sy(y, M, N * e, ldy * e), st(t, M * R * 4),
+      sw(workspace, lora_workspace_bytes(M, R, n_adapters, f32)),
+      sb(base, base ? M : 0, N * e, ldbase * e);
+  if ((base != y && overlap(sy, sb)) || overlaps_any(sy, sx, in.A, in.B, in.scale, in.plan) ||
+      overlaps_any(st, sy, sb, sx, in.A, in.B, in.scale, in.plan) ||
+      overlaps_any(sw, st, sy, sb, sx, in.A, in.B, in.scale, in.plan))
+    return SQ_ERR_INVALID_ARG;
   LoraRequest q = {};
   SQ_TRY(device_word(&q.status));
   q.x = static_cast<const uint16_t *>(x);
@@ -233,6 +259,19 @@ sq_status sq_lora_backward(const void *dy, int64_t lddy, const void *x, int64_t 
   if (!aligned(t, 16) || !aligned(workspace, 16) || !aligned(dA, 16) || !aligned(dB, 16))
     return SQ_ERR_ALIGNMENT;
   if (dA == nullptr && (dx == nullptr || M == 0)) return SQ_OK;
+  // The expansion reads A beside the outer products, which write dA and dB.
+  const int64_t e = f32 ? 4 : 2, rank = static_cast<int64_t>(n_adapters) * R;
+  const LoraSpans in(M, N, K, R, n_adapters, A, B, scale, plan);
+  const Span sg(dy, M, N * 2, lddy * 2), sx(x, M, K * 2, ldx * 2), st(t, M * R * 4),
+      sb(dx_base, dx_base ? M : 0, K * 2, ldbase * 2), sd(dx, dx ? M : 0, K * 2, lddx * 2),
+      sA(dA, rank * K * e), sB(dB, rank * N * e),
+      sw(workspace, lora_workspace_bytes(M, R, n_adapters, f32));
+  if ((dx_base != dx && overlap(sd, sb)) ||
+      overlaps_any(sd, sg, sx, st, in.A, in.B, in.scale, in.plan) || overlap(sA, sB) ||
+      overlaps_any(sA, sd, sb, sg, sx, st, in.A, in.B, in.scale, in.plan) ||
+      overlaps_any(sB, sd, sb, sg, sx, st, in.A, in.B, in.scale, in.plan) ||
+      (M > 0 && overlaps_any(sw, sA, sB, sd, sb, sg, sx, st, in.A, in.B, in.scale, in.plan)))
+    return SQ_ERR_INVALID_ARG;
   LoraRequest q = {};
   SQ_TRY(device_word(&q.status));
   q.x = static_cast<const uint16_t *>(x);
@@ -329,6 +368,13 @@ sq_status sq_group_norm_forward(const void *x, int64_t ldx, int64_t B, int64_t S
   SQ_TRY(check_rows(y, B * S, C, ldy));
   if (B == 0) return SQ_OK;
   if (x == y && ldx != ldy) return SQ_ERR_INVALID_ARG;
+  const Span sx(x, B * S, C * 2, ldx * 2), sy(y, B * S, C * 2, ldy * 2), sg(gamma, C * 2),
+      sb(beta, C * 2), sm(mean, B * G * 4), sr(rstd, B * G * 4),
+      sw(workspace, group_norm_workspace_bytes(B, S, C, G));
+  if ((x != y && overlap(sy, sx)) || overlaps_any(sy, sg, sb, sm, sr, sw) ||
+      overlaps_any(sm, sr, sw, sx, sg, sb) || overlaps_any(sr, sw, sx, sg, sb) ||
+      overlaps_any(sw, sx, sg, sb))
+    return SQ_ERR_INVALID_ARG;
   int *status = nullptr;
   SQ_TRY(device_word(&status));
   GroupNormArgs p = group_norm_args(x, ldx, B, S, C, G, gamma, beta, mean, rstd, status);
@@ -353,6 +399,16 @@ sq_status sq_group_norm_backward(const void *dy, int64_t lddy, const void *x, in
   const bool gf32 = grad_dtype == SQ_OUT_F32;
   if (!aligned(dgamma, gf32 ? 4 : 2) || !aligned(dbeta, gf32 ? 4 : 2)) return SQ_ERR_ALIGNMENT;
   if (dx == nullptr && dgamma == nullptr && dbeta == nullptr) return SQ_OK;
+  const Span sd(dy, B * S, C * 2, lddy * 2), sx(x, B * S, C * 2, ldx * 2),
+      so(dx, dx ? B * S : 0, C * 2, lddx * 2), sg(gamma, C * 2), sb(beta, C * 2),
+      sm(mean, B * G * 4), sr(rstd, B * G * 4), sdg(dgamma, C * (gf32 ? 4 : 2)),
+      sdb(dbeta, C * (gf32 ? 4 : 2)),
+      sw(workspace, B > 0 ? group_norm_workspace_bytes(B, S, C, G) : 0);
+  if ((dx != dy && overlap(so, sd)) || overlaps_any(so, sx, sg, sb, sm, sr) ||
+      overlaps_any(sdg, sdb, so, sd, sx, sg, sb, sm, sr) ||
+      overlaps_any(sdb, so, sd, sx, sg, sb, sm, sr) ||
+      overlaps_any(sw, sdg, sdb, so, sd, sx, sg, sb, sm, sr))
+    return SQ_ERR_INVALID_ARG;
   int *status = nullptr;
   SQ_TRY(device_word(&status));
   if (B == 0) {
@@ -395,6 +451,11 @@ sq_status sq_dualscale_seglinear_input_grad(const void *dy, int64_t lddy, const 
   if (workspace_bytes < input_grad_workspace_bytes(N, K)) return SQ_ERR_INVALID_ARG;
   if (!aligned(wq, 16) || !aligned(s_w, 4) || (d && !aligned(d, 4)) || !aligned(workspace, 256))
     return SQ_ERR_ALIGNMENT;
+  const Span sg(dy, M, N * 2, lddy * 2), so(dx, M, K * 2, lddx * 2), swq(wq, N * K),
+      ss(s_w, r.seg.S * N * 4), sd(d, d ? r.seg.G * K * 4 : 0),
+      sw(workspace, input_grad_workspace_bytes(N, K));
+  if (overlaps_any(so, sg, swq, ss, sd, sw) || overlaps_any(sw, sg, swq, ss, sd))
+    return SQ_ERR_INVALID_ARG;
   SQ_TRY(device_word(&r.status));
   r.dy = static_cast<const uint16_t *>(dy);
   r.lddy = lddy;
