@@ -83,6 +83,15 @@ bool plain(const Tensor &t, ScalarType type, int dev) {
   return t.is_cuda() && t.layout() == at::kStrided && t.scalar_type() == type &&
          t.get_device() == dev;
 }
+// For each tensor that a call will write (absent ones left out), before any
+// address is taken: a tensor that shares its storage until the first write (copy
+// on write) gets its own now.  Addresses can then be taken as for reading, which
+// leaves such inputs shared.
+void will_write(std::initializer_list<PyObject *> out) {
+  for (PyObject *o : out)
+    if (const Tensor *t = optional_tensor(o))
+      if (t->is_cuda() && t->layout() == at::kStrided) t->mutable_data_ptr();
+}
 // The device of the tensor that gives a call its sizes: the current one.
 int device_of(const Tensor &t) {
   need(t.is_cuda() && t.get_device() == c10::cuda::current_device());
@@ -177,6 +186,7 @@ PyObject *results(sq_status s, std::initializer_list<Tensor> out) {
 
 // x, A, B, scale, plan, base, y, t, workspace -> (y, t)
 PyObject *lora_forward(PyObject *const *a) {
+  will_write({a[6], a[7], a[8]});
   const Tensor &x = tensor(a[0]), &A = tensor(a[1]), &B = tensor(a[2]);
   const Tensor *base = optional_tensor(a[5]), *y_in = optional_tensor(a[6]),
                *t_in = optional_tensor(a[7]);
@@ -209,6 +219,7 @@ PyObject *lora_forward(PyObject *const *a) {
 // dy, x, t, A, B, scale, plan, dx_base, dx, dA, dB, fp32 gradients, workspace,
 // need_dx, need_weights -> (dA, dB, dx)
 PyObject *lora_backward(PyObject *const *a) {
+  will_write({a[8], a[9], a[10], a[12]});
   const Tensor &dy = tensor(a[0]), &x = tensor(a[1]), &A = tensor(a[3]), &B = tensor(a[4]);
   const Tensor *base = optional_tensor(a[7]), *dx_in = optional_tensor(a[8]),
                *dA_in = optional_tensor(a[9]), *dB_in = optional_tensor(a[10]);
@@ -254,6 +265,7 @@ PyObject *lora_backward(PyObject *const *a) {
 
 // backward, x, positions, inv_freq, head_dim, out, layout, axis_pairs, factor -> (out,)
 PyObject *rope(PyObject *const *a) {
+  will_write({a[5]});
   const Tensor &x = tensor(a[1]), &pos = tensor(a[2]), &inv_freq = tensor(a[3]);
   const Tensor *out_in = optional_tensor(a[5]);
   const int dev = device_of(x);
@@ -294,6 +306,7 @@ PyObject *rope(PyObject *const *a) {
 
 // x, groups, gamma, beta, eps, act, y, workspace -> (y, mean, rstd)
 PyObject *group_norm_forward(PyObject *const *a) {
+  will_write({a[6], a[7]});
   const Tensor &x = tensor(a[0]);
   const Tensor *gamma = optional_tensor(a[2]), *beta = optional_tensor(a[3]),
                *y_in = optional_tensor(a[6]);
@@ -322,6 +335,7 @@ PyObject *group_norm_forward(PyObject *const *a) {
 // dy, x, groups, gamma, beta, mean, rstd, act, dx, fp32 gradients, workspace,
 // need_dx -> (dx, dgamma, dbeta)
 PyObject *group_norm_backward(PyObject *const *a) {
+  will_write({a[8], a[10]});
   const Tensor &dy = tensor(a[0]), &x = tensor(a[1]);
   const Tensor *gamma = optional_tensor(a[3]), *beta = optional_tensor(a[4]),
                *dx_in = optional_tensor(a[8]);
@@ -360,6 +374,7 @@ PyObject *group_norm_backward(PyObject *const *a) {
 // dy, wq, s_w, d, address of the segment table, its groups, its rows of steps, dx,
 // workspace -> (dx,)
 PyObject *input_grad(PyObject *const *a) {
+  will_write({a[7], a[8]});
   const Tensor &dy = tensor(a[0]), &wq = tensor(a[1]);
   const Tensor *d = optional_tensor(a[3]), *dx_in = optional_tensor(a[7]);
   const int dev = device_of(dy);
