@@ -599,12 +599,12 @@ def _whole(name: str, t, dtype, shape, dev: int) -> int:
 
 def _matrix(name: str, t, dtype, shape, dev: int):
     """(address, leading dimension) of a tensor of rows with unit column stride; a
-    single row's stride says nothing and is taken as its length."""
+    single row's stride says nothing: its length up to a multiple of 8 is taken."""
     try:
         if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
             ld, unit = t.stride()
             if shape[0] <= 1:
-                ld = max(ld, (shape[1] + 7) // 8 * 8)
+                ld = (shape[1] + 7) // 8 * 8
             if unit == 1 or shape[1] <= 1 or shape[0] == 0:
                 return t.data_ptr(), ld
     except AttributeError:
@@ -826,8 +826,6 @@ def _rope(call: str, x, positions, inv_freq, head_dim, out, layout, axis_pairs, 
         out = torch.empty(M, cols, dtype=kind, device=dev)
     px, ldx = _matrix("x", x, kind, (M, cols), dev)
     po, ldo = _matrix("out", out, kind, (M, cols), dev)
-    if px == po and M == 1:
-        ldo = ldx
     _check(getattr(lib(), call)(px, ldx, po, ldo, dtype,
                                 _whole("positions", positions, _I32, (M,) if flat else (M, axes),
                                        dev),

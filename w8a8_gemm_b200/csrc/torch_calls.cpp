@@ -110,8 +110,7 @@ struct Rows {
 Rows rows_of(const Tensor &t, ScalarType type, int64_t rows, int64_t cols, int dev) {
   need(plain(t, type, dev) && t.dim() == 2 && t.size(0) == rows && t.size(1) == cols);
   need(t.stride(1) == 1 || cols <= 1 || rows == 0);
-  int64_t ld = t.stride(0);
-  if (rows <= 1) ld = std::max(ld, (cols + 7) / 8 * 8);
+  const int64_t ld = rows <= 1 ? (cols + 7) / 8 * 8 : t.stride(0);
   return {const_cast<void *>(t.const_data_ptr()), ld};
 }
 // [B][S][C] whose samples and rows lie at one row stride.
@@ -291,8 +290,7 @@ PyObject *rope(PyObject *const *a) {
   const sq_rope_layout layout = static_cast<sq_rope_layout>(int32_of(a[6]));
   const float factor = real(a[8]);
   const Tensor out = out_in ? *out_in : empty({M, cols}, type, dev);
-  Rows po = rows_of(out, type, M, cols, dev);
-  if (po.p == px.p && M == 1) po.ld = px.ld;
+  const Rows po = rows_of(out, type, M, cols, dev);
   const auto call = truth(a[0]) ? lib.rope_backward : lib.rope_forward;
   const sq_stream_t stream = stream_on(dev);
   return results(unlocked([&] {
