@@ -13,10 +13,13 @@ import ctypes
 import functools
 import importlib.util
 import os
+import warnings
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
 import torch
+
+from .build import calls_path
 
 # The library: the release build, or another build of it named by the
 # environment variable SQ_LIBRARY (the test suite runs some cases against the
@@ -207,19 +210,23 @@ _native = None
 
 def _calls():
     """The compiled calls of the operators around the quantized linear
-    (csrc/torch_calls.cpp) on this library, or False where they are not built."""
+    (csrc/torch_calls.cpp) on this library, or False (with a warning, once) where
+    there are none for this Python and this torch."""
     global _native
     if _native is None:
         L = lib()
-        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_sqtorch.so")
-        if not os.path.exists(path):
-            _native = False
-        else:
+        path = calls_path()
+        try:
             spec = importlib.util.spec_from_file_location("_sqtorch", path)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
             module.init(L._handle)
             _native = module
+        except (ImportError, OSError, RuntimeError) as e:
+            warnings.warn(f"{os.path.basename(path)} cannot be used ({e}): the operators' calls go "
+                          "through ctypes; python -m w8a8_gemm_b200.build builds it",
+                          RuntimeWarning)
+            _native = False
     return _native
 
 
