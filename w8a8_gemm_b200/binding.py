@@ -19,8 +19,6 @@ from typing import Optional, Sequence
 
 import torch
 
-from .build import calls_path
-
 # The library: the release build, or another build of it named by the
 # environment variable SQ_LIBRARY (the test suite runs some cases against the
 # bounds-checked debug build, libsegquant_debug.so).
@@ -206,6 +204,11 @@ def lib() -> ctypes.CDLL:
 
 
 _native = None
+
+
+def calls_path() -> str:
+    from .build import calls_path as path   # here: python -m w8a8_gemm_b200.build imports this
+    return path()
 
 
 def _calls():
