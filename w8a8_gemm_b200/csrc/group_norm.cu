@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(const GroupNormAr
   join_stats(p, b, first, groups, sh, sums);
   if (blockIdx.x == 0)
     for (int g = threadIdx.x; g < groups; g += kThreads)
-      if (store_ok(p.status, b < p.B && first + g < p.G)) {
+      if (store_ok(p.status, b * p.G + first + g < p.B * p.G)) {
         p.mean[b * p.G + first + g] = sh[g].x;
         p.rstd[b * p.G + first + g] = sh[g].y;
       }
@@ -457,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(const GroupNormAr
     }
     const uint16_t *src = x + c0;
     uint16_t *dst = p.y + (row0 + lane) * p.ldy + c0;
+    const uint16_t *end = p.y + (static_cast<int64_t>(p.B) * p.S - 1) * p.ldy + p.C;
     for (int left = mine; left > 0; left -= kAhead) {
       if (!loaded) load(src, left);
       loaded = false;
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(const GroupNormAr
           const float2 z = f2_get(act<ACT>(f2_fma(d, scale[j], beta[j])));
           y[j] = bf16x2(z.x, z.y);
         }
-        if (store_ok(p.status, row0 + rows <= static_cast<int64_t>(p.B) * p.S && c0 + 8 <= p.ldy))
+        if (store_ok(p.status, c0 + 8 <= p.C && dst + q * stepy + 8 <= end))
           *reinterpret_cast<uint4 *>(dst + q * stepy) = make_uint4(y[0], y[1], y[2], y[3]);
       });
       src += kAhead * stepx;
@@ -510,6 +511,7 @@ struct Octet {
 
 template <bool GF32>
 __device__ __forceinline__ void store_param_grads(const GroupNormArgs &p, int c, float s, float sx) {
+  if (!store_ok(p.status, c >= 0 && c < p.C)) return;
   if constexpr (GF32) {
     if (p.dgamma) static_cast<float *>(p.dgamma)[c] = sx;
     if (p.dbeta) static_cast<float *>(p.dbeta)[c] = s;
@@ -575,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_sums_kernel(const GroupNor
   float2 *chan = sh + sp.lanes * p.C;
   channel_sums<kThreads>(sh, chan, sp.lanes, p.C);
   for (int c = threadIdx.x; c < p.C; c += kThreads)
-    if (store_ok(p.status, slot < static_cast<int64_t>(p.B) * p.chunks))
+    if (store_ok(p.status, slot * p.C + c < static_cast<int64_t>(p.B) * p.chunks * p.C))
       p.chan_part[slot * p.C + c] = chan[c];
   const int n = threads_per_group(cg), part = threadIdx.x % n;
   for (int g0 = 0; g0 < p.G; g0 += kThreads / n) {
@@ -588,7 +590,8 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_sums_kernel(const GroupNor
         s.y = fmaf(gm, chan[c].y, s.y);
       }
     s = sum_over(s, n);
-    if (g < p.G && part == 0 && store_ok(p.status, slot < static_cast<int64_t>(p.B) * p.chunks))
+    if (g < p.G && part == 0 &&
+        store_ok(p.status, slot * p.G + g < static_cast<int64_t>(p.B) * p.chunks * p.G))
       p.part[slot * p.G + g] = s;
   }
 }
@@ -614,13 +617,12 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_dx_kernel(const GroupNormA
     }
     sums[warp * 32 + ln] = make_double2(s, sx);
     __syncthreads();
-    if (warp != 0 || c >= p.C) return;
+    if (warp != 0) return;
     for (int w = 1; w < kWarps; ++w) {
       s += sums[w * 32 + ln].x;
       sx += sums[w * 32 + ln].y;
     }
-    if (!store_ok(p.status, c < p.C)) return;
-    store_param_grads<GF32>(p, c, static_cast<float>(s), static_cast<float>(sx));
+    if (c < p.C) store_param_grads<GF32>(p, c, static_cast<float>(s), static_cast<float>(sx));
     return;
   }
   const int blk = blockIdx.x - p.grad_blocks;
@@ -682,6 +684,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_dx_kernel(const GroupNormA
     }
     const uint16_t *xs = x0 + o * 8, *ds = d0 + o * 8;
     uint16_t *dst = p.dx + (row0 + lane) * p.lddx + c0;
+    const uint16_t *end = p.dx + (static_cast<int64_t>(p.B) * p.S - 1) * p.lddx + p.C;
     for (int left = mine; left > 0; left -= kAhead) {
       if (!loaded) load(xs, ds, left);
       loaded = false;
@@ -697,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_dx_kernel(const GroupNormA
               f2_get(f2_mul(ch.rstd[j], f2_fma(xh, m2[j], f2_fma(dv, ch.gamma[j], m1[j]))));
           y[j] = bf16x2(z.x, z.y);
         }
-        if (store_ok(p.status, row0 + rows <= static_cast<int64_t>(p.B) * p.S && c0 + 8 <= p.lddx))
+        if (store_ok(p.status, c0 + 8 <= p.C && dst + q * stepo + 8 <= end))
           *reinterpret_cast<uint4 *>(dst + q * stepo) = make_uint4(y[0], y[1], y[2], y[3]);
       });
       xs += kAhead * stepx;

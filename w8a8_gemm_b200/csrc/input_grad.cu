@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kDeqThreads) dequant_kernel(
 #pragma unroll
       for (int j = 0; j < 8; ++j) q[j] = inverts ? q[j] * inv[j] : __fdiv_rn(q[j], dv[j]);
     }
-    if (store_ok(status, k + 8 <= K))
+    if (store_ok(status, n * K + k + 8 <= N * K))
       *reinterpret_cast<uint4 *>(w + n * K + k) = make_uint4(
           bf16x2(q[0], q[1]), bf16x2(q[2], q[3]), bf16x2(q[4], q[5]), bf16x2(q[6], q[7]));
   }
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {  // K % 16 == 0: 8 columns are all in or all out
           const int c8 = col + q * 8;
-          if (row < p.M && c8 < p.K && store_ok(p.status, c8 + 8 <= p.lddx)) {
+          if (row < p.M && c8 < p.K && store_ok(p.status, c8 + 8 <= p.K)) {
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
       }
       const int row = (first / p.num_n_tiles * 2 + rank) * BM + m, c8 = nt * BN + c;
-      if (row < p.M && c8 < p.K && store_ok(p.status, c8 + 8 <= p.lddx))
+      if (row < p.M && c8 < p.K && store_ok(p.status, c8 + 8 <= p.K))
         *reinterpret_cast<uint4 *>(p.dx + static_cast<int64_t>(row) * p.lddx + c8) =
             make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
                        bf16x2(v[6], v[7]));

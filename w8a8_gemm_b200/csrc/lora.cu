@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kContractThreads)
                        : *reinterpret_cast<const float4 *>(part + r * PS + j);
         if constexpr (TRANS) {
           t = *reinterpret_cast<const float4 *>(p.t + at);
-        } else if (store_ok(p.status, row >= 0 && row < p.M)) {
+        } else if (store_ok(p.status, row >= 0 && row < p.M && j + 4 <= p.R)) {
           *reinterpret_cast<float4 *>(p.t + at) = s;
         }
         s = make_float4(f * s.x, f * s.y, f * s.z, f * s.w);
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const FewArgs p) 
     if (p.base == p.y) return;
     for (int m = warp; m < count; m += kFewWarps)
       for (int c = c_lo + lane * 2; c < c_hi; c += 64)
-        if (store_ok(p.status, c + 2 <= p.ldy))
+        if (store_ok(p.status, row[m] >= 0 && row[m] < p.M && c + 2 <= p.N))
           store_pair<F32>(p.y, row[m] * p.ldy + c,
                           p.base ? load_pair<F32>(p.base, row[m] * p.ld_base + c)
                                  : make_float2(0.0f, 0.0f));
@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const FewArgs p) 
       if (m0 + m >= count) break;
       float4 s = cluster_sum(cluster, part, 0, kFewCluster - 1, [&](int) { return e * 4; });
       const int64_t r = row[m0 + m];
-      if (e % kFewCluster == rank && store_ok(p.status, r >= 0 && r < p.M))
+      if (e % kFewCluster == rank && store_ok(p.status, r >= 0 && r < p.M && j + 4 <= R))
         *reinterpret_cast<float4 *>(p.t + r * R + j) = s;
       uint2 d[TERMS];
       split_terms<TERMS>(make_float4(f * s.x, f * s.y, f * s.z, f * s.w), d);
@@ -738,10 +738,10 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const FewArgs p) 
                         *reinterpret_cast<const uint4 *>(at + 8 * S::kTermRow), w[q]);
           }
       const int64_t to = c + t8 / 4;
-      const bool ok = store_ok(p.status, to + 2 <= p.ldy);
-      if (ok && m0 + g < count)
+      auto fits = [&](int64_t r) { return r >= 0 && r < p.M && to + 2 <= p.N; };
+      if (m0 + g < count && store_ok(p.status, fits(r0)))
         store_pair<F32>(p.y, r0 * p.ldy + to, make_float2(b0.x + d[0], b0.y + d[1]));
-      if (ok && m0 + g + 8 < count)
+      if (m0 + g + 8 < count && store_ok(p.status, fits(r1)))
         store_pair<F32>(p.y, r1 * p.ldy + to, make_float2(b1.x + d[2], b1.y + d[3]));
       c += kFewWarps * 8;
       load();
@@ -1128,7 +1128,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             const int64_t to = __shfl_sync(~0u, row, rr);
             const int col = c0 + q * (16 / E);
             if (rr < mine && col < p.C &&
-                store_ok(p.status, to >= 0 && to < p.M && col + 16 / E <= p.ld_out))
+                store_ok(p.status, to >= 0 && to < p.M && col + 16 / E <= p.C))
               *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) +
                                          (to * p.ld_out + col) * E) =
                   *reinterpret_cast<const uint4 *>(data + swz128(quarter * 32 + rr, q));
@@ -1341,6 +1341,7 @@ __global__ void __launch_bounds__(kOuterThreads, OuterSmem<RT, TERMS>::kPerSm)
   if (!p.beside) grid_dependency_wait();
 
   const int cols = sd.C - c0 < kOuterSlab ? sd.C - c0 : kOuterSlab;
+  const int64_t grads = static_cast<int64_t>(p.L) * p.R * sd.C;  // elements of sd.out
   float keep[RT];  // storing warps: the sums of a first adapter that is shared
   bool kept = false, last_shared = false, ok_all = true;
   uint32_t last_buf = 0;
@@ -1540,7 +1541,11 @@ __global__ void __launch_bounds__(kOuterThreads, OuterSmem<RT, TERMS>::kPerSm)
           __syncwarp();
           tmem_ld_32x32b_x32(acc + j0, r);
           tmem_ld_wait();
-          if (c < cols && store_ok(p.status, c0 + c < sd.C)) {
+          const int js = p.R - j0 < 32 ? p.R - j0 : 32;  // of this thread's stores
+          const int64_t end = sd.transposed
+                                  ? obase + static_cast<int64_t>(j0 + js - 1) * sd.C + c0 + c + 1
+                                  : obase + static_cast<int64_t>(c0 + c) * p.R + j0 + js;
+          if (c < cols && js > 0 && store_ok(p.status, end <= grads)) {
             if (sd.transposed) {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
@@ -1639,7 +1644,10 @@ __global__ void __launch_bounds__(kOuterThreads, OuterSmem<RT, TERMS>::kPerSm)
           const float4 s = cluster_sum(cluster, part, r_lo, r_hi, [&](int r) {
             return (first_tile(r) < lo ? kOuterSlab * PS : 0) + c * PS + j;
           });
-          if (!store_ok(p.status, j + 4 <= p.R && c0 + c < sd.C)) continue;
+          const int64_t end = sd.transposed
+                                  ? obase + static_cast<int64_t>(j + 3) * sd.C + c0 + c + 1
+                                  : obase + static_cast<int64_t>(c0 + c) * p.R + j + 4;
+          if (!store_ok(p.status, end <= grads)) continue;
           const float v[4] = {f * s.x, f * s.y, f * s.z, f * s.w};
           if (sd.transposed) {
 #pragma unroll
@@ -1667,7 +1675,7 @@ __global__ void __launch_bounds__(kOuterThreads, OuterSmem<RT, TERMS>::kPerSm)
         const int64_t at = sd.transposed
                                ? obase + static_cast<int64_t>(e / cols) * sd.C + c0 + e % cols
                                : obase + static_cast<int64_t>(c0) * p.R + e;
-        if (store_ok(p.status, at < (static_cast<int64_t>(bin) + 1) * p.R * sd.C))
+        if (store_ok(p.status, at < grads))
           store_grad<F32>(sd.out, at, 0.0f);
       }
     }

@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         if (r + q * lanes >= rows) break;
         const int64_t row = row0 + r + q * lanes;
         T *dst = out + row * p.ldo + at;
-        const bool ok = store_ok(p.status, row < p.M && at + N <= p.ldo);
+        const int64_t end = at + (HALF && unit < turned ? pairs : 0) + N;  // columns
+        const bool ok = store_ok(p.status, row < p.M && end <= static_cast<int64_t>(p.H) * p.D);
         if (unit >= turned) {
           if (ok) *reinterpret_cast<uint4 *>(dst) = a[q];
           continue;
@@ -201,7 +202,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       const int h = v / per_head, i = v - h * per_head;
       const T *src = x + (row0 + r) * p.ldx + static_cast<int64_t>(h) * p.D;
       T *dst = out + (row0 + r) * p.ldo + static_cast<int64_t>(h) * p.D;
-      if (!store_ok(p.status, row0 + r < p.M && (h + 1) * p.D <= p.ldo)) continue;
+      const int last = i >= pairs ? p.rot + i - pairs : HALF ? i + pairs : 2 * i + 1;
+      if (!store_ok(p.status, row0 + r < p.M && last < p.D && h < p.H)) continue;
       if (i >= pairs) {
         dst[p.rot + i - pairs] = src[p.rot + i - pairs];
         continue;
