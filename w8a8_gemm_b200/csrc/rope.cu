@@ -230,7 +230,8 @@ cudaError_t run(RopeArgs p, bool half, cudaStream_t stream) {
   if (rows < ahead) rows = ahead;
   const int64_t most = 32768 / (static_cast<int64_t>(p.rot / 2) * 8);
   if (rows > most) rows = most;
-  if (rows > p.M / (4 * 148)) rows = p.M / (4 * 148);
+  const int64_t blocks4 = 4 * static_cast<int64_t>(sm_count());
+  if (rows > p.M / blocks4) rows = p.M / blocks4;
   if (rows < 1) rows = 1;
   p.rows_per_block = static_cast<int>(rows);
   const int64_t blocks = (p.M + rows - 1) / rows;
