@@ -582,8 +582,8 @@ SQ_API sq_status sq_lora_forward(const void *x, int64_t ldx, const void *A, cons
  *   dx[m] = dx_base[m] + A[a]^T dt[m]
  * dA and dB are written whole (zeros for an adapter without rows); rows without
  * an adapter get dx[m] = dx_base[m].  (dL/dbase is dy itself.)  t and dt enter
- * the second products rounded to bf16 where the result is bf16, with 24 bits
- * where it is fp32.  Every sum has a fixed order: the same call gives the same
+ * the second products rounded to bf16 where grad_dtype is bf16; where it is fp32,
+ * with 24 bits for dA and dB and 16 for dx.  Every sum has a fixed order: the same call gives the same
  * bits.  Infinities and NaN follow the formulas, as in the forward call.
  *   dy       bf16 [M][lddy];  x, A, B, scale, plan as in the forward call
  *   t        fp32 [M][R] of the forward call

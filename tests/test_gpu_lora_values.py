@@ -108,3 +108,27 @@ def test_a_prompt_in_place(M, K, N, R, L, spread, out):
     assert all(torch.equal(u, w) for u, w in zip(apart, (dA, dB, view)))
     assert (wide[:, K:] == 5.0).all()
     assert B.sq_get_device_status() == B.SQ_OK
+
+
+@pytest.mark.parametrize("M,K,N,R,L,spread", [(1825, 72, 144, 8, 4, "one"), (646, 48, 104, 8, 37, "runs"),
+                                              (596, 424, 72, 16, 26, "scattered"),
+                                              (300, 1000, 264, 72, 2, "mixed"),
+                                              (5000, 256, 128, 128, 3, "mixed")])
+def test_dx_beside_fp32_gradients_keeps_16_bits_of_dt(M, K, N, R, L, spread):
+    """The bound is that of the formula with dt in fp32, its first two cut-off bf16
+    terms (2^-14 at most, 8 bits each) and the sums over N and 2 R products."""
+    p = _problem(M, K, N, R, L, seed=R, spread=spread)
+    plan = B.sq_lora_plan(p["ids"], L)
+    t = torch.randn(M, R, device="cuda", generator=torch.Generator("cuda").manual_seed(M))
+    _, _, dx = B.sq_lora_backward(p["dy"], p["x"], t, p["A"], p["B"], p["scale"], plan, None,
+                                  grad_dtype=F32)
+    want, bound = torch.zeros(M, K, dtype=F64, device="cuda"), torch.zeros(M, K, dtype=F64,
+                                                                           device="cuda")
+    for a in range(L):
+        r = (p["ids"] == a).nonzero()[:, 0]
+        g, A, Bm, c = p["dy"][r].double(), p["A"][a].double(), p["B"][a].double(), float(p["scale"][a])
+        dt = c * (g @ Bm)
+        e = abs(c) * ref.ACC(N + 8) * (g.abs() @ Bm.abs()) + 2.0 ** -23 * dt.abs()
+        want[r] = dt @ A
+        bound[r] = (e + (2.0 ** -14 + ref.ACC(2 * R)) * (dt.abs() + e)) @ A.abs()
+    ref.check(dx, want, bound, "dx")

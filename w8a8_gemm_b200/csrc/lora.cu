@@ -784,9 +784,9 @@ struct ExpandMaps {
 constexpr int kExpandWarps = 8;                            // adding and storing
 constexpr int kExpandThreads = 64 + 32 * (kExpandWarps + kCopyWarps);  // and producer, MMA
 
-template <int RT, bool F32>
+template <int RT, bool F32, int TERMS>
 struct ExpandSmem {
-  static constexpr int kTerms = F32 ? 3 : 1;
+  static constexpr int kTerms = TERMS;
   static constexpr int kSlab = F32 ? 64 : 128;  // columns of a unit
   static constexpr int kBase = kTileRows * 256;
   static constexpr int kW = kSlab * RT * 2;
@@ -830,10 +830,10 @@ struct Units {
   }
 };
 
-template <int RT, bool TRANS, bool F32>
+template <int RT, bool TRANS, bool F32, int TERMS>
 __global__ void __launch_bounds__(kExpandThreads, 1)
     lora_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs p) {
-  using S = ExpandSmem<RT, F32>;
+  using S = ExpandSmem<RT, F32, TERMS>;
   constexpr int STAGES = S::kStages, SLAB = S::kSlab, E = F32 ? 4 : 2;
   constexpr int BOX = 128 / E;  // columns of a 128-byte box
   extern __shared__ uint8_t smem_raw[];
@@ -1784,10 +1784,10 @@ cudaError_t run_contract(const uint16_t *w, const ContractArgs &a, cudaStream_t 
       ContractSmem<RT>::kBytes, slices, 1, stream, tm_in, tm_in32, tm_w, a);
 }
 
-template <int RT, bool TRANS, bool F32>
+template <int RT, bool TRANS, bool F32, int TERMS>
 cudaError_t run_expand(const uint16_t *w, const uint16_t *v, const ExpandArgs &a,
                        cudaStream_t stream) {
-  using S = ExpandSmem<RT, F32>;
+  using S = ExpandSmem<RT, F32, TERMS>;
   ExpandMaps maps;
   const void *base = a.base ? a.base : a.out;  // not read without a base
   cudaError_t e = tile_map(&maps.base, F32, base, a.C, a.M, 0, a.base ? a.ld_base : a.ld_out,
@@ -1803,7 +1803,7 @@ cudaError_t run_expand(const uint16_t *w, const uint16_t *v, const ExpandArgs &a
   if (e != cudaSuccess) return e;
   const int64_t units = a.max_tiles * ((a.C + S::kSlab - 1) / S::kSlab);
   const int sms = sm_count();
-  return launch<lora_expand_kernel<RT, TRANS, F32>>(
+  return launch<lora_expand_kernel<RT, TRANS, F32, TERMS>>(
       dim3(static_cast<unsigned>(units < sms ? units : sms)), kExpandThreads, S::kBytes, 1, 0,
       stream, maps, a);
 }
@@ -1859,8 +1859,10 @@ cudaError_t run_backward(const LoraRequest &q, cudaStream_t stream) {
   if (e == cudaSuccess && q.dx != nullptr) {
     const ExpandArgs x = {q.plan, q.base, q.ld_base, q.dx, q.lddx, q.M,
                           max_tiles, K, q.R, q.L, q.status};
+    // dt's only term, or the first two of three (16 bits: they are cut off, not
+    // rounded)
     e = by_rank(q.R, [&](auto rt) {
-      return run_expand<decltype(rt)::value, true, false>(q.A, vdt, x, stream);
+      return run_expand<decltype(rt)::value, true, false, TERMS == 1 ? 1 : 2>(q.A, vdt, x, stream);
     });
   }
   if (e == cudaSuccess && q.dA != nullptr) {
@@ -1913,7 +1915,7 @@ cudaError_t run_forward(const LoraRequest &q, cudaStream_t stream) {
   return by_rank(q.R, [&](auto rt) {
     constexpr int RT = decltype(rt)::value;
     const cudaError_t e = run_contract<RT, false, F32 ? 3 : 1>(q.A, c, stream);
-    return e != cudaSuccess ? e : run_expand<RT, false, F32>(q.B, v, x, stream);
+    return e != cudaSuccess ? e : run_expand<RT, false, F32, F32 ? 3 : 1>(q.B, v, x, stream);
   });
 }
 
