@@ -619,8 +619,8 @@ typedef enum {
  *   (u, v) -> factor * (u cos phi - v sin phi, u sin phi + v cos phi)
  * The backward call maps dL/dout to dL/dx.  Columns rot .. D - 1 of a head are
  * copied (left alone in place).  One call covers the q and the k columns of a
- * QKV row, which are neighbours.  The angle is formed and reduced in fp64, so
- * far positions keep their phase.
+ * QKV row, which are neighbours.  The angle is formed and reduced in fp64, so far
+ * positions keep their phase: of p radians it is off by 2^-51 p at most.
  *   x, out      bf16 or fp32 (dtype) rows [M][ldx], [M][ldo]; out may be x with
  *               ldo == ldx (in place), otherwise they must not overlap
  *   positions   int32 [M][n_axes] device, any values
