@@ -7,14 +7,16 @@
 //   dbeta = sum dv, dgamma = sum dv xh over samples and rows,
 //   dx = rstd (h - (sum_group h + xh sum_group h xh) / n).
 //
-// Both directions are bound by memory traffic and the special-function unit
-// (two operations an element for SiLU and GELU) and take two kernels: one reads
-// the rows and leaves partial results of its chunk of rows, the other joins the
-// partials (a few KB) and reads the rows again, from L2 where they fit.  (One
+// Both directions take two kernels: one reads the rows and leaves partial results
+// of its chunk of rows, the other joins the partials (a few KB) and reads the rows
+// again, from L2 where they fit.  What bounds them is latency: two kernels one
+// behind the other, at 16 to 24 warps an SM, which keep the issue slots and (two
+// operations an element for SiLU and GELU) the special-function unit busy 35 to 45%
+// of the time.  2 x 16384 x 320 with SiLU: 17.6 us in a replayed graph on one input,
+// 20.2 a call with new ones; backward, 4 x 4096 x 640 with SiLU: 26.2 and 30.0.  (One
 // kernel with the rows kept in a cluster's shared memory was measured: clusters
-// of eight with 200 KB a block find room for 120 of 148 SMs, and 2 x 16384 x 320
-// took 34 us in two rounds, 17.3 in two kernels.)  Backward, 4 x 4096 x 640 with
-// SiLU: 26.2 us.
+// of eight with 200 KB a block find room for 120 of 148 SMs, and the forward pass
+// took 34 us in two rounds.)
 //
 // The statistics are (count, mean, sum of squares about the mean).  A thread sums
 // x - c and (x - c)^2 over up to 32 rows, c the first of them, in fp32: the sum of
@@ -764,7 +766,7 @@ void fill_chunks(GroupNormArgs &p, int blocks2) {
   // A block of the second kernel has a slice of the channels, whole octets and
   // whole groups, eight groups or 128 bytes a row at least: every block joins its
   // groups' partials of the whole sample before it starts (all 32 groups of
-  // 2 x 16384 x 320 in every block: 23.1 us, eight: 19.0 us).
+  // 2 x 16384 x 320 in every block: 23.1 us, eight: 19.0 us then).
   const int cg = p.C / p.G;
   const int unit = cg % 8 == 0 ? cg : cg % 4 == 0 ? cg * 2 : cg % 2 == 0 ? cg * 4 : cg * 8;
   const int least_width = 8 * cg > 64 ? 8 * cg : 64;

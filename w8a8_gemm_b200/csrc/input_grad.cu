@@ -18,8 +18,10 @@
 // contraction and add their sums in a fixed order.  What bounds it is the way of
 // the operands from L2 to an SM, 40 to 60 bytes a clock: one block by itself with
 // 128 x 256 tiles fetches 48 KB for 512 clocks of products, a pair 32 KB a block.
-// 8858 x 6144 -> 1536: 114 us for the product (1466 TFLOP/s), 121 in all; with one
-// block a tile 122 and 129.  1109 x 1536 -> 1536: 18.9 us.
+// 8858 x 6144 -> 1536: 121 to 126 us in a replayed graph on one input (129 with one
+// block a tile), 142 to 146 a call with new ones, under the power cap; the product
+// by itself 120 us at 1.58 GHz (profiler: 1389 TFLOP/s, tensor pipe 73%).  1109 x 1536
+// -> 1536: 18.9 us, 19.3 a call.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>

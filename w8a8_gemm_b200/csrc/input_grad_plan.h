@@ -24,8 +24,8 @@ inline InputGradPlan input_grad_plan(int64_t M, int64_t N, int64_t K, int sms) {
   // enough to pay for the sums' way through distributed shared memory (about 3
   // us) and all the clusters run at once: 148 SMs have room for 15 of eight blocks,
   // 33 of four, a cluster lying within one of the GPU's partitions, other numbers of
-  // SMs in proportion.  200 rows: 3840 -> 1920 18.0 us by four pairs, 22.1 by two, 27.7
-  // by one; 1536 -> 1536 13.5, 14.6, 15.4; 384 -> 768 10.5, 10.5, 9.1.
+  // SMs in proportion.  200 rows, replayed graphs: 3840 -> 1920 18.0 us by four pairs,
+  // 22.1 by two, 27.7 by one; 1536 -> 1536 13.5, 14.6, 15.4; 384 -> 768 10.5, 10.5, 9.1.
   // The sums of a tile take the place of the stages, so a cluster that shares one
   // has no other: as many clusters as tiles, whatever runs at once.
   const int64_t narrow = tiles(128), steps = (N + kGradStep - 1) / kGradStep;

@@ -18,7 +18,10 @@
 // and written, four bytes, meets 128 flop).  Sums are fp32; the small operand t
 // (dt) enters the second product as bf16 where the result is rounded to bf16
 // anyway, or split into three bf16 terms (24 significant bits) where the result
-// stays fp32.
+// stays fp32; dx beside fp32 gradients takes two of dt's.
+//
+// Times here are of replayed graphs of ten calls on one input, which leave out the
+// host and find in L2 what fits; a call with new inputs takes up to a tenth more.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -61,7 +64,8 @@ __device__ __forceinline__ bool plan_fits(const int32_t *plan, int64_t M, int32_
 // One block: a stable counting sort of the rows by adapter.  Warp w owns the
 // rows [w chunk, (w + 1) chunk) and a histogram of its own, so that the order
 // within an adapter, and with it every sum over its rows, is always the same.
-// (Once per batch: 10 us for 8858 rows, 150 for 100,000.)
+// (Once per batch: 4 us up to 333 rows, 5.3 for 1501, 9 for 8858 of two adapters, 16
+// of 64, 59 for 100,000; through ctypes a call takes 7 at least.)
 constexpr int kPlanWarps = 32;
 __global__ void __launch_bounds__(kPlanWarps * 32) lora_plan_kernel(
     const int32_t *__restrict__ adapter, int32_t M, int32_t L, int32_t *plan, int *status) {
@@ -293,11 +297,11 @@ __device__ __forceinline__ void split_terms(float4 v, uint2 (&out)[TERMS]) {
 // tcgen05.mma (M = 128, N = RT, sums in tensor memory), so that reading the rows
 // costs the SM next to no instructions.  The blocks of a cluster hold the slices
 // of one tile and add their partial sums through distributed shared memory in a
-// fixed order.  The
-// operand of the second products is stored as bf16 terms by tile, 128 rows each
-// with zeros past the tile's last: scale t (forward, beside t by row in fp32),
-// or dt and t (backward).  Bound by the rows' way from HBM: 8858 x 6144, rank 64,
-// 27 us by itself, of which 24 are at 4.7 TB/s and the rest start and end.
+// fixed order.  The operand of the second products is stored as bf16 terms by
+// tile, 128 rows each with zeros past the tile's last: scale t (forward, beside t by
+// row in fp32), or dt and t (backward).  Bound by the rows' way from HBM: 8858 x
+// 6144, rank 64, 113 MB in 30 us from a cold L2 (profiler; tensor pipe 11%, issue
+// 13%).
 struct ContractArgs {
   const uint16_t *in;  // as tm_in
   int64_t ld;
@@ -764,9 +768,10 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const FewArgs p) 
 // Where a tile's rows are not neighbours, four warps take 32 rows of base each, as
 // boxes or by copies, and begin before the contraction has ended (1501 ragged
 // rows, 1536 -> 2304 in fp32: 18.9 us with the contraction; 21.0 when they wait
-// for it, 25.7 with two warps).  Rows without an adapter are
-// copied from base (left alone when out is base).  8858 x 6144, rank 64, bf16: 38
-// us, 5.7 TB/s.
+// for it, 25.7 with two warps), on SMs that no block of the contraction holds any
+// more: the two together need more shared memory than an SM has.  Rows without
+// an adapter are copied from base (left alone when out is base).  8858 x 6144, rank 64, bf16: 218
+// MB in 40.5 us from a cold L2 (profiler), 5.4 TB/s.
 struct ExpandArgs {
   const int32_t *plan;
   const void *base;    // nullptr: 0
@@ -1227,7 +1232,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 // shares at most its first and its last adapter with its neighbours: those
 // partial sums meet in distributed shared memory, added in block order.
 // Bound by the rows' way from HBM: 8858 rows of two adapters, 6144 + 1536 columns,
-// rank 64, 42 us by itself, 34 of them at 4 TB/s (256 bytes a row and stage).
+// rank 64, 138 MB in 46 us from a cold L2 (profiler; 256 bytes a row and stage).
 struct OuterSide {
   const uint16_t *src;  // as the side's map
   int64_t ld;
@@ -1337,7 +1342,9 @@ __global__ void __launch_bounds__(kOuterThreads, OuterSmem<RT, TERMS>::kPerSm)
   auto bin_of = [&](int tile) { return recs[static_cast<int64_t>(tile) * kRecWords]; };
   // Behind the expansion: that one lets this kernel begin when the contraction
   // is complete, and nothing here touches what it writes, so the two run side by
-  // side; the wait at the end keeps the stream's order for what comes next.
+  // side, on the SMs that the expansion leaves free or has left (a block of each
+  // needs more shared memory than an SM has); the wait at the end keeps the stream's
+  // order for what comes next.
   if (!p.beside) grid_dependency_wait();
 
   const int cols = sd.C - c0 < kOuterSlab ? sd.C - c0 : kOuterSlab;

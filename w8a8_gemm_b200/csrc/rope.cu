@@ -12,8 +12,9 @@
 // angle is formed and reduced to a fraction of a turn in fp64 (a position of a
 // million times a frequency near one has an fp32 product that is off by 0.03
 // rad); sine and cosine of the reduced angle are fp32.  9216 rows of 48 heads of
-// 128, bf16: 38.2 us, 0.91 of the copy rate (51.7 when a thread found its place in
-// the row anew for every unit); 24 rows of 32 heads: 2.5 us.
+// 128, bf16: 38.2 us in a replayed graph on one input, 0.91 of the copy rate (51.7
+// when a thread found its place in the row anew for every unit), 40.4 a call; 24
+// rows of 32 heads: 2.5 us, 5.5 a call.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
