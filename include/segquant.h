@@ -694,6 +694,7 @@ typedef enum {
  *   C a multiple of 8, 8..8192; G 1..1024, dividing C; S 1..2^24; B 0..65535;
  *   ld >= C, multiples of 8; x, y 16-byte aligned, gamma and beta 2-byte, mean
  *   and rstd 4-byte; B * S * ld <= 2^44; eps >= 0, finite.
+ * Squares are summed in fp32: distances within a group of at most 2^48.
  * The mean is taken off before anything is multiplied: a group of equal values
  * gives act(beta) exactly.  A group with an infinity or a NaN has no finite mean,
  * NaN for rstd and for its outputs; the other groups do not notice.

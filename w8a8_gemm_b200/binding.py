@@ -622,6 +622,12 @@ def _matrix(name: str, t, dtype, shape, dev: int):
     _explain(name, t, dtype, shape, dev, False)
 
 
+def _is_tensor(name: str, t, dev: int):
+    """Raises unless t is a tensor (of which type and shape is checked later)."""
+    if not isinstance(t, torch.Tensor):
+        _explain(name, t, None, (), dev, False)
+
+
 def _rows_of(name: str, t, dtype):
     """(rows, columns, device) of the tensor that gives a call its sizes."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -657,7 +663,8 @@ def _workspace(t, nbytes: int, dev: int):
     work of the same stream only."""
     if t is None:
         t = torch.empty(nbytes, dtype=_U8, device=dev)
-    elif t.dtype is not _U8 or not t.is_contiguous() or t.get_device() != dev:
+    elif (not isinstance(t, torch.Tensor) or t.dtype is not _U8 or not t.is_contiguous()
+          or t.get_device() != dev):
         raise ValueError("workspace must be a contiguous uint8 tensor on the call's device")
     return t, t.data_ptr(), t.numel()
 
@@ -723,6 +730,9 @@ def sq_lora_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: to
     L, R, Ka, N = _lora_sizes(A, B)
     if Ka != K:
         raise ValueError(f"A has K = {Ka}, x has {K}")
+    for name, given in (("base", base), ("y", y)):
+        if given is not None:
+            _is_tensor(name, given, dev)
     if y is None:
         y = torch.empty(M, N, dtype=_BF16 if base is None else base.dtype, device=dev)
     if t is None:
@@ -831,6 +841,7 @@ def _rope(call: str, x, positions, inv_freq, head_dim, out, layout, axis_pairs, 
         raise ValueError(f"{cols} columns are no whole number of heads of {head_dim}")
     axes = 1 if axis_pairs is None else len(axis_pairs)
     flat = axes == 1 and isinstance(positions, torch.Tensor) and positions.dim() == 1
+    _is_tensor("inv_freq", inv_freq, dev)
     pairs = inv_freq.numel()
     if out is None:
         out = torch.empty(M, cols, dtype=kind, device=dev)
@@ -916,7 +927,7 @@ def sq_group_norm_forward(x: torch.Tensor, groups: int, gamma: Optional[torch.Te
     B, S, C, dev = _gn_sizes(x)
     if y is None:
         y = torch.empty(B, S, C, dtype=_BF16, device=dev)
-    mean, rstd = torch.empty(2, B, max(groups, 0), dtype=_F32, device=dev).unbind(0)
+    mean, rstd = torch.empty(2, B, min(max(groups, 0), C), dtype=_F32, device=dev).unbind(0)
     ws, wp, wn = _workspace(workspace, sq_group_norm_workspace_bytes(B, S, C, groups)
                             if workspace is None else 0, dev)
     px, ldx = _samples("x", x, (B, S, C), dev)
